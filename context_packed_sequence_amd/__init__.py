@@ -4,9 +4,11 @@ Low level: the C entry points of libthdcp under their own names
 (``thd_build_route``, ``thd_swap``, ``thd_roll_labels``, ...), see
 ``binding.py`` and ``include/thd_cp.h``.
 
-High level: ``Route`` (one per micro-batch: build once, swap many times) and
-``roll_labels``.  Both only allocate output tensors with torch and hand
-pointers to the library; the work runs in the library's HIP kernels.
+High level: ``Route`` (one per micro-batch: build once, swap many times),
+``roll_labels`` and the losses on packed streams (``losses.py``:
+``token_logprobs``, ``policy_loss``, ``preference_loss``, ``distill_topk``).
+They only allocate output tensors with torch and hand pointers to the library;
+the work runs in the library's HIP kernels.
 """
 
 from __future__ import annotations
@@ -27,13 +29,21 @@ from .binding import (  # noqa: F401
     THD_ERR_DIRECTION,
     THD_ERR_HIP,
     THD_ERR_INTEGRITY,
+    THD_ERR_LABEL,
     THD_ERR_NOT_BUILT,
     THD_ERR_PACK_CAPACITY,
     THD_ERR_PACK_DOCS,
+    THD_ERR_PAIR,
     THD_ERR_REAL_GT_PADDED,
     THD_ERR_SHAPE,
+    THD_BF16,
+    THD_FP16,
+    THD_FP32,
     THD_IDENTITY,
     THD_MAX_BATCH,
+    THD_MAX_PAIRS,
+    THD_MAX_TOPK,
+    THD_MAX_VOCAB,
     THD_PACK_MAX_SEQ,
     THD_MAX_CP,
     THD_MAX_SHIFT,
@@ -42,6 +52,11 @@ from .binding import (  # noqa: F401
     ThdError,
     thd_build_route,
     thd_copy,
+    thd_distill_topk,
+    thd_loss_workspace_bytes,
+    thd_policy_loss,
+    thd_preference_loss,
+    thd_preference_workspace_bytes,
     thd_read_stream,
     thd_write_stream,
     thd_pack,
@@ -55,6 +70,8 @@ from .binding import (  # noqa: F401
     thd_route_info,
     thd_route_status,
     thd_strerror,
+    thd_token_logprobs,
+    thd_token_logprobs_backward,
     thd_swap,
     thd_route_launch_shape,
     thd_swap_batch,
@@ -228,3 +245,12 @@ def pack(tokens, pad_id: int, eod_id: int, align: int, capacity: int, max_docs: 
     thd_pack(tokens, batch, seq, pad_id, eod_id, align, capacity, max_docs, pad_value, workspace, nbytes, packed,
              cu_real, cu_pad, status, stream)
     return packed, cu_real, cu_pad, status
+
+
+from .losses import (  # noqa: E402,F401
+    distill_topk,
+    policy_loss,
+    preference_loss,
+    token_logprobs,
+    token_logprobs_backward,
+)

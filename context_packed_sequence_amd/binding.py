@@ -1,7 +1,7 @@
 """ctypes binding of libthdcp (include/thd_cp.h).
 
-Argument marshalling only: every step of the route build, the swap and the
-label roll runs in the library's HIP kernels.  Torch is used for device
+Argument marshalling only: every step of the route build, the swap, the label
+roll and the losses (include/thd_loss.h) runs in the library's HIP kernels.  Torch is used for device
 memory and streams: tensors are passed as their ``data_ptr()``, streams as
 ``torch.cuda.current_stream().cuda_stream`` unless one is given.
 
@@ -39,6 +39,8 @@ THD_ERR_REAL_GT_PADDED = -14
 THD_ERR_INTEGRITY = -15
 THD_ERR_PACK_DOCS = -16
 THD_ERR_PACK_CAPACITY = -17
+THD_ERR_LABEL = -18
+THD_ERR_PAIR = -19
 
 THD_ZIGZAG_TO_CONTIGUOUS = 0
 THD_CONTIGUOUS_TO_ZIGZAG = 1
@@ -48,11 +50,20 @@ THD_MAX_BATCH = 16
 THD_PACK_MAX_SEQ = 2147479552
 THD_PACK_STATIC_BYTES = 1048576
 
+THD_BF16 = 0
+THD_FP16 = 1
+THD_FP32 = 2
+THD_MAX_VOCAB = 1073741824
+THD_MAX_TOPK = 256
+THD_MAX_PAIRS = 65536
+
 EXPORTS = (
     "thd_route_create", "thd_route_destroy", "thd_build_route", "thd_swap", "thd_roll_labels",
     "thd_route_status", "thd_route_copy_out", "thd_route_info", "thd_strerror",
     "thd_swap_batch", "thd_roll_labels_zigzag", "thd_pack_workspace_bytes", "thd_pack", "thd_copy",
     "thd_route_launch_shape", "thd_read_stream", "thd_write_stream", "thd_pack_noalloc",
+    "thd_loss_workspace_bytes", "thd_token_logprobs", "thd_token_logprobs_backward", "thd_policy_loss",
+    "thd_distill_topk", "thd_preference_workspace_bytes", "thd_preference_loss",
 )
 
 
@@ -68,7 +79,9 @@ def _load() -> ctypes.CDLL:
             f"{LIB_PATH} is not built; run `python context_packed_sequence_amd/build_lib.py` "
             "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(LIB_PATH)
-    c_i32, c_i64, c_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+    c_i32, c_i64, c_p, c_f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
+    logits = [c_p, c_i32, c_i64, c_i64, c_i64]       # pointer, dtype, rows, vocab, row_stride
+    work = [c_p, c_i64, c_p]                         # workspace, workspace_bytes, stream
     sig = {
         "thd_route_create": (ctypes.c_int, [c_i32, c_i32, c_i64, ctypes.POINTER(c_p)]),
         "thd_route_destroy": (None, [c_p]),
@@ -93,6 +106,16 @@ def _load() -> ctypes.CDLL:
                                     c_p, c_p, c_p, c_p]),
         "thd_pack_noalloc": (ctypes.c_int, [c_p, c_i32, c_i32, c_i64, c_i64, c_i32, c_i64, c_i32, c_i64, c_p, c_p,
                                             c_p, c_p, c_p]),
+        "thd_loss_workspace_bytes": (ctypes.c_int64, [c_i64, c_i64, c_i32, c_i32]),
+        "thd_token_logprobs": (ctypes.c_int, [*logits, c_p, c_p, c_p, c_p, c_p, *work]),
+        "thd_token_logprobs_backward": (ctypes.c_int, [c_p, *logits, c_p, c_p, c_p, c_p, c_i64, c_p]),
+        "thd_policy_loss": (ctypes.c_int, [*logits, c_p, c_p, c_p, c_p, c_p, c_p, c_f64, c_f64, c_f64, c_p, c_p, c_p,
+                                           c_i64, c_p, *work]),
+        "thd_distill_topk": (ctypes.c_int, [*logits, c_p, c_i32, c_p, c_i32, c_i32, c_i64, c_p, c_p, c_f64, c_p, c_p,
+                                            c_i64, c_p, *work]),
+        "thd_preference_workspace_bytes": (ctypes.c_int64, [c_i64, c_i32]),
+        "thd_preference_loss": (ctypes.c_int, [c_p, c_p, c_p, c_p, c_i32, c_i64, c_p, c_i32, c_f64, c_f64, c_f64,
+                                               c_p, c_p, c_p, c_p, *work]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -256,6 +279,59 @@ def thd_route_launch_shape(route: int, tile_bytes: int = 0, nontemporal: int = 1
     choice); no shape arguments restore the defaults (include/thd_cp_bench.h)."""
     _check(_lib.thd_route_launch_shape(route, tile_bytes, nontemporal, block_threads, tile_order),
            "thd_route_launch_shape")
+
+
+# ---- the losses (include/thd_loss.h), same names ------------------------------
+# Logits and gradients are passed as addresses: their rows may be strided.
+
+def thd_loss_workspace_bytes(rows: int, vocab: int, dtype: int, targets: int) -> int:
+    return int(_lib.thd_loss_workspace_bytes(rows, vocab, dtype, targets))
+
+
+def thd_token_logprobs(logits: int, dtype: int, rows: int, vocab: int, row_stride: int, labels, mask, logp, lse,
+                       status, workspace, workspace_bytes: int, stream=None) -> int:
+    return _check(_lib.thd_token_logprobs(logits, dtype, rows, vocab, row_stride, _ptr(labels), _ptr(mask),
+                                          _ptr(logp), _ptr(lse), _ptr(status), _ptr(workspace), workspace_bytes,
+                                          _stream(stream)), "thd_token_logprobs")
+
+
+def thd_token_logprobs_backward(dlogp, logits: int, dtype: int, rows: int, vocab: int, row_stride: int, labels, lse,
+                                mask, dlogits: int, grad_stride: int, stream=None) -> int:
+    return _check(_lib.thd_token_logprobs_backward(_ptr(dlogp), logits, dtype, rows, vocab, row_stride, _ptr(labels),
+                                                   _ptr(lse), _ptr(mask), dlogits, grad_stride, _stream(stream)),
+                  "thd_token_logprobs_backward")
+
+
+def thd_policy_loss(logits: int, dtype: int, rows: int, vocab: int, row_stride: int, labels, mask, old_logp, ref_logp,
+                    advantages, weights, clip_low: float, clip_high: float, kl_coef: float, loss, logp, dlogits: int,
+                    grad_stride: int, status, workspace, workspace_bytes: int, stream=None) -> int:
+    return _check(_lib.thd_policy_loss(logits, dtype, rows, vocab, row_stride, _ptr(labels), _ptr(mask),
+                                       _ptr(old_logp), _ptr(ref_logp), _ptr(advantages), _ptr(weights), clip_low,
+                                       clip_high, kl_coef, _ptr(loss), _ptr(logp), dlogits, grad_stride, _ptr(status),
+                                       _ptr(workspace), workspace_bytes, _stream(stream)), "thd_policy_loss")
+
+
+def thd_distill_topk(logits: int, dtype: int, rows: int, vocab: int, row_stride: int, teacher_logits: int,
+                     teacher_dtype: int, teacher_ids: int, id_bytes: int, k: int, teacher_stride: int, mask, weights,
+                     temperature: float, loss, dlogits: int, grad_stride: int, status, workspace,
+                     workspace_bytes: int, stream=None) -> int:
+    return _check(_lib.thd_distill_topk(logits, dtype, rows, vocab, row_stride, teacher_logits, teacher_dtype,
+                                        teacher_ids, id_bytes, k, teacher_stride, _ptr(mask), _ptr(weights),
+                                        temperature, _ptr(loss), dlogits, grad_stride, _ptr(status), _ptr(workspace),
+                                        workspace_bytes, _stream(stream)), "thd_distill_topk")
+
+
+def thd_preference_workspace_bytes(total_tokens: int, n_slots: int) -> int:
+    return int(_lib.thd_preference_workspace_bytes(total_tokens, n_slots))
+
+
+def thd_preference_loss(logp, ref_logp, mask, cu_seqlens_padded, n_slots: int, total_tokens: int, pairs, n_pairs: int,
+                        beta: float, label_smoothing: float, scale: float, loss, rewards, dlogp, status, workspace,
+                        workspace_bytes: int, stream=None) -> int:
+    return _check(_lib.thd_preference_loss(_ptr(logp), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens_padded), n_slots,
+                                           total_tokens, _ptr(pairs), n_pairs, beta, label_smoothing, scale,
+                                           _ptr(loss), _ptr(rewards), _ptr(dlogp), _ptr(status), _ptr(workspace),
+                                           workspace_bytes, _stream(stream)), "thd_preference_loss")
 
 
 def library():

@@ -28,7 +28,8 @@ LIB_NAME = "libthdcp.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
 
-SOURCES = ["thd_route.hip", "thd_swap.hip", "thd_roll.hip", "thd_pack.hip", "thd_stream.hip", "thd_api.hip"]
+SOURCES = ["thd_route.hip", "thd_swap.hip", "thd_roll.hip", "thd_pack.hip", "thd_stream.hip", "thd_api.hip",
+           "thd_loss.hip", "thd_loss_policy.hip", "thd_loss_distill.hip", "thd_preference.hip", "thd_loss_api.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

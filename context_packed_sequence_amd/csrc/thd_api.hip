@@ -98,6 +98,8 @@ const char* thd_strerror(int32_t code) {
     case THD_ERR_INTEGRITY: return "route integrity check failed";
     case THD_ERR_PACK_DOCS: return "more documents than document slots";
     case THD_ERR_PACK_CAPACITY: return "padded documents exceed the token budget";
+    case THD_ERR_LABEL: return "a label or teacher column is outside the vocabulary";
+    case THD_ERR_PAIR: return "a preference pair names a slot that does not exist";
     default: return "unknown code";
   }
 }

@@ -66,6 +66,10 @@ extern "C" {
 #define THD_ERR_PACK_DOCS     -16   /* pack: more documents than max_docs              */
 #define THD_ERR_PACK_CAPACITY -17   /* pack: padded documents longer than capacity     */
 
+/* Written on the device by the losses of thd_loss.h: */
+#define THD_ERR_LABEL         -18   /* a label or teacher column is not a column       */
+#define THD_ERR_PAIR          -19   /* a preference pair names no slot                 */
+
 /* ---- directions ---------------------------------------------------------- */
 #define THD_ZIGZAG_TO_CONTIGUOUS 0
 #define THD_CONTIGUOUS_TO_ZIGZAG 1

@@ -29,10 +29,21 @@ Pins (each function is checked against something other than itself in
   the same page, plus hand-worked corner cases (all-pad rows, PAD inside a
   document, rows ending in EOD, a last document without EOD).
 
+* losses (``loss_oracle.py``): every gradient against central differences of its
+  loss, closed forms (uniform rows, a one-column vocabulary, a teacher equal to
+  the student, equal documents), masks that leave nothing.
+
 Parity unpinned: the values written at masked positions (the pages only say the
 positions are cleared; the oracle writes ``fill``).
 """
 
+from .loss_oracle import (  # noqa: F401
+    distill_topk,
+    policy_loss,
+    preference_loss,
+    token_logprobs,
+    token_logprobs_backward,
+)
 from .thd_oracle import (  # noqa: F401
     CONTIGUOUS,
     ZIGZAG,
