@@ -53,7 +53,7 @@ THD_PACK_STATIC_BYTES = 1048576
 THD_BF16 = 0
 THD_FP16 = 1
 THD_FP32 = 2
-THD_MAX_VOCAB = 1073741824
+THD_MAX_VOCAB = 268435456
 THD_MAX_TOPK = 256
 THD_MAX_PAIRS = 65536
 

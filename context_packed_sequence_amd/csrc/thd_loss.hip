@@ -1,22 +1,33 @@
 // Label log-probabilities and their gradient, and the two-pass form of the
 // losses for few rows (each row cut into parts over many workgroups).
+#include <atomic>
+
 #include "thd_loss_device.h"
 
 namespace thdcp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;      // words a thread has in flight
-constexpr int kMaxParts = 64;  // one per lane of the wave that joins them
+constexpr int kStep = 16 * kThreads;  // bytes from one of a thread's words to the next
+constexpr int kStatsAhead = 8;        // words a thread has in flight
+constexpr int kGradAhead = 2;
+constexpr int kBackwardTurns = 2;
+constexpr int kBackwardChunkShift = 4;
+constexpr int kMaxParts = 64;         // one per lane of the wave that joins them
 
 __global__ void status_init_kernel(int32_t* status) { *status = THD_OK; }
 
-// A part's words [w0, w1) of a row of `words` words cut into `parts`.
-__device__ __forceinline__ void part_words(int32_t words, int32_t parts, int32_t part, int32_t* w0, int32_t* w1) {
-  const int32_t per = (words + parts - 1) / parts;
-  *w0 = min(part * per, words);
-  *w1 = min(*w0 + per, words);
-}
+// Which row and part of it a workgroup has.  A part is `turns` turns of 256
+// words, counted from the 128-byte line that holds the row's first word.
+struct PartOf {
+  int64_t row;
+  int32_t part;
+  __device__ __forceinline__ PartOf(const LossParts& p, int32_t row0) {
+    const int32_t tile = tile_of(blockIdx.x, gridDim.x, p.chunk_shift);
+    row = row0 + static_cast<int64_t>(tile / p.parts);
+    part = tile % p.parts;
+  }
+};
 
 // Maximum and sum of a row's part.  With one part the row's log-probability
 // and log-sum-exp are written, else the part's pair; part 0 also saves the
@@ -26,8 +37,7 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
   constexpr int kPer = Elem<T>::kPer;
   __shared__ float2 s_red[kThreads / 64];
   const int32_t tid = threadIdx.x;
-  const int64_t row = row0 + static_cast<int64_t>(blockIdx.x / p.parts);
-  const int32_t part = blockIdx.x % p.parts;
+  const auto [row, part] = PartOf(p, row0);
   const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
   // in the two-pass form only the second pass reports errors
   if (a.status && p.parts > 1 && blockIdx.x == 0 && row0 == 0 && tid == 0) *a.status = THD_OK;
@@ -49,9 +59,7 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
   }
 
   const RowCut<T> cut(in, r.vocab);
-  const Word4* body = reinterpret_cast<const Word4*>(in + cut.head);
-  int32_t w0, w1;
-  part_words(cut.words, p.parts, part, &w0, &w1);
+  const RowWords<T> words(in + cut.head, cut.words);
   float edge[1] = {kNegInf};
   float z_label = 0.0f;
   if (part == 0) {
@@ -68,14 +76,23 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
     }
   }
   const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
+  const Word4 nothing = {Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord};
+  const int32_t begin = part * p.turns * kStep - 16 * line_shift(in + cut.head);
+  const int32_t end = min(begin + p.turns * kStep, words.bytes);
   Stat st;
-  int32_t w = w0 + tid;
-  for (; w + (kAhead - 1) * kThreads < w1; w += kAhead * kThreads) {
-    Word4 x[kAhead];
+  for (int32_t b0 = begin; b0 < end; b0 += kStatsAhead * kStep) {
+    Word4 x[kStatsAhead];
+    const int32_t b = b0 + 16 * tid;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) x[k] = load_word(body + w + k * kThreads);
+    for (int k = 0; k < kStatsAhead; ++k) x[k] = words.load(b + k * kStep);
+    if (b0 < 0 || b0 + kStatsAhead * kStep > end) {
 #pragma unroll
-    for (int k = 0; k < kAhead; k += 2) {
+      for (int k = 0; k < kStatsAhead; ++k)
+        if (b + k * kStep < 0 || b + k * kStep >= end) x[k] = nothing;
+    }
+#pragma unroll
+    for (int k = 0; k < kStatsAhead; k += 2) {
+      if (b0 + k * kStep >= end) break;
       float f[2 * kPer], one[kPer];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -85,11 +102,6 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
       }
       absorb(st, f, scale);
     }
-  }
-  for (; w < w1; w += kThreads) {
-    float f[kPer];
-    Elem<T>::unpack(load_word(body + w), f);
-    absorb(st, f, scale);
   }
   absorb(st, edge, scale);
   st = join_block<kThreads>(st, scale, s_red);
@@ -112,7 +124,7 @@ __device__ __forceinline__ Stat join_parts(const LossParts& p, int64_t row, floa
     const float2 v = p.stats[row * p.parts + lane];
     st = Stat{v.x, v.y};
   }
-  return join_lanes<64>(st, scale);
+  return join_lanes<false>(st, scale);
 }
 
 // Log-probability and log-sum-exp from the parts: one wave per row.
@@ -148,16 +160,15 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
   using List = typename std::conditional<kKind == kLossDistill, TargetList<kThreads>, NoList>::type;
   __shared__ List s_list;
   const int32_t tid = threadIdx.x;
-  const int64_t row = row0 + static_cast<int64_t>(blockIdx.x / p.parts);
-  const int32_t part = blockIdx.x % p.parts;
+  const auto [row, part] = PartOf(p, row0);
   const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
   T* out = static_cast<T*>(r.out) + row * r.out_stride;
 
   const RowCut<T> cut(in, r.vocab);
-  const Word4* body = reinterpret_cast<const Word4*>(in + cut.head);
-  int32_t w0, w1;
-  part_words(cut.words, p.parts, part, &w0, &w1);
-  // 0: live, else the value that fills the part
+  const RowWords<T> words(in + cut.head, cut.words);
+  const int32_t shift = line_shift(out + cut.head);
+  const int32_t begin = part * p.turns * kStep - 16 * shift;
+  const int32_t end = min(begin + p.turns * kStep, words.bytes);
   bool live = !a.mask || a.mask[row] != 0;
   bool bad = false;
   int64_t label = 0;
@@ -165,27 +176,36 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
     label = a.labels[row];
     bad = live && (label < 0 || label >= r.vocab);
   }
-  // the first words, read in the same round trip as the row's values
-  Word4 x[kAhead];
+  TeacherRaw raw;
+  if constexpr (kKind == kLossDistill) {
+    if (live && tid < 64) read_teacher(raw, a, row);
+  }
+  // the row's values and its first words, read in one round trip
+  PolicyValues values;
+  if constexpr (kKind == kLossPolicy) values = policy_values(a, row);
+  Word4 x[kGradAhead];
   if (live) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (w0 + k * kThreads + tid < w1) x[k] = load_word(body + w0 + k * kThreads + tid);
+    for (int k = 0; k < kGradAhead; ++k) x[k] = words.load(begin + 16 * tid + k * kStep);
   }
   if constexpr (kKind == kLossDistill) {
     if (live) {
-      if (tid < 64)
-        list_targets<T, kThreads, kRestBit>(s_list, a, row, in, p.targets, cut, r.vocab, w0, w1 - w0, part == 0);
+      if (tid < 64) {
+        float z[kMine];
+        list_targets<T, kThreads, kRestBit>(s_list, raw, z, a, row, in, p.targets, cut, r.vocab,
+                                            part * p.turns * kThreads - shift, p.turns * kThreads, 0, part == 0);
+        store_logits(s_list.z, z, a.k);
+      }
       __syncthreads();
-      bad = s_list.state == kRowBad;
-      live = s_list.state == kRowLive;
+      const int32_t state = __builtin_amdgcn_readfirstlane(s_list.state);
+      bad = state == kRowBad;
+      live = state == kRowLive;
     }
   }
   if (!live || bad) {
-    // the gradient row's words, by its own alignment: the parts tile them too
-    const RowCut<T> to(out, r.vocab);
-    int32_t v0, v1;
-    part_words(to.words, p.parts, part, &v0, &v1);
+    // the gradient row's words, by its own place: the parts tile them too
+    const int32_t v0 = part * p.turns * kThreads;
+    const int32_t v1 = part == p.parts - 1 ? INT32_MAX : v0 + p.turns * kThreads;
     fill_words<T>(out, r.vocab, bad ? Elem<T>::kNanWord : 0u, v0, v1, part == 0, kThreads);
     if (kKind != kLossLogp && part == 0 && tid == 0) {
       const float v = bad ? __builtin_nanf("") : 0.0f;
@@ -207,7 +227,7 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
     base = base_of(st.m);
     if constexpr (kKind == kLossPolicy) {
       const float logp = (p.targets[row] - st.m) - logf(st.s);
-      const PolicyRow pr = policy_row(a, row, logp);
+      const PolicyRow pr = policy_row(a, values, logp);
       amount = -pr.dlogp;
       if (part == 0 && tid == 0) {
         a.loss[row] = pr.loss;
@@ -217,63 +237,86 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
       const float w = a.weights ? a.weights[row] : 1.0f;
       amount = a.temperature * w;
       if (part == 0 && tid < 64) {
-        const float loss = distill_loss(s_list, a, w, st.m, logf(st.s));
+        const float loss = distill_loss(s_list, a, w, [&](float z) { return (z - base) * scale; }, logf(st.s));
         if (tid == 0) a.loss[row] = loss;
       }
     }
     coef = amount / st.s;
   }
 
-  const OutRow<T> dst(out, in, cut.head);
-  const int32_t label_word = kKind != kLossDistill ? cut.word_of(static_cast<int32_t>(label)) : -1;
-  const int32_t label_place = kKind != kLossDistill ? cut.place_of(static_cast<int32_t>(label)) : 0;
   uint32_t hit = 0;
   if constexpr (kKind == kLossDistill) hit = s_list.hit[tid];
-  auto gradient = [&](Word4 word, int32_t w) {
-    float f[kPer], g[kPer];
-    Elem<T>::unpack(word, f);
+  if (same_place(in, out)) {
+    const RowWords<T> to(out + cut.head, cut.words);
+    const int32_t label_word = kKind != kLossDistill ? cut.word_of(static_cast<int32_t>(label)) : -1;
+    const int32_t label_at = label_word >= 0 ? 16 * label_word : -1;
+    const int32_t label_place = kKind != kLossDistill ? cut.place_of(static_cast<int32_t>(label)) : 0;
+    for (int32_t b = begin + 16 * tid; b < end; b += kGradAhead * kStep) {
+      if (b != begin + 16 * tid) {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) g[e] = coef * exp2_fast((f[e] - base) * scale);
-    if constexpr (kKind != kLossDistill) {
-      if (w == label_word) {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (e == label_place) g[e] -= amount;
+        for (int k = 0; k < kGradAhead; ++k) x[k] = words.load(b + k * kStep);
       }
-    } else {
-      const int bit = min((w - w0) / kThreads, kRestBit);
-      if ((hit >> bit) & 1u) take_targets<T, kThreads>(s_list, cut, w, amount, g);
-    }
-    dst.store(w, g);
-  };
-  for (int32_t w = w0 + tid; w < w1; w += kAhead * kThreads) {
-    if (w != w0 + tid) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (w + k * kThreads < w1) x[k] = load_word(body + w + k * kThreads);
-    }
+      for (int k = 0; k < kGradAhead; ++k) {
+        const int32_t at = b + k * kStep;
+        if (at >= end) break;
+        float f[kPer], g[kPer];
+        Elem<T>::unpack(x[k], f);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (w + k * kThreads < w1) gradient(x[k], w + k * kThreads);
+        for (int e = 0; e < kPer; ++e) g[e] = coef * exp2_fast((f[e] - base) * scale);
+        if constexpr (kKind != kLossDistill) {
+          if (at == label_at) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (e == label_place) g[e] -= amount;
+          }
+        } else {
+          const int bit = min((at - begin) / kStep, kRestBit);
+          if ((hit >> bit) & 1u) take_targets<T, kThreads>(s_list, cut, at / 16, amount, g);
+        }
+        to.store(at, Elem<T>::pack(g));
+      }
+    }
+    if (part == 0 && tid < cut.edge) {
+      const int32_t v = cut.edge_column(tid);
+      float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
+      if constexpr (kKind != kLossDistill) {
+        if (v == label) g -= amount;
+      } else {
+        if ((hit >> kEdgeBit) & 1u) g = take_edge_target<T, kThreads>(s_list, cut, amount, g);
+      }
+      out[v] = Elem<T>::round(g);
+    }
+    return;
   }
-  if (part == 0 && tid < cut.edge) {
-    const int32_t v = cut.edge_column(tid);
+  // a gradient row at another place within 16 bytes: element by element
+  const int64_t v0 = static_cast<int64_t>(part) * p.turns * kThreads * kPer + cut.head - shift * kPer;
+  const int64_t v1 = v0 + static_cast<int64_t>(p.turns) * kThreads * kPer;
+  const int32_t from = part == 0 ? 0 : static_cast<int32_t>(max(v0, static_cast<int64_t>(0)));
+  const int32_t to_v = part == p.parts - 1 ? r.vocab : static_cast<int32_t>(min(v1, static_cast<int64_t>(r.vocab)));
+  for (int32_t v = from + tid; v < to_v; v += kThreads) {
     float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
-    if constexpr (kKind != kLossDistill) {
-      if (v == label) g -= amount;
-    } else {
-      if ((hit >> kEdgeBit) & 1u) g = take_edge_target<T, kThreads>(s_list, cut, amount, g);
-    }
+    if (kKind != kLossDistill && v == label) g -= amount;
     out[v] = Elem<T>::round(g);
+  }
+  if constexpr (kKind == kLossDistill) {
+    __syncthreads();  // a target's element is stored again, after the first time
+    put_targets<T, kThreads>(s_list, out, coef, base, scale, amount);
   }
 }
 
 int32_t words_of(int32_t vocab, int32_t dtype) { return vocab / (dtype == THD_FP32 ? 4 : 8); }
 
-int32_t clamp_parts(int64_t want, int32_t words) {
-  const int64_t most = words / kThreads < kMaxParts ? words / kThreads : kMaxParts;
-  if (want > most) want = most;
-  return want < 1 ? 1 : static_cast<int32_t>(want);
+// About `want` parts a row: the turns of a part, and the parts that cover a
+// row whose first word lies anywhere in its 128-byte line.
+LossParts cut_row(int64_t want, int32_t vocab, int32_t dtype) {
+  const int64_t turns = (words_of(vocab, dtype) + 7LL + kThreads - 1) / kThreads;
+  if (want > kMaxParts) want = kMaxParts;
+  if (want < 1) want = 1;
+  LossParts p{};
+  p.turns = static_cast<int32_t>((turns + want - 1) / want);
+  p.parts = static_cast<int32_t>((turns + p.turns - 1) / p.turns);
+  return p;
 }
 
 // Slices of rows whose workgroups a grid can count (2^32 threads).
@@ -320,12 +363,26 @@ hipError_t launch_part_grad(const LogitRows& r, const LossArgs& a, const LossPar
 
 }  // namespace
 
-int32_t logp_parts(int32_t rows, int32_t vocab, int32_t dtype) {
-  return rows < 1 ? 1 : clamp_parts(1024 / rows, words_of(vocab, dtype));
+int32_t compute_units() {
+  static std::atomic<int32_t> known[64];
+  int device = 0;
+  if (hipGetDevice(&device) != hipSuccess || device < 0 || device >= 64) return 256;
+  int32_t n = known[device].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int v = 0;
+    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || v < 1) return 256;
+    n = v;
+    known[device].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
-int32_t loss_parts(int32_t rows, int32_t vocab, int32_t dtype) {
-  return rows < 1 ? 1 : clamp_parts(512 / rows, words_of(vocab, dtype));
+LossParts logp_parts(int32_t rows, int32_t vocab, int32_t dtype) {
+  return cut_row(rows < 1 ? 1 : 1024 / rows, vocab, dtype);
+}
+
+LossParts loss_parts(int32_t rows, int32_t vocab, int32_t dtype) {
+  return cut_row(rows < 1 ? 1 : 512 / rows, vocab, dtype);
 }
 
 hipError_t launch_status_init(int32_t* status, hipStream_t stream) {
@@ -341,9 +398,11 @@ hipError_t launch_token_logprobs(const LogitRows& r, const LossArgs& a, const Lo
 }
 
 hipError_t launch_logp_backward(const LogitRows& r, const LossArgs& a, hipStream_t stream) {
-  const int32_t words = words_of(r.vocab, r.dtype);
+  const int64_t turns = (words_of(r.vocab, r.dtype) + 7LL + kThreads - 1) / kThreads;
   LossParts p{};
-  p.parts = words / (kAhead * kThreads) > 0 ? (words + kAhead * kThreads - 1) / (kAhead * kThreads) : 1;
+  p.turns = kBackwardTurns;
+  p.parts = static_cast<int32_t>((turns + kBackwardTurns - 1) / kBackwardTurns);
+  p.chunk_shift = kBackwardChunkShift;
   return launch_part_grad<kLossLogp>(r, a, p, stream);
 }
 

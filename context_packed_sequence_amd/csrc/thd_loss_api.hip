@@ -62,7 +62,7 @@ Layout loss_layout(void* workspace, int64_t rows, int64_t vocab, int32_t dtype, 
   Layout l{};
   const auto n = static_cast<int32_t>(rows);
   const auto v = static_cast<int32_t>(vocab);
-  l.parts.parts = targets == 0 ? thdcp::logp_parts(n, v, dtype) : thdcp::loss_parts(n, v, dtype);
+  l.parts = targets == 0 ? thdcp::logp_parts(n, v, dtype) : thdcp::loss_parts(n, v, dtype);
   if (l.parts.parts == 1) return l;
   const int64_t stats = rows * l.parts.parts * static_cast<int64_t>(sizeof(float2));
   l.bytes = stats + rows * (targets > 1 ? targets : 1) * static_cast<int64_t>(sizeof(float));

@@ -7,10 +7,16 @@
 //   lse    = M + ln s                      (c = 1)
 // Maximum and sum come from one pass: a thread holds (m, s) of what it has
 // seen, and on a new maximum m' its sum becomes s exp(c (m - m')) plus the new
-// terms.  Two such pairs join the same way.  Every exponent is taken of a
-// difference that is formed first, c (z - m) = log2(e) c (z - m) in base 2:
-// z - m is exact or rounded once, so that the size of the logits costs the
-// result nothing.
+// terms.  Two such pairs join the same way.  In base 2, with scale = log2(e) c,
+// the exponents are either
+//   (z - m) scale           z - m exact or rounded once (Stat), or
+//   fma(z, scale, -top)     rounded once, where top is the rounded m scale
+//                           (FastStat),
+// so that the size of the logits costs the result nothing.  The second form
+// takes one instruction less for every exponential and is used where those
+// bound the kernel; its pair is relative to top itself, not to m, which makes
+// the rounding of top cancel.  It does not hold logits of any size: rows whose
+// top is beyond kHuge take the first form.
 //
 // A gradient row has the form g_v = coef (q_v - sum_k p_k [v = id_k]): one
 // target with p = 1 for the label losses, k targets for the distillation.
@@ -20,6 +26,7 @@
 
 #include <type_traits>
 
+#include "thd_device.h"
 #include "thd_loss_internal.h"
 
 namespace thdcp {
@@ -124,6 +131,21 @@ struct Elem<float> {
   static __device__ __forceinline__ float round(float g) { return g; }
 };
 
+// One element as it lies in memory, to be decoded later: decoding is the first
+// use of a load, and waits for it and every load before it.
+template <typename T>
+__device__ __forceinline__ uint32_t load_raw(const T* p) {
+  if constexpr (sizeof(T) == 2) return *reinterpret_cast<const uint16_t*>(p);
+  else return *reinterpret_cast<const uint32_t*>(p);
+}
+template <typename T>
+__device__ __forceinline__ float decode(uint32_t raw) {
+  if constexpr (std::is_same_v<T, Bf16>) return __builtin_bit_cast(float, raw << 16);
+  else if constexpr (std::is_same_v<T, Fp16>)
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(raw)));
+  else return __builtin_bit_cast(float, raw);
+}
+
 // A row as a head of single elements up to the first 16-byte boundary, whole
 // words, and a tail of single elements: no access leaves the row.  Head and
 // tail together ("edge") hold at most 2 (kPer - 1) elements; edge element i is
@@ -154,29 +176,56 @@ struct RowCut {
 
 __device__ __forceinline__ Word4 load_word(const Word4* p) { return __builtin_nontemporal_load(p); }
 
-// Where a gradient row goes.  It has the words of the logits' row when both
-// start at the same place within 16 bytes, else its elements are stored one
-// by one.
+// The words of a row behind a buffer resource of exactly their size: a load
+// past either end gives zeros and a store there is dropped, both in hardware,
+// so that the loops over a thread's words have no branches and every load of a
+// row is issued before the first one is waited for.  Word w of the row belongs
+// to thread (w + shift) mod threads, where shift puts a wave's 64 words on whole
+// 128-byte lines of the row that is written: without it every wave of an
+// unaligned row writes two part lines.
 template <typename T>
-struct OutRow {
-  T* row;
-  Word4* body;
-  int32_t head;
-  bool whole;
-  __device__ __forceinline__ OutRow(T* out, const void* in, int32_t head_) : row(out), head(head_) {
-    whole = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(in)) & 15) == 0;
-    body = reinterpret_cast<Word4*>(out + head_);
+struct RowWords {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int32_t bytes;
+  __device__ __forceinline__ RowWords(const void* body, int32_t words)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(body), 0, 16 * words, kBufferWord3)),
+        bytes(16 * words) {}
+  // byte offsets: negative ones (as unsigned, huge) are out of range as well
+  __device__ __forceinline__ Word4 load(int32_t at) const {
+    return __builtin_bit_cast(Word4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, kStreamLoad));
   }
-  __device__ __forceinline__ void store(int32_t word, const float (&g)[Elem<T>::kPer]) const {
-    if (whole) {
-      __builtin_nontemporal_store(Elem<T>::pack(g), body + word);
-    } else {
-#pragma unroll
-      for (int e = 0; e < Elem<T>::kPer; ++e)
-        row[head + static_cast<int64_t>(word) * Elem<T>::kPer + e] = Elem<T>::round(g[e]);
-    }
+  __device__ __forceinline__ void store(int32_t at, Word4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, at, 0, kStreamStorePolicy);
   }
+  // 64 lanes' words straight to LDS, lane i's to to[i]; `to` is uniform
+  __device__ __forceinline__ void load_to_lds(Word4* to, int32_t at) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(to)), 16, at, 0, 0,
+        kStreamLoad);
+  }
+  static constexpr int kStreamLoad = 2;  // non-temporal
 };
+
+// Words by which a row's threads are shifted, from the place its body is
+// written to.
+__device__ __forceinline__ int32_t line_shift(const void* body) {
+  return static_cast<int32_t>((reinterpret_cast<uintptr_t>(body) >> 4) & 7);
+}
+
+__device__ __forceinline__ bool same_place(const void* a, const void* b) {
+  return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
+// Which of n tiles workgroup b takes.  Workgroup b runs on XCD b mod 8; the
+// tiles are cut into chunks of 2^shift and XCD x takes chunks x, x + 8, ...
+// front to back, so that each XCD streams through memory of its own (the
+// remainder past the last 8 whole chunks in plain order).
+__device__ __forceinline__ int32_t tile_of(int32_t b, int32_t n, int32_t shift) {
+  const int32_t x = b & 7, j = b >> 3;
+  const int32_t tile = ((((j >> shift) << 3) + x) << shift) + (j & ((1 << shift) - 1));
+  const int32_t whole = (n >> (shift + 3)) << (shift + 3);
+  return b < whole ? tile : b;
+}
 
 // Fills elements [0, n) of a row with one value (0 or NaN, given as a word of
 // equal elements): rows that a mask leaves out, or whose target is not a
@@ -217,35 +266,109 @@ __device__ __forceinline__ void absorb(Stat& st, const float (&x)[N], float scal
   st.s = s;
 }
 
-// Joins the pairs of kWidth neighbouring lanes (a power of two); every lane
-// of the group gets the same result.
-template <int kWidth>
-__device__ __forceinline__ Stat join_lanes(Stat st, float scale) {
-  float m = st.m;
+// The form with top = max(z) scale.  The exponent of the largest logit is what
+// top was rounded by, up to 2^-24 of it: harmless in the result, but beyond the
+// exponential's range from about 2^31 on.  So top starts at a value well within:
+// a thread that has seen nothing, or nothing above it, has the sum 0 and needs
+// no case of its own, and a row that ends there, or as far above, is huge.
+constexpr float kLowestTop = -1.0e9f;
+constexpr float kHuge = 0.9e9f;
+
+struct FastStat {
+  float top = kLowestTop;
+  float s = 0.0f;
+};
+
+template <int N>
+__device__ __forceinline__ void absorb(FastStat& st, const float (&x)[N], float scale) {
+  float m = x[0];
 #pragma unroll
-  for (int d = kWidth / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+  const float top = fmaxf(st.top, m * scale);
+  float s = st.s * exp2_fast(st.top - top);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += exp2_fast(fmaf(x[i], scale, -top));
+  st.top = top;
+  st.s = s;
+}
+
+// Maximum and sum over a wave, or over its first row of 16 lanes, on DPP lane
+// moves (device helper dpp_move); the result is the same in every lane.
+template <bool kRowOnly, typename Op>
+__device__ __forceinline__ float wave_reduce(float x, float identity, Op op) {
+  const auto move = [&](auto ctrl, auto mask) {
+    const int32_t y = dpp_move<decltype(ctrl)::value, decltype(mask)::value>(
+        __builtin_bit_cast(int32_t, x), __builtin_bit_cast(int32_t, identity));
+    x = op(x, __builtin_bit_cast(float, y));
+  };
+  using std::integral_constant;
+  move(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
+  move(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  move(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  move(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  if constexpr (kRowOnly)
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, x), 15));
+  move(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+  move(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, x), 63));
+}
+
+struct FloatMax {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct FloatAdd {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+__device__ __forceinline__ float wave_max(float x) { return wave_reduce<false>(x, kNegInf, FloatMax{}); }
+__device__ __forceinline__ float wave_add(float x) { return wave_reduce<false>(x, 0.0f, FloatAdd{}); }
+
+// Joins the pairs of a wave's lanes (of its first 16 if kRowOnly).
+template <bool kRowOnly>
+__device__ __forceinline__ Stat join_lanes(Stat st, float scale) {
+  const float m = wave_reduce<kRowOnly>(st.m, kNegInf, FloatMax{});
   const float b = base_of(m);
   // a NaN among the logits leaves its thread's maximum untouched and its sum
   // NaN, which this product keeps
-  float s = st.s * exp2_fast((st.m - b) * scale);
-#pragma unroll
-  for (int d = kWidth / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
-  return Stat{m, s};
+  return Stat{m, wave_reduce<kRowOnly>(st.s * exp2_fast((st.m - b) * scale), 0.0f, FloatAdd{})};
 }
+
+template <bool kRowOnly>
+__device__ __forceinline__ FastStat join_lanes(FastStat st, float) {
+  const float top = wave_reduce<kRowOnly>(st.top, kLowestTop, FloatMax{});
+  return FastStat{top, wave_reduce<kRowOnly>(st.s * exp2_fast(st.top - top), 0.0f, FloatAdd{})};
+}
+
+__device__ __forceinline__ float2 as_pair(Stat st) { return make_float2(st.m, st.s); }
+__device__ __forceinline__ float2 as_pair(FastStat st) { return make_float2(st.top, st.s); }
 
 // Joins the pairs of a workgroup in a fixed order.  s_red holds one pair per
 // wave.  Contains one barrier; what threads wrote to LDS before it can be
 // read after it.
-template <int kThreads>
-__device__ __forceinline__ Stat join_block(Stat st, float scale, float2* s_red) {
+template <int kThreads, typename S>
+__device__ __forceinline__ S join_block(S st, float scale, float2* s_red) {
   constexpr int kWaves = kThreads / 64;
-  st = join_lanes<64>(st, scale);
+  static_assert(kWaves <= 16);
+  st = join_lanes<false>(st, scale);
   const int lane = threadIdx.x & 63;
-  if (lane == 0) s_red[threadIdx.x >> 6] = make_float2(st.m, st.s);
+  if (lane == 0) s_red[threadIdx.x >> 6] = as_pair(st);
   __syncthreads();
   if constexpr (kWaves == 1) return st;
-  const float2 r = s_red[lane & (kWaves - 1)];
-  return join_lanes<kWaves>(Stat{r.x, r.y}, scale);
+  S other;
+  if (lane < kWaves) other = S{s_red[lane].x, s_red[lane].y};
+  return join_lanes<true>(other, scale);
+}
+
+// Maximum and sum of a whole row in the first form, element by element: rows
+// beyond kHuge.  Every thread of the workgroup calls it.
+template <typename T, int kThreads>
+__device__ __forceinline__ Stat row_stat(const T* in, int32_t vocab, float scale, float2* s_red) {
+  Stat st;
+  for (int32_t v = threadIdx.x; v < vocab; v += kThreads) {
+    const float f[1] = {Elem<T>::load(in + v)};
+    absorb(st, f, scale);
+  }
+  __syncthreads();  // s_red may still be read
+  return join_block<kThreads>(st, scale, s_red);
 }
 
 // ---- row values of the policy loss ----------------------------------------
@@ -277,34 +400,49 @@ __device__ __forceinline__ float exp_minus_1_minus(float u) {
   return exp2_fast(u * kLog2e) - 1.0f - u;
 }
 
-__device__ __forceinline__ PolicyRow policy_row(const LossArgs& a, int64_t row, float logp) {
-  const float adv = a.advantages[row];
-  const double d = static_cast<double>(logp) - static_cast<double>(a.old_logp[row]);
+// What a row brings to it.
+struct PolicyValues {
+  float old_logp = 0.0f, ref_logp = 0.0f, advantage = 0.0f, weight = 1.0f;
+};
+
+__device__ __forceinline__ PolicyValues policy_values(const LossArgs& a, int64_t row) {
+  PolicyValues v;
+  v.old_logp = a.old_logp[row];
+  v.advantage = a.advantages[row];
+  if (a.ref_logp) v.ref_logp = a.ref_logp[row];
+  if (a.weights) v.weight = a.weights[row];
+  return v;
+}
+
+__device__ __forceinline__ PolicyRow policy_row(const LossArgs& a, const PolicyValues& v, float logp) {
+  const float adv = v.advantage;
+  const double d = static_cast<double>(logp) - static_cast<double>(v.old_logp);
   const bool clipped = adv >= 0.0f ? d > a.ln_high : d < a.ln_low;
   const float edge = adv >= 0.0f ? a.high : a.low;
   const float ratio = exp2_fast(static_cast<float>(d) * kLog2e);
   float loss = -(clipped ? edge : ratio) * adv;
   float g = clipped ? 0.0f : -ratio * adv;
   if (a.ref_logp) {
-    const float u = a.ref_logp[row] - logp;
+    const float u = v.ref_logp - logp;
     const float k = exp_minus_1_minus(u);
     loss = fmaf(a.kl_coef, k, loss);
     g = fmaf(-a.kl_coef, k + u, g);
   }
-  const float w = a.weights ? a.weights[row] : 1.0f;
-  return PolicyRow{w * loss, w * g};
+  return PolicyRow{v.weight * loss, v.weight * g};
 }
 
 // ---- targets of the distillation -------------------------------------------
 // Up to THD_MAX_TOPK teacher columns of one row, in LDS.  p = softmax(t / tau)
 // over the given columns; a column given as -1, or with a logit of -inf, has no
-// part in it.  Each column that occurs is listed once, with the sum of its
-// probabilities in the order they are given, under the thread that holds the
-// column's element, so that a gradient word costs its thread one bit test and a
-// list walk only where a target falls into it.  The order of a thread's list
-// depends on the lanes' order; no result does, as every element is in it once.
+// part in it.  A column is listed under the thread that holds its element, so
+// that a gradient word costs its thread one bit test and a list walk only where
+// a target falls into it.  The order of a list depends on the lanes' order; no
+// result does, as every column is in it once: a column that is given more than
+// once (found by walking the lists, which are short) makes the wave sum its
+// probabilities, in the order they are given, into the first of its entries.
 constexpr int kEdgeBit = 31;
-constexpr int kRestBit = 30;  // words beyond the ones a thread holds in registers
+constexpr int kRestBit = 30;  // words beyond the ones that have a bit each
+constexpr int kMine = THD_MAX_TOPK / 64;
 
 template <int kThreads>
 struct alignas(16) TargetList {
@@ -326,44 +464,65 @@ __device__ __forceinline__ void wave_sync_lds() {
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ float load_any(const void* p, int64_t i, int32_t dtype) {
-  if (dtype == THD_BF16) return Elem<Bf16>::load(static_cast<const Bf16*>(p) + i);
-  if (dtype == THD_FP16) return Elem<Fp16>::load(static_cast<const Fp16*>(p) + i);
-  return static_cast<const float*>(p)[i];
+// A row's teacher entries as they lie in memory, entry lane + 64 j in lane's
+// place j: issued early and decoded later, so that nothing waits for them.
+struct TeacherRaw {
+  uint32_t id_low[kMine], id_high[kMine], logit[kMine];
+};
+
+__device__ __forceinline__ void read_teacher(TeacherRaw& raw, const LossArgs& a, int64_t row) {
+  const int64_t at = row * a.teacher_stride;
+  const int64_t wide = a.ids64 ? 2 : 1;
+  const uint32_t* ids = static_cast<const uint32_t*>(a.teacher_ids) + at * wide;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int32_t i = static_cast<int32_t>(threadIdx.x) + 64 * j;
+    raw.id_low[j] = ~0u;
+    raw.id_high[j] = ~0u;
+    raw.logit[j] = 0;
+    if (i < a.k) {
+      raw.id_low[j] = ids[i * wide];
+      if (a.ids64) raw.id_high[j] = ids[i * wide + 1];
+      if (a.teacher_dtype == THD_FP32) raw.logit[j] = static_cast<const uint32_t*>(a.teacher)[at + i];
+      else raw.logit[j] = static_cast<const uint16_t*>(a.teacher)[at + i];
+    }
+  }
 }
 
-// Fills the list; run by wave 0 alone, its results are visible to the
-// workgroup after the next barrier.  The workgroup holds the row's words
-// [w0, w0 + n_words), word w0 + i in thread i % kThreads, of which a thread has
-// a bit each for its first kHeld and one for the rest, and the row's edge if
-// own_edge.  The student's logits are read from the row, or from z_saved
-// where the row may be overwritten by then.
+__device__ __forceinline__ float teacher_logit(uint32_t raw, int32_t dtype) {
+  if (dtype == THD_BF16) return __builtin_bit_cast(float, raw << 16);
+  if (dtype == THD_FP16) return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(raw)));
+  return __builtin_bit_cast(float, raw);
+}
+
+// Fills the list from the row's entries; run by wave 0 alone.  The workgroup
+// holds the row's words [w0, w0 + n_words), word w in thread (w - w0 + shift) %
+// kThreads, of which a thread has a bit each for its first kHeld and one for the
+// rest, and the row's edge if own_edge.  Returns the lane's student logits in z
+// (read from the row, or from z_saved where the row may be overwritten by
+// then): store_logits puts them into the list once they are here.  The list is
+// complete after the next barrier.
 template <typename T, int kThreads, int kHeld>
-__device__ __forceinline__ void list_targets(TargetList<kThreads>& l, const LossArgs& a, int64_t row, const T* in,
-                                             const float* z_saved, const RowCut<T>& cut, int32_t vocab, int32_t w0,
-                                             int32_t n_words, bool own_edge) {
-  constexpr int kMine = THD_MAX_TOPK / 64;
+__device__ __forceinline__ void list_targets(TargetList<kThreads>& l, const TeacherRaw& raw, float (&z)[kMine],
+                                             const LossArgs& a, int64_t row, const T* in, const float* z_saved,
+                                             const RowCut<T>& cut, int32_t vocab, int32_t w0, int32_t n_words,
+                                             int32_t shift, bool own_edge) {
   const int lane = threadIdx.x;
-  const int64_t at = row * a.teacher_stride;
   int32_t id[kMine];
-  float t[kMine], sum[kMine];
-  bool first[kMine];
+  float t[kMine];
   bool bad = false;
   float top = kNegInf;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
-    const int32_t i = lane + 64 * j;
-    id[j] = -1;
-    t[j] = kNegInf;
-    if (i < a.k) {
-      const int64_t v = a.ids64 ? static_cast<const int64_t*>(a.teacher_ids)[at + i]
-                                : static_cast<const int32_t*>(a.teacher_ids)[at + i];
-      if (v < -1 || v >= vocab) bad = true;
-      else if (v >= 0) {
-        id[j] = static_cast<int32_t>(v);
-        t[j] = load_any(a.teacher, at + i, a.teacher_dtype);
-      }
-    }
+    const int32_t low = static_cast<int32_t>(raw.id_low[j]);
+    const int32_t high = a.ids64 ? static_cast<int32_t>(raw.id_high[j]) : low >> 31;
+    const bool unused = low == -1 && high == -1;
+    const bool column = high == 0 && low >= 0 && low < vocab;
+    if (!unused && !column) bad = true;
+    id[j] = column ? low : -1;
+    t[j] = column ? teacher_logit(raw.logit[j], a.teacher_dtype) : kNegInf;
+    z[j] = 0.0f;
+    if (id[j] >= 0) z[j] = z_saved ? z_saved[row * a.k + lane + 64 * j] : Elem<T>::load(in + id[j]);
     top = fmaxf(top, t[j]);
   }
   for (int i = lane; i < kThreads; i += 64) {
@@ -371,87 +530,102 @@ __device__ __forceinline__ void list_targets(TargetList<kThreads>& l, const Loss
     l.hit[i] = 0;
   }
   bad = __any(bad);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float base = base_of(top);
+  const float base = base_of(wave_max(top));
   float ts = 0.0f;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) ts += exp2_fast((t[j] - base) * a.inv_temperature * kLog2e);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) ts += __shfl_xor(ts, d);
+  ts = wave_add(ts);
   const float ln_ts = logf(ts);
   const float inv_ts = 1.0f / ts;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
+    if (64 * j >= a.k) continue;  // entries up to the next multiple of 64 are written
     const int32_t i = lane + 64 * j;
     const float x = (t[j] - base) * a.inv_temperature;
     const float p = exp2_fast(x * kLog2e) * inv_ts;
     if (p == 0.0f || bad) id[j] = -1;
-    if (64 * j < a.k) {  // entries up to the next multiple of 64 are written
-      l.id[i] = id[j];
-      l.p[i] = id[j] >= 0 ? p : 0.0f;
-      l.ln_p[i] = x - ln_ts;
-      float z = 0.0f;
-      if (id[j] >= 0) z = z_saved ? z_saved[row * a.k + i] : Elem<T>::load(in + id[j]);
-      l.z[i] = z;
-    }
+    l.id[i] = id[j];
+    l.p[i] = l.sum[i] = id[j] >= 0 ? p : 0.0f;
+    l.ln_p[i] = x - ln_ts;
   }
   if (lane == 0) l.state = bad ? kRowBad : (ts == 0.0f ? kRowEmpty : kRowLive);
   wave_sync_lds();
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    sum[j] = 0.0f;
-    first[j] = true;
-    if (64 * j >= a.k) continue;
+
+  bool listed[kMine];
+  const auto insert = [&](int j) {
     const int32_t i = lane + 64 * j;
-    for (int n = 0; n < a.k; n += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(l.id + n);
-      const int32_t other[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (other[e] == id[j]) {
-          sum[j] += l.p[n + e];
-          if (n + e < i) first[j] = false;
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    const int32_t i = lane + 64 * j;
-    if (64 * j >= a.k || id[j] < 0 || !first[j]) continue;
-    l.sum[i] = sum[j];
     int32_t owner, bit;
     const int32_t w = cut.word_of(id[j]);
     if (w < 0) {
-      if (!own_edge) continue;
+      if (!own_edge) return false;
       owner = cut.edge_of(id[j]);
       bit = kEdgeBit;
     } else {
-      const int32_t local = w - w0;
-      if (local < 0 || local >= n_words) continue;
+      if (w < w0 || w >= w0 + n_words) return false;
+      const int32_t local = w - w0 + shift;
       owner = local % kThreads;
       bit = local / kThreads < kHeld ? local / kThreads : kRestBit;
     }
     l.next[i] = atomicExch(&l.head[owner], i);
     atomicOr(&l.hit[owner], 1u << bit);
+    return true;
+  };
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) listed[j] = 64 * j < a.k && id[j] >= 0 && insert(j);
+  wave_sync_lds();
+  bool twice = false;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    if (!listed[j]) continue;
+    for (int32_t n = l.next[lane + 64 * j]; n >= 0; n = l.next[n]) twice |= l.id[n] == id[j];
+  }
+  if (!__any(twice)) return;
+
+  float sum[kMine];
+  bool first[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    sum[j] = 0.0f;
+    first[j] = true;
+    if (64 * j >= a.k) continue;
+    for (int n = 0; n < a.k; ++n) {
+      if (l.id[n] != id[j]) continue;
+      sum[j] += l.p[n];
+      if (n < lane + 64 * j) first[j] = false;
+    }
+  }
+  for (int i = lane; i < kThreads; i += 64) {
+    l.head[i] = -1;
+    l.hit[i] = 0;
+  }
+  wave_sync_lds();
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    if (!listed[j] || !first[j]) continue;
+    l.sum[lane + 64 * j] = sum[j];
+    insert(j);
   }
 }
 
+__device__ __forceinline__ void store_logits(float* to, const float (&z)[kMine], int32_t k) {
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    if (64 * j < k) to[threadIdx.x + 64 * j] = z[j];
+}
+
 // Loss of the row from the filled list, on wave 0 (the same value in every
-// lane): tau^2 w sum p (ln p - ln q).
-template <int kThreads>
-__device__ __forceinline__ float distill_loss(const TargetList<kThreads>& l, const LossArgs& a, float w, float m,
+// lane): tau^2 w sum p (ln p - ln q).  exponent(z) is log2 of exp(z / tau) over
+// the row's largest one.
+template <int kThreads, typename F>
+__device__ __forceinline__ float distill_loss(const TargetList<kThreads>& l, const LossArgs& a, float w, F exponent,
                                               float ln_s) {
   float loss = 0.0f;
   for (int i = threadIdx.x; i < a.k; i += 64) {
     if (l.id[i] < 0) continue;
-    const float ln_q = (l.z[i] - m) * a.inv_temperature - ln_s;
+    const float ln_q = exponent(l.z[i]) * kLn2 - ln_s;
     loss += l.p[i] * (l.ln_p[i] - ln_q);
   }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) loss += __shfl_xor(loss, d);
-  return a.temperature * a.temperature * w * loss;
+  return a.temperature * a.temperature * w * wave_add(loss);
 }
 
 // Takes a gradient word's targets from it: g[e] -= amount * sum.
@@ -462,9 +636,10 @@ __device__ __forceinline__ void take_targets(const TargetList<kThreads>& l, cons
     const int32_t v = l.id[n];
     if (cut.word_of(v) != word) continue;
     const int32_t place = cut.place_of(v);
+    const float p = l.sum[n];
 #pragma unroll
     for (int e = 0; e < Elem<T>::kPer; ++e)
-      if (e == place) g[e] = fmaf(-amount, l.sum[n], g[e]);
+      if (e == place) g[e] = fmaf(-amount, p, g[e]);
   }
 }
 
@@ -473,9 +648,20 @@ __device__ __forceinline__ float take_edge_target(const TargetList<kThreads>& l,
                                                   float g) {
   for (int32_t n = l.head[threadIdx.x]; n >= 0; n = l.next[n]) {
     const int32_t v = l.id[n];
-    if (cut.word_of(v) < 0) g = fmaf(-amount, l.sum[n], g);
+    if (cut.word_of(v) < 0 && cut.edge_of(v) == static_cast<int32_t>(threadIdx.x)) g = fmaf(-amount, l.sum[n], g);
   }
   return g;
+}
+
+// Stores the targets' elements of a gradient row whose other elements are
+// stored already: g = coef exp2((z - base) scale) - amount * sum.
+template <typename T, int kThreads>
+__device__ __forceinline__ void put_targets(const TargetList<kThreads>& l, T* out, float coef, float base,
+                                            float scale, float amount) {
+  for (int32_t n = l.head[threadIdx.x]; n >= 0; n = l.next[n]) {
+    const float g = coef * exp2_fast((l.z[n] - base) * scale);
+    out[l.id[n]] = Elem<T>::round(fmaf(-amount, l.sum[n], g));
+  }
 }
 
 }  // namespace thdcp

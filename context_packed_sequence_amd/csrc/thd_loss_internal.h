@@ -59,14 +59,19 @@ struct LossArgs {
 // the logits of the row's targets (its label, or the teacher's columns).
 struct LossParts {
   int32_t parts;             // 1: the one-pass form, no workspace
+  int32_t turns;             // turns of 256 words in a part
+  int32_t chunk_shift;       // parts per chunk of an XCD's order, as a power of two
   float2* stats;             // [rows][parts] (maximum, sum of exponentials)
   float* targets;            // [rows][k]
 };
 
-// Parts a row is cut into so that few rows still fill the chip; 1 where one
+// How a row is cut so that few rows still fill the chip; one part where one
 // workgroup per row is the faster form.
-int32_t logp_parts(int32_t rows, int32_t vocab, int32_t dtype);
-int32_t loss_parts(int32_t rows, int32_t vocab, int32_t dtype);
+LossParts logp_parts(int32_t rows, int32_t vocab, int32_t dtype);
+LossParts loss_parts(int32_t rows, int32_t vocab, int32_t dtype);
+
+// Compute units of the current device (256 where it does not say).
+int32_t compute_units();
 
 hipError_t launch_status_init(int32_t* status, hipStream_t stream);
 hipError_t launch_token_logprobs(const LogitRows& r, const LossArgs& a, const LossParts& p, hipStream_t stream);

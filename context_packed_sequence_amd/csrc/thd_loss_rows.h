@@ -8,63 +8,89 @@
 
 namespace thdcp {
 
-constexpr int kJoinWords = 2;  // words absorbed at a time: 16 elements share one rescale
+constexpr int kRestWords = 4;  // words in flight of a row's part beyond the registers
 
-template <typename T, int kThreads, int kWords, LossKind kKind>
-__global__ __launch_bounds__(kThreads, 4) void row_loss_kernel(LogitRows r, LossArgs a, int32_t row0) {
+// kWords words of a row per thread in registers, kLds more in LDS.  Up to 8 words
+// leave room for 8 waves per SIMD.
+template <typename T, int kThreads, int kWords, int kLds, LossKind kKind>
+__global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel(LogitRows r, LossArgs a, int32_t row0,
+                                                               int32_t chunk_shift) {
   constexpr int kPer = Elem<T>::kPer;
-  static_assert(kWords % kJoinWords == 0 && kWords < kRestBit);
+  constexpr int kStep = 16 * kThreads;  // bytes from one of a thread's words to the next
+  constexpr int kHeld = kWords + kLds;
+  // words absorbed at a time, whose elements share one rescale
+  constexpr int kJoinWords = kWords <= 8 ? 1 : 2;
+  static_assert(kWords % kJoinWords == 0 && kHeld <= kRestBit);
   struct NoList {
     int32_t state;
   };
   using List = typename std::conditional<kKind == kLossDistill, TargetList<kThreads>, NoList>::type;
   __shared__ float2 s_red[kThreads / 64];
   __shared__ List s_list;
+  extern __shared__ Word4 s_row[];  // [kLds][kThreads], each word used by its own thread alone
   const int32_t tid = threadIdx.x;
-  const int64_t row = static_cast<int64_t>(row0) + blockIdx.x;
+  const int64_t row = row0 + static_cast<int64_t>(tile_of(blockIdx.x, gridDim.x, chunk_shift));
   const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
   T* out = static_cast<T*>(r.out) + row * r.out_stride;
+  const auto fill_row = [&](bool bad) {
+    fill_words<T>(out, r.vocab, bad ? Elem<T>::kNanWord : 0u, 0, INT32_MAX, true, kThreads);
+    if (tid == 0) {
+      const float v = bad ? __builtin_nanf("") : 0.0f;
+      a.loss[row] = v;
+      if (kKind == kLossPolicy) a.logp[row] = v;
+      if (bad && a.status) *a.status = THD_ERR_LABEL;
+    }
+  };
 
+  // The row's own values and what its first columns need are issued before its
+  // words: loads return in order, and these are wanted first.
+  const uint8_t live = a.mask ? a.mask[row] : 1;
   int64_t label = 0;
-  if constexpr (kKind == kLossPolicy) label = a.labels[row];
-  if (a.mask && a.mask[row] == 0) {
-    fill_words<T>(out, r.vocab, 0u, 0, INT32_MAX, true, kThreads);
-    if (tid == 0) {
-      a.loss[row] = 0.0f;
-      if (kKind == kLossPolicy) a.logp[row] = 0.0f;
-    }
-    return;
+  PolicyValues value;
+  TeacherRaw raw;
+  if constexpr (kKind == kLossPolicy) {
+    label = a.labels[row];
+    value = policy_values(a, row);
+  } else {
+    if (a.weights) value.weight = a.weights[row];
+    if (tid < 64) read_teacher(raw, a, row);
   }
-  if (kKind == kLossPolicy && (label < 0 || label >= r.vocab)) {
-    fill_words<T>(out, r.vocab, Elem<T>::kNanWord, 0, INT32_MAX, true, kThreads);
-    if (tid == 0) {
-      a.loss[row] = a.logp[row] = __builtin_nanf("");
-      if (a.status) *a.status = THD_ERR_LABEL;
-    }
-    return;
-  }
+  if (!live) return fill_row(false);
+  if (kKind == kLossPolicy && (label < 0 || label >= r.vocab)) return fill_row(true);
 
   const RowCut<T> cut(in, r.vocab);
-  const Word4* body = reinterpret_cast<const Word4*>(in + cut.head);
+  const RowWords<T> words(in + cut.head, cut.words);
+  const int32_t shift = line_shift(out + cut.head);
+  const int32_t at0 = 16 * (tid - shift);
+  constexpr uint32_t kNegInfRaw = sizeof(T) == 2 ? Elem<T>::kNegInfWord & 0xffffu : Elem<T>::kNegInfWord;
+  uint32_t edge_raw = kNegInfRaw, label_raw = 0;
+  if (tid < cut.edge) edge_raw = load_raw(in + cut.edge_column(tid));
+  if constexpr (kKind == kLossPolicy) label_raw = load_raw(in + label);
   Word4 x[kWords];
 #pragma unroll
-  for (int k = 0; k < kWords; ++k) {
-    const int32_t w = k * kThreads + tid;
-    x[k] = Word4{Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord};
-    if (w < cut.words) x[k] = load_word(body + w);
-  }
-  float edge[1] = {kNegInf};
-  if (tid < cut.edge) edge[0] = Elem<T>::load(in + cut.edge_column(tid));
-  float z_label = 0.0f;
-  if constexpr (kKind == kLossPolicy) z_label = Elem<T>::load(in + label);
+  for (int k = 0; k < kWords; ++k) x[k] = words.load(at0 + k * kStep);
+#pragma unroll
+  for (int k = 0; k < kLds; ++k)
+    words.load_to_lds(s_row + k * kThreads + __builtin_amdgcn_readfirstlane(tid & ~63), at0 + (kWords + k) * kStep);
+
+  float z_teacher[kMine];
   if constexpr (kKind == kLossDistill) {
-    if (tid < 64) list_targets<T, kThreads, kWords>(s_list, a, row, in, nullptr, cut, r.vocab, 0, cut.words, true);
+    if (tid < 64)
+      list_targets<T, kThreads, kHeld>(s_list, raw, z_teacher, a, row, in, nullptr, cut, r.vocab, 0, cut.words,
+                                        shift, true);
   }
 
   const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
-  Stat st;
+  const Word4 nothing = {Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord};
+  FastStat fast;
 #pragma unroll
   for (int k = 0; k < kWords; k += kJoinWords) {
+    if ((k == 0 && shift > 0) || (k + kJoinWords) * kThreads > cut.words + shift) {
+      // words out of the row came as zeros
+#pragma unroll
+      for (int j = 0; j < kJoinWords; ++j)
+        if (static_cast<uint32_t>(at0 + (k + j) * kStep) >= static_cast<uint32_t>(words.bytes)) x[k + j] = nothing;
+    }
     float f[kJoinWords * kPer];
 #pragma unroll
     for (int j = 0; j < kJoinWords; ++j) {
@@ -73,97 +99,249 @@ __global__ __launch_bounds__(kThreads, 4) void row_loss_kernel(LogitRows r, Loss
 #pragma unroll
       for (int e = 0; e < kPer; ++e) f[j * kPer + e] = one[e];
     }
-    absorb(st, f, scale);
+    absorb(fast, f, scale);
   }
-  for (int32_t w = kWords * kThreads + tid; w < cut.words; w += kThreads) {
-    float f[kPer];
-    Elem<T>::unpack(body[w], f);
-    absorb(st, f, scale);
+  if constexpr (kLds > 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the words on their way to LDS
+#pragma unroll
+    for (int k = 0; k < kLds; ++k) {
+      float f[kPer];
+      Elem<T>::unpack(at0 + (kWords + k) * kStep < words.bytes ? s_row[k * kThreads + tid] : nothing, f);
+      absorb(fast, f, scale);
+    }
   }
-  absorb(st, edge, scale);
-  st = join_block<kThreads>(st, scale, s_red);
+  for (int32_t b = at0 + kHeld * kStep; b < words.bytes; b += kRestWords * kStep) {
+    Word4 y[kRestWords];
+#pragma unroll
+    for (int j = 0; j < kRestWords; ++j) y[j] = words.load(b + j * kStep);
+#pragma unroll
+    for (int j = 0; j < kRestWords; ++j) {
+      float f[kPer];
+      Elem<T>::unpack(b + j * kStep < words.bytes ? y[j] : nothing, f);
+      absorb(fast, f, scale);
+    }
+  }
+  const float edge[1] = {decode<T>(edge_raw)};
+  const float z_label = decode<T>(label_raw);
+  absorb(fast, edge, scale);
+  if constexpr (kKind == kLossDistill) {
+    if (tid < 64) store_logits(s_list.z, z_teacher, a.k);
+  }
+  fast = join_block<kThreads>(fast, scale, s_red);
   // The words are unpacked a second time below.  Without this the compiler
   // keeps the 32-bit values of the first time instead: for 16-bit elements
   // twice the registers there are, spilled to memory.
 #pragma unroll
   for (int k = 0; k < kWords; ++k) asm volatile("" : "+v"(x[k]));
 
+  // a row beyond the fast form: its sum, and below its gradient, are taken
+  // element by element from memory
+  const bool huge = !(fabsf(fast.top) < kHuge);
+  Stat st;
+  if (huge) st = row_stat<T, kThreads>(in, r.vocab, scale, s_red);
+  const float sum = huge ? st.s : fast.s;
+  const float ln_s = logf(sum);
   const float base = base_of(st.m);
-  float coef, amount;  // of q, and of the targets
+  // scale times the distance from the maximum
+  const auto exponent = [&](float z) { return huge ? (z - base) * scale : fmaf(z, scale, -fast.top); };
+  float amount;  // factor of the targets
+  int32_t state = kRowLive;
   if constexpr (kKind == kLossPolicy) {
-    const float logp = (z_label - st.m) - logf(st.s);
-    const PolicyRow p = policy_row(a, row, logp);
+    const float logp = exponent(z_label) * kLn2 - ln_s;
+    const PolicyRow p = policy_row(a, value, logp);
     if (tid == 0) {
       a.loss[row] = p.loss;
       a.logp[row] = logp;
     }
     amount = -p.dlogp;
   } else {
-    if (s_list.state != kRowLive) {
-      const bool bad = s_list.state == kRowBad;
-      fill_words<T>(out, r.vocab, bad ? Elem<T>::kNanWord : 0u, 0, INT32_MAX, true, kThreads);
-      if (tid == 0) {
-        a.loss[row] = bad ? __builtin_nanf("") : 0.0f;
-        if (bad && a.status) *a.status = THD_ERR_LABEL;
-      }
-      return;
-    }
-    const float w = a.weights ? a.weights[row] : 1.0f;
-    if (tid < 64) {
-      const float loss = distill_loss(s_list, a, w, st.m, logf(st.s));
+    state = __builtin_amdgcn_readfirstlane(s_list.state);
+    if (tid < 64 && state == kRowLive) {
+      const float loss = distill_loss(s_list, a, value.weight, exponent, ln_s);
       if (tid == 0) a.loss[row] = loss;
     }
-    amount = a.temperature * w;
+    amount = a.temperature * value.weight;
   }
-  coef = amount / st.s;
+  const float coef = amount / sum;  // factor of the exponentials
+  // in a row beyond the fast form no word is stored from the registers
+  const RowWords<T> to(out + cut.head, huge ? 0 : cut.words);
 
-  const OutRow<T> dst(out, in, cut.head);
-  const int32_t label_word = kKind == kLossPolicy ? cut.word_of(static_cast<int32_t>(label)) : -1;
-  const int32_t label_place = kKind == kLossPolicy ? cut.place_of(static_cast<int32_t>(label)) : 0;
   uint32_t hit = 0;
   if constexpr (kKind == kLossDistill) hit = s_list.hit[tid];
-
-  auto gradient = [&](Word4 word, int32_t w, int bit) {
+  int32_t label_turn = -1, label_thread = -1, label_place = 0;
+  if constexpr (kKind == kLossPolicy) {
+    const int32_t w = cut.word_of(label);
+    if (w >= 0) {
+      label_turn = (w + shift) / kThreads;
+      label_thread = (w + shift) % kThreads;
+      label_place = cut.place_of(label);
+    }
+  }
+  const auto gradient = [&](Word4 word, int32_t b, int32_t k, int bit) {
     float f[kPer], g[kPer];
     Elem<T>::unpack(word, f);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) g[e] = coef * exp2_fast((f[e] - base) * scale);
+    for (int e = 0; e < kPer; ++e) g[e] = coef * exp2_fast(fmaf(f[e], scale, -fast.top));
     if constexpr (kKind == kLossPolicy) {
-      if (w == label_word) {
+      if (k == label_turn && tid == label_thread) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
           if (e == label_place) g[e] -= amount;
       }
     } else {
-      if ((hit >> bit) & 1u) take_targets<T, kThreads>(s_list, cut, w, amount, g);
+      if ((hit >> bit) & 1u) take_targets<T, kThreads>(s_list, cut, b / 16, amount, g);
     }
-    dst.store(w, g);
+    to.store(b, Elem<T>::pack(g));
   };
+
+  // the barriers keep each word's values in its own step: the scheduler would
+  // gather them, and spill
+  int32_t here = at0;
+  asm volatile("" : "+v"(here));
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {
-    const int32_t w = k * kThreads + tid;
-    if (w < cut.words) gradient(x[k], w, k);
+    gradient(x[k], here, k, k);
+    here += kStep;
+    __builtin_amdgcn_sched_barrier(0);
   }
-  for (int32_t w = kWords * kThreads + tid; w < cut.words; w += kThreads) gradient(body[w], w, kRestBit);
-  if (tid < cut.edge) {
-    float g = coef * exp2_fast((edge[0] - base) * scale);
+#pragma unroll
+  for (int k = kWords; k < kHeld; ++k) {
+    gradient(s_row[(k - kWords) * kThreads + tid], here, k, k);
+    here += kStep;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int32_t b = at0 + kHeld * kStep, k = kHeld; b < words.bytes; b += kRestWords * kStep, k += kRestWords) {
+    Word4 y[kRestWords];
+#pragma unroll
+    for (int j = 0; j < kRestWords; ++j) y[j] = words.load(b + j * kStep);
+#pragma unroll
+    for (int j = 0; j < kRestWords; ++j) gradient(y[j], b + j * kStep, k + j, kRestBit);
+  }
+  if (tid < cut.edge && !huge) {
+    const int32_t v = cut.edge_column(tid);
+    float g = coef * exp2_fast(fmaf(edge[0], scale, -fast.top));
     if constexpr (kKind == kLossPolicy) {
-      if (cut.edge_column(tid) == label) g -= amount;
+      if (v == label) g -= amount;
     } else {
       if ((hit >> kEdgeBit) & 1u) g = take_edge_target<T, kThreads>(s_list, cut, amount, g);
     }
-    out[cut.edge_column(tid)] = Elem<T>::round(g);
+    out[v] = Elem<T>::round(g);
+  }
+  if (huge && state == kRowLive) {
+    for (int32_t v = tid; v < r.vocab; v += kThreads) {
+      float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
+      if (kKind == kLossPolicy && v == label) g -= amount;
+      out[v] = Elem<T>::round(g);
+    }
+    if constexpr (kKind == kLossDistill) {
+      __syncthreads();  // a target's element is stored again, after the first time
+      put_targets<T, kThreads>(s_list, out, coef, base, scale, amount);
+    }
+  }
+  if (kKind == kLossDistill && state != kRowLive) {
+    __syncthreads();  // over what was just stored
+    fill_row(state == kRowBad);
   }
 }
 
-// Launches in slices whose threads a grid can count (2^32).
-template <typename T, int kThreads, int kWords, LossKind kKind>
+// The same for a gradient whose rows lie at another place within 16 bytes than
+// the logits' rows: the row is read twice and the gradient stored element by
+// element.
+template <typename T, LossKind kKind>
+__global__ __launch_bounds__(256) void row_loss_apart_kernel(LogitRows r, LossArgs a) {
+  constexpr int kThreads = 256;
+  struct NoList {
+    int32_t state;
+  };
+  using List = typename std::conditional<kKind == kLossDistill, TargetList<kThreads>, NoList>::type;
+  __shared__ float2 s_red[kThreads / 64];
+  __shared__ List s_list;
+  const int32_t tid = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < r.rows; row += gridDim.x) {
+    const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
+    T* out = static_cast<T*>(r.out) + row * r.out_stride;
+    const bool live = !a.mask || a.mask[row] != 0;
+    int32_t state = live ? kRowLive : kRowEmpty;
+    int64_t label = 0;
+    if constexpr (kKind == kLossPolicy) {
+      label = a.labels[row];
+      if (live && (label < 0 || label >= r.vocab)) state = kRowBad;
+    } else {
+      if (live && tid < 64) {
+        TeacherRaw raw;
+        float z[kMine];
+        const RowCut<T> cut(in, r.vocab);
+        read_teacher(raw, a, row);
+        list_targets<T, kThreads, kRestBit>(s_list, raw, z, a, row, in, nullptr, cut, r.vocab, 0, cut.words, 0, true);
+        store_logits(s_list.z, z, a.k);
+      }
+      __syncthreads();
+      if (live) state = __builtin_amdgcn_readfirstlane(s_list.state);
+    }
+    if (state != kRowLive) {
+      fill_words<T>(out, r.vocab, state == kRowBad ? Elem<T>::kNanWord : 0u, 0, INT32_MAX, true, kThreads);
+      if (tid == 0) {
+        const float v = state == kRowBad ? __builtin_nanf("") : 0.0f;
+        a.loss[row] = v;
+        if (kKind == kLossPolicy) a.logp[row] = v;
+        if (state == kRowBad && a.status) *a.status = THD_ERR_LABEL;
+      }
+    } else {
+      const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
+      Stat st;
+      for (int32_t v = tid; v < r.vocab; v += kThreads) {
+        const float f[1] = {Elem<T>::load(in + v)};
+        absorb(st, f, scale);
+      }
+      st = join_block<kThreads>(st, scale, s_red);
+      const float base = base_of(st.m);
+      float amount;
+      if constexpr (kKind == kLossPolicy) {
+        const float logp = (Elem<T>::load(in + label) - st.m) - logf(st.s);
+        const PolicyRow p = policy_row(a, policy_values(a, row), logp);
+        if (tid == 0) {
+          a.loss[row] = p.loss;
+          a.logp[row] = logp;
+        }
+        amount = -p.dlogp;
+      } else {
+        const float w = a.weights ? a.weights[row] : 1.0f;
+        if (tid < 64) {
+          const float loss = distill_loss(s_list, a, w, [&](float z) { return (z - st.m) * scale; }, logf(st.s));
+          if (tid == 0) a.loss[row] = loss;
+        }
+        amount = a.temperature * w;
+      }
+      const float coef = amount / st.s;
+      for (int32_t v = tid; v < r.vocab; v += kThreads) {
+        float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
+        if (kKind == kLossPolicy && v == label) g -= amount;
+        out[v] = Elem<T>::round(g);
+      }
+      if constexpr (kKind == kLossDistill) {
+        __syncthreads();  // a target's element is stored again, after the first time
+        put_targets<T, kThreads>(s_list, out, coef, base, scale, amount);
+      }
+    }
+    __syncthreads();  // the next row reuses what is shared
+  }
+}
+
+// Rows per chunk of an XCD's order: about 1 MiB, and at least 16 rows.
+inline int32_t row_chunk_shift(const LogitRows& r) {
+  const int64_t bytes = static_cast<int64_t>(r.vocab) * (r.dtype == THD_FP32 ? 4 : 2);
+  int32_t shift = 4;
+  while (shift < 8 && (bytes << (shift + 1)) <= (1 << 20)) ++shift;
+  return shift;
+}
+
+template <typename T, int kThreads, int kWords, int kLds, LossKind kKind>
 hipError_t launch_rows_as(const LogitRows& r, const LossArgs& a, hipStream_t stream) {
-  constexpr int32_t kSlice = static_cast<int32_t>((1LL << 31) / kThreads);
+  constexpr int32_t kSlice = static_cast<int32_t>((1LL << 31) / kThreads);  // a grid counts 2^32 threads
   for (int64_t row0 = 0; row0 < r.rows; row0 += kSlice) {
     const int32_t n = static_cast<int32_t>(r.rows - row0 < kSlice ? r.rows - row0 : kSlice);
-    hipLaunchKernelGGL((row_loss_kernel<T, kThreads, kWords, kKind>), dim3(n), dim3(kThreads), 0, stream, r, a,
-                       static_cast<int32_t>(row0));
+    hipLaunchKernelGGL((row_loss_kernel<T, kThreads, kWords, kLds, kKind>), dim3(n), dim3(kThreads),
+                       kLds * kThreads * sizeof(Word4), stream, r, a, static_cast<int32_t>(row0), row_chunk_shift(r));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -172,14 +350,26 @@ hipError_t launch_rows_as(const LogitRows& r, const LossArgs& a, hipStream_t str
 
 template <typename T, LossKind kKind>
 hipError_t launch_rows(const LogitRows& r, const LossArgs& a, hipStream_t stream) {
-  const int32_t words = r.vocab / Elem<T>::kPer;
-  if (words <= 256) return launch_rows_as<T, 64, 4, kKind>(r, a, stream);
-  if (words <= 1024) return launch_rows_as<T, 128, 8, kKind>(r, a, stream);
-  if (words <= 2048) return launch_rows_as<T, 256, 8, kKind>(r, a, stream);
-  if (words <= 4096) return launch_rows_as<T, 256, 16, kKind>(r, a, stream);
-  if (words <= 8192) return launch_rows_as<T, 512, 16, kKind>(r, a, stream);
-  if (words <= 16384) return launch_rows_as<T, 1024, 16, kKind>(r, a, stream);
-  return launch_rows_as<T, 1024, 20, kKind>(r, a, stream);
+  const int64_t lag = reinterpret_cast<intptr_t>(r.out) - reinterpret_cast<intptr_t>(r.in);
+  const int64_t pitch = r.rows > 1 ? r.out_stride * static_cast<int64_t>(sizeof(T)) : 0;
+  const int64_t drift = r.rows > 1 ? pitch - r.in_stride * static_cast<int64_t>(sizeof(T)) : 0;
+  if (lag % 16 != 0 || drift % 16 != 0) {
+    const int32_t resident = compute_units() * 8;
+    hipLaunchKernelGGL((row_loss_apart_kernel<T, kKind>), dim3(r.rows < resident ? r.rows : resident), dim3(256), 0,
+                       stream, r, a);
+    return hipGetLastError();
+  }
+  // rows that do not all start on a 128-byte line are shifted by up to 7 words
+  const bool lines = reinterpret_cast<uintptr_t>(r.out) % 128 == 0 && pitch % 128 == 0;
+  const int32_t words = r.vocab / Elem<T>::kPer + (lines ? 0 : 7);
+  if (words <= 64 * 4) return launch_rows_as<T, 64, 4, 0, kKind>(r, a, stream);
+  if (words <= 128 * 8) return launch_rows_as<T, 128, 8, 0, kKind>(r, a, stream);
+  if (words <= 256 * 8) return launch_rows_as<T, 256, 8, 0, kKind>(r, a, stream);
+  if (words <= 512 * 8) return launch_rows_as<T, 512, 8, 0, kKind>(r, a, stream);
+  if (words <= 1024 * 8) return launch_rows_as<T, 1024, 8, 0, kKind>(r, a, stream);
+  if (words <= 1024 * 12) return launch_rows_as<T, 1024, 8, 4, kKind>(r, a, stream);
+  if (words <= 1024 * 16) return launch_rows_as<T, 1024, 16, 0, kKind>(r, a, stream);
+  return launch_rows_as<T, 1024, 18, 8, kKind>(r, a, stream);
 }
 
 template <LossKind kKind>

@@ -55,7 +55,7 @@ extern "C" {
 #define THD_FP32 2
 
 /* ---- limits -------------------------------------------------------------- */
-#define THD_MAX_VOCAB 1073741824    /* 2^30 columns */
+#define THD_MAX_VOCAB 268435456     /* 2^28 columns: a row of 1 GiB in 32 bits */
 #define THD_MAX_TOPK  256           /* teacher columns per row */
 #define THD_MAX_PAIRS 65536         /* document pairs per call */
 
