@@ -9,7 +9,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 16 * kThreads;  // bytes from one of a thread's words to the next
-constexpr int kStatsAhead = 8;        // words a thread has in flight
 constexpr int kGradAhead = 2;
 constexpr int kBackwardTurns = 2;
 constexpr int kBackwardChunkShift = 4;
@@ -22,8 +21,8 @@ __global__ void status_init_kernel(int32_t* status) { *status = THD_OK; }
 struct PartOf {
   int64_t row;
   int32_t part;
-  __device__ __forceinline__ PartOf(const LossParts& p, int32_t row0) {
-    const int32_t tile = tile_of(blockIdx.x, gridDim.x, p.chunk_shift);
+  __device__ __forceinline__ PartOf(const LossParts& p, int32_t row0, int32_t tiles) {
+    const int32_t tile = tile_of(blockIdx.x, tiles, p.chunk_shift);
     row = row0 + static_cast<int64_t>(tile / p.parts);
     part = tile % p.parts;
   }
@@ -32,12 +31,15 @@ struct PartOf {
 // Maximum and sum of a row's part.  With one part the row's log-probability
 // and log-sum-exp are written, else the part's pair; part 0 also saves the
 // logits of the row's targets, which the second pass may overwrite.
-template <typename T, LossKind kKind>
+template <typename T, LossKind kKind, int kThreads>
 __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossArgs a, LossParts p, int32_t row0) {
   constexpr int kPer = Elem<T>::kPer;
+  constexpr int kStep = 16 * kThreads;
+  constexpr int kStatsAhead = kThreads == 256 ? 8 : 4;  // words a thread has in flight
   __shared__ float2 s_red[kThreads / 64];
   const int32_t tid = threadIdx.x;
-  const auto [row, part] = PartOf(p, row0);
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status<kThreads>(a, r.rows, r.vocab);
+  const auto [row, part] = PartOf(p, row0, gridDim.x - a.scan);
   const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
   // in the two-pass form only the second pass reports errors
   if (a.status && p.parts > 1 && blockIdx.x == 0 && row0 == 0 && tid == 0) *a.status = THD_OK;
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
     if (label < 0 || label >= r.vocab) {
       if (kKind == kLossLogp && p.parts == 1 && tid == 0) {
         a.logp[row] = a.lse[row] = __builtin_nanf("");
-        if (a.status) *a.status = THD_ERR_LABEL;
+        if (a.status && !a.scan) *a.status = THD_ERR_LABEL;
       }
       return;
     }
@@ -160,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
   using List = typename std::conditional<kKind == kLossDistill, TargetList<kThreads>, NoList>::type;
   __shared__ List s_list;
   const int32_t tid = threadIdx.x;
-  const auto [row, part] = PartOf(p, row0);
+  const auto [row, part] = PartOf(p, row0, gridDim.x);
   const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
   T* out = static_cast<T*>(r.out) + row * r.out_stride;
 
@@ -307,6 +309,14 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
 
 int32_t words_of(int32_t vocab, int32_t dtype) { return vocab / (dtype == THD_FP32 ? 4 : 8); }
 
+// Rows that 1024 threads each read faster than 256 do: where a compute unit has
+// few (256 rows of 65536 bf16 8.4 us against 9.7; 32768 rows of 32000 columns
+// 359 us against 275).
+constexpr int kWideThreads = 1024;
+bool wide_rows(int32_t rows, int32_t vocab, int32_t dtype) {
+  return words_of(vocab, dtype) > 2048 && rows <= 2 * compute_units();
+}
+
 // About `want` parts a row: the turns of a part, and the parts that cover a
 // row whose first word lies anywhere in its 128-byte line.
 LossParts cut_row(int64_t want, int32_t vocab, int32_t dtype) {
@@ -345,8 +355,21 @@ template <LossKind kKind>
 hipError_t launch_stats(const LogitRows& r, const LossArgs& a, const LossParts& p, hipStream_t stream) {
   return by_dtype(r.dtype, [&](auto t) {
     using T = decltype(t);
+    if constexpr (kKind == kLossLogp) {
+      if (p.parts == 1 && wide_rows(r.rows, r.vocab, r.dtype)) {
+        LossParts whole = p;
+        whole.turns = (words_of(r.vocab, r.dtype) + 7) / kWideThreads + 1;
+        return over_rows(r.rows, kWideThreads / kThreads, [&](dim3, int32_t row0) {
+          const int32_t slice = static_cast<int32_t>((1LL << 31) / kWideThreads);
+          const int32_t n = r.rows - row0 < slice ? r.rows - row0 : slice;
+          hipLaunchKernelGGL((row_stats_kernel<T, kKind, kWideThreads>), dim3(n + a.scan), dim3(kWideThreads), 0,
+                             stream, r, a, whole, row0);
+        });
+      }
+    }
     return over_rows(r.rows, p.parts, [&](dim3 grid, int32_t row0) {
-      hipLaunchKernelGGL((row_stats_kernel<T, kKind>), grid, dim3(kThreads), 0, stream, r, a, p, row0);
+      hipLaunchKernelGGL((row_stats_kernel<T, kKind, kThreads>), dim3(grid.x + a.scan), dim3(kThreads), 0,
+                         stream, r, a, p, row0);
     });
   });
 }
@@ -377,12 +400,18 @@ int32_t compute_units() {
   return n;
 }
 
+// Two launches take about 2 us more than one, which they gain back where a row
+// is long and the rows are few (bf16, us per call, two launches against one):
+// log-probabilities of 65536 columns 5.5 / 5.9 for one row, 8.2 / 7.1 for 64;
+// of 131072 columns 5.5 / 8.8, 9.5 / 11.0 for 64, 13.8 / 11.5 for 128; the
+// policy loss of 32000 columns 6.8 / 6.4, of 50000 6.6 / 8.0, 8.0 / 8.6 for 32
+// and 9.4 / 8.7 for 64, of 131072 6.7 / 13.9, 9.9 / 14.4 and 15.6 / 14.5.
 LossParts logp_parts(int32_t rows, int32_t vocab, int32_t dtype) {
-  return cut_row(rows < 1 ? 1 : 1024 / rows, vocab, dtype);
+  return cut_row(rows < 1 || rows > 64 || words_of(vocab, dtype) <= 8192 ? 1 : 1024 / rows, vocab, dtype);
 }
 
 LossParts loss_parts(int32_t rows, int32_t vocab, int32_t dtype) {
-  return cut_row(rows < 1 ? 1 : 512 / rows, vocab, dtype);
+  return cut_row(rows < 1 || rows > 48 || words_of(vocab, dtype) <= 4096 ? 1 : 512 / rows, vocab, dtype);
 }
 
 hipError_t launch_status_init(int32_t* status, hipStream_t stream) {

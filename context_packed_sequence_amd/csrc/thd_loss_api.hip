@@ -80,8 +80,15 @@ hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 int launched(hipError_t e) { return e == hipSuccess ? THD_OK : THD_ERR_HIP; }
 
-// The one-workgroup-per-row kernels report into a status word that is THD_OK
-// before them.
+// The one-pass kernels' status word: written by a workgroup of the launch that
+// looks through all targets where they are few, else set to THD_OK by a launch
+// before and by the rows that fail.
+int prepare_status(thdcp::LossArgs& a, int64_t targets, void* stream) {
+  if (!a.status) return THD_OK;
+  a.scan = targets <= thdcp::kScanTargets;
+  return a.scan ? THD_OK : launched(thdcp::launch_status_init(a.status, as_stream(stream)));
+}
+
 int init_status(int32_t* status, void* stream) {
   return status ? launched(thdcp::launch_status_init(status, as_stream(stream))) : THD_OK;
 }
@@ -115,7 +122,7 @@ int thd_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t 
   a.lse = lse;
   a.status = status;
   if (l.parts.parts == 1) {
-    const int rc = init_status(status, stream);
+    const int rc = prepare_status(a, rows, stream);
     if (rc != THD_OK) return rc;
   }
   return launched(thdcp::launch_token_logprobs(r, a, l.parts, as_stream(stream)));
@@ -191,7 +198,7 @@ int thd_policy_loss(const void* logits, int32_t dtype, int64_t rows, int64_t voc
   a.loss = loss;
   a.status = status;
   if (l.parts.parts > 1) return launched(thdcp::launch_policy_parts(r, a, l.parts, as_stream(stream)));
-  const int rc = init_status(status, stream);
+  const int rc = prepare_status(a, rows, stream);
   if (rc != THD_OK) return rc;
   return launched(thdcp::launch_policy_rows(r, a, as_stream(stream)));
 }
@@ -241,7 +248,7 @@ int thd_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vo
   a.loss = loss;
   a.status = status;
   if (l.parts.parts > 1) return launched(thdcp::launch_distill_parts(r, a, l.parts, as_stream(stream)));
-  const int rc = init_status(status, stream);
+  const int rc = prepare_status(a, rows * k, stream);
   if (rc != THD_OK) return rc;
   return launched(thdcp::launch_distill_rows(r, a, as_stream(stream)));
 }

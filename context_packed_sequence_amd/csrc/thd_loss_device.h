@@ -371,6 +371,44 @@ __device__ __forceinline__ Stat row_stat(const T* in, int32_t vocab, float scale
   return join_block<kThreads>(st, scale, s_red);
 }
 
+// The status word from a look at every row's targets (labels, or the teacher's
+// columns), by one workgroup beside the rows': a launch that would set the word
+// first costs more wherever the targets are few.
+template <int kThreads>
+__device__ __forceinline__ void scan_status(const LossArgs& a, int32_t rows, int32_t vocab) {
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  bool bad = false;
+  constexpr int kEach = 8;  // loads in flight
+  const int32_t n = a.k == 0 ? rows : rows * a.k;
+  for (int32_t i0 = threadIdx.x; i0 < n; i0 += kEach * kThreads) {
+    int64_t v[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int32_t i = i0 + j * kThreads;
+      v[j] = 0;
+      if (i >= n) continue;
+      if (a.k == 0) {
+        v[j] = a.labels[i];
+      } else {
+        const int64_t at = a.teacher_stride == a.k ? i : i / a.k * a.teacher_stride + i % a.k;
+        v[j] = a.ids64 ? static_cast<const int64_t*>(a.teacher_ids)[at]
+                       : static_cast<const int32_t*>(a.teacher_ids)[at];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      if (v[j] >= (a.k == 0 ? 0 : -1) && v[j] < vocab) continue;
+      const int32_t t = (i0 + j * kThreads) / (a.k == 0 ? 1 : a.k);
+      bad |= !a.mask || a.mask[t] != 0;
+    }
+  }
+  if (bad) s_bad = 1;
+  __syncthreads();
+  if (threadIdx.x == 0) *a.status = s_bad ? THD_ERR_LABEL : THD_OK;
+}
+
 // ---- row values of the policy loss ----------------------------------------
 // r = exp(logp - old), u = ref - logp:
 //   L = w ( -min(r A, clip(r, low, high) A) + beta (exp(u) - u - 1) )

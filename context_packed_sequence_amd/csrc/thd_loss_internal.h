@@ -53,7 +53,12 @@ struct LossArgs {
   // outputs
   float* loss;               // [rows]
   int32_t* status;           // or null
+  int32_t scan;              // 1: a workgroup of its own writes it (scan_status)
 };
+
+// Targets a call may have for one workgroup to look through them all: 64
+// threads take about 10 us for as many, beside rows that take as long.
+constexpr int64_t kScanTargets = 8192;
 
 // Row parts of the two-pass form: every part's running maximum and sum, then
 // the logits of the row's targets (its label, or the teacher's columns).

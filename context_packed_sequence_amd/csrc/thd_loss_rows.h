@@ -29,7 +29,8 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   __shared__ List s_list;
   extern __shared__ Word4 s_row[];  // [kLds][kThreads], each word used by its own thread alone
   const int32_t tid = threadIdx.x;
-  const int64_t row = row0 + static_cast<int64_t>(tile_of(blockIdx.x, gridDim.x, chunk_shift));
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status<kThreads>(a, r.rows, r.vocab);
+  const int64_t row = row0 + static_cast<int64_t>(tile_of(blockIdx.x, gridDim.x - a.scan, chunk_shift));
   const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
   T* out = static_cast<T*>(r.out) + row * r.out_stride;
   const auto fill_row = [&](bool bad) {
@@ -38,7 +39,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
       const float v = bad ? __builtin_nanf("") : 0.0f;
       a.loss[row] = v;
       if (kKind == kLossPolicy) a.logp[row] = v;
-      if (bad && a.status) *a.status = THD_ERR_LABEL;
+      if (bad && a.status && !a.scan) *a.status = THD_ERR_LABEL;
     }
   };
 
@@ -62,6 +63,9 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   const RowWords<T> words(in + cut.head, cut.words);
   const int32_t shift = line_shift(out + cut.head);
   const int32_t at0 = 16 * (tid - shift);
+  // turns in which this wave has a word of the row
+  const int32_t wave0 = __builtin_amdgcn_readfirstlane(tid & ~63);
+  const int32_t turns = (cut.words + shift - wave0 + kThreads - 1) / kThreads;
   constexpr uint32_t kNegInfRaw = sizeof(T) == 2 ? Elem<T>::kNegInfWord & 0xffffu : Elem<T>::kNegInfWord;
   uint32_t edge_raw = kNegInfRaw, label_raw = 0;
   if (tid < cut.edge) edge_raw = load_raw(in + cut.edge_column(tid));
@@ -71,7 +75,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   for (int k = 0; k < kWords; ++k) x[k] = words.load(at0 + k * kStep);
 #pragma unroll
   for (int k = 0; k < kLds; ++k)
-    words.load_to_lds(s_row + k * kThreads + __builtin_amdgcn_readfirstlane(tid & ~63), at0 + (kWords + k) * kStep);
+    words.load_to_lds(s_row + k * kThreads + wave0, at0 + (kWords + k) * kStep);
 
   float z_teacher[kMine];
   if constexpr (kKind == kLossDistill) {
@@ -85,6 +89,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   FastStat fast;
 #pragma unroll
   for (int k = 0; k < kWords; k += kJoinWords) {
+    if (k >= turns) continue;
     if ((k == 0 && shift > 0) || (k + kJoinWords) * kThreads > cut.words + shift) {
       // words out of the row came as zeros
 #pragma unroll
@@ -105,6 +110,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the words on their way to LDS
 #pragma unroll
     for (int k = 0; k < kLds; ++k) {
+      if (kWords + k >= turns) continue;
       float f[kPer];
       Elem<T>::unpack(at0 + (kWords + k) * kStep < words.bytes ? s_row[k * kThreads + tid] : nothing, f);
       absorb(fast, f, scale);
@@ -200,12 +206,14 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   asm volatile("" : "+v"(here));
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {
+    if (k >= turns) continue;
     gradient(x[k], here, k, k);
     here += kStep;
     __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
   for (int k = kWords; k < kHeld; ++k) {
+    if (k >= turns) continue;
     gradient(s_row[(k - kWords) * kThreads + tid], here, k, k);
     here += kStep;
     __builtin_amdgcn_sched_barrier(0);
@@ -257,7 +265,8 @@ __global__ __launch_bounds__(256) void row_loss_apart_kernel(LogitRows r, LossAr
   __shared__ float2 s_red[kThreads / 64];
   __shared__ List s_list;
   const int32_t tid = threadIdx.x;
-  for (int64_t row = blockIdx.x; row < r.rows; row += gridDim.x) {
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status<kThreads>(a, r.rows, r.vocab);
+  for (int64_t row = blockIdx.x; row < r.rows; row += gridDim.x - a.scan) {
     const T* in = static_cast<const T*>(r.in) + row * r.in_stride;
     T* out = static_cast<T*>(r.out) + row * r.out_stride;
     const bool live = !a.mask || a.mask[row] != 0;
@@ -284,7 +293,7 @@ __global__ __launch_bounds__(256) void row_loss_apart_kernel(LogitRows r, LossAr
         const float v = state == kRowBad ? __builtin_nanf("") : 0.0f;
         a.loss[row] = v;
         if (kKind == kLossPolicy) a.logp[row] = v;
-        if (state == kRowBad && a.status) *a.status = THD_ERR_LABEL;
+        if (state == kRowBad && a.status && !a.scan) *a.status = THD_ERR_LABEL;
       }
     } else {
       const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
@@ -340,7 +349,7 @@ hipError_t launch_rows_as(const LogitRows& r, const LossArgs& a, hipStream_t str
   constexpr int32_t kSlice = static_cast<int32_t>((1LL << 31) / kThreads);  // a grid counts 2^32 threads
   for (int64_t row0 = 0; row0 < r.rows; row0 += kSlice) {
     const int32_t n = static_cast<int32_t>(r.rows - row0 < kSlice ? r.rows - row0 : kSlice);
-    hipLaunchKernelGGL((row_loss_kernel<T, kThreads, kWords, kLds, kKind>), dim3(n), dim3(kThreads),
+    hipLaunchKernelGGL((row_loss_kernel<T, kThreads, kWords, kLds, kKind>), dim3(n + a.scan), dim3(kThreads),
                        kLds * kThreads * sizeof(Word4), stream, r, a, static_cast<int32_t>(row0), row_chunk_shift(r));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -355,17 +364,18 @@ hipError_t launch_rows(const LogitRows& r, const LossArgs& a, hipStream_t stream
   const int64_t drift = r.rows > 1 ? pitch - r.in_stride * static_cast<int64_t>(sizeof(T)) : 0;
   if (lag % 16 != 0 || drift % 16 != 0) {
     const int32_t resident = compute_units() * 8;
-    hipLaunchKernelGGL((row_loss_apart_kernel<T, kKind>), dim3(r.rows < resident ? r.rows : resident), dim3(256), 0,
-                       stream, r, a);
+    hipLaunchKernelGGL((row_loss_apart_kernel<T, kKind>), dim3((r.rows < resident ? r.rows : resident) + a.scan),
+                       dim3(256), 0, stream, r, a);
     return hipGetLastError();
   }
   // rows that do not all start on a 128-byte line are shifted by up to 7 words
   const bool lines = reinterpret_cast<uintptr_t>(r.out) % 128 == 0 && pitch % 128 == 0;
   const int32_t words = r.vocab / Elem<T>::kPer + (lines ? 0 : 7);
   if (words <= 64 * 4) return launch_rows_as<T, 64, 4, 0, kKind>(r, a, stream);
-  if (words <= 128 * 8) return launch_rows_as<T, 128, 8, 0, kKind>(r, a, stream);
-  if (words <= 256 * 8) return launch_rows_as<T, 256, 8, 0, kKind>(r, a, stream);
-  if (words <= 512 * 8) return launch_rows_as<T, 512, 8, 0, kKind>(r, a, stream);
+  if (words <= 128 * 4) return launch_rows_as<T, 128, 4, 0, kKind>(r, a, stream);
+  if (words <= 256 * 4) return launch_rows_as<T, 256, 4, 0, kKind>(r, a, stream);
+  if (words <= 512 * 4) return launch_rows_as<T, 512, 4, 0, kKind>(r, a, stream);
+  if (words <= 1024 * 4) return launch_rows_as<T, 1024, 4, 0, kKind>(r, a, stream);
   if (words <= 1024 * 8) return launch_rows_as<T, 1024, 8, 0, kKind>(r, a, stream);
   if (words <= 1024 * 12) return launch_rows_as<T, 1024, 8, 4, kKind>(r, a, stream);
   if (words <= 1024 * 16) return launch_rows_as<T, 1024, 16, 0, kKind>(r, a, stream);

@@ -24,11 +24,42 @@ namespace {
 constexpr int kTile = 512;
 constexpr int kEach = kTile / 64;  // tokens per lane
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// Sums of a wave's two halves of 32 lanes, each in every lane of its half:
+// DPP moves within 16 lanes, then one exchange of the two rows of each half.
+__device__ __forceinline__ double move_lanes(double x, int step) {
+  const int64_t bits = __builtin_bit_cast(int64_t, x);
+  switch (step) {  // 0x111, ...: row_shr by 1, 2, 4, 8; lanes without a source take 0
+    case 1: return __builtin_bit_cast(double, dpp_move<0x111, 0xf>(bits, int64_t{0}));
+    case 2: return __builtin_bit_cast(double, dpp_move<0x112, 0xf>(bits, int64_t{0}));
+    case 4: return __builtin_bit_cast(double, dpp_move<0x114, 0xf>(bits, int64_t{0}));
+    default: return __builtin_bit_cast(double, dpp_move<0x118, 0xf>(bits, int64_t{0}));
+  }
 }
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const int64_t bits = __builtin_bit_cast(int64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int32_t>(bits), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int32_t>(bits >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo));
+}
+struct HalfSums {
+  double low, high;  // of lanes 0-31 and 32-63
+};
+__device__ __forceinline__ HalfSums half_sums(double v) {
+  v += move_lanes(v, 1);
+  v += move_lanes(v, 2);
+  v += move_lanes(v, 4);
+  v += move_lanes(v, 8);
+  return HalfSums{lane_of(v, 15) + lane_of(v, 31), lane_of(v, 47) + lane_of(v, 63)};
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  const HalfSums h = half_sums(v);
+  return h.low + h.high;
+}
+
+// Boundaries and pairs that fit are read into LDS with the tile's tokens, in one
+// round trip; of longer lists each search round and each piece costs one.
+constexpr int kLdsSlots = 1023;
+constexpr int kLdsPairs = 512;
 
 // Slot that holds token t: the last one whose start is at or before it.  Each
 // round probes 64 boundaries.  Some slot is returned for any list, so that a
@@ -46,6 +77,28 @@ __device__ __forceinline__ int32_t slot_of(const int32_t* cu, int32_t n_slots, i
   }
   return lo;
 }
+
+// A list on its way to LDS, by one wave: its first 64 * N words are issued with
+// whatever else the tile reads, the rest follows.
+template <int N>
+struct Staged {
+  int32_t v[N];
+  __device__ __forceinline__ void issue(const int32_t* from, int32_t n) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int32_t i = 64 * j + static_cast<int32_t>(threadIdx.x);
+      v[j] = i < n ? from[i] : 0;
+    }
+  }
+  __device__ __forceinline__ void finish(int32_t* to, const int32_t* from, int32_t n) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int32_t i = 64 * j + static_cast<int32_t>(threadIdx.x);
+      if (i < n) to[i] = v[j];
+    }
+    for (int32_t i = 64 * N + static_cast<int32_t>(threadIdx.x); i < n; i += 64) to[i] = from[i];
+  }
+};
 
 // Calls f(slot, begin, end) for every non-empty piece of a document inside
 // tokens [t0, t1), in order; the arguments are the same in every lane.
@@ -76,12 +129,29 @@ __global__ __launch_bounds__(64) void preference_sums_kernel(PreferenceArgs a, i
       if (a.cu[0] != 0) sev = kSevStart;
       if (a.cu[a.n_slots] != a.total) sev = max(sev, kSevTotal);
     }
-    for (int32_t i = lane; i < a.n_slots; i += 64)
-      if (a.cu[i + 1] < a.cu[i]) sev = max(sev, kSevMonotone);
-    for (int32_t i = lane; i < a.n_pairs; i += 64) {
-      const int32_t c = a.pairs[2 * i], r = a.pairs[2 * i + 1];
-      const bool unused = c == -1 && r == -1;
-      if (!unused && (c < 0 || c >= a.n_slots || r < 0 || r >= a.n_slots)) bad_pair = true;
+    constexpr int kAhead = 4;  // entries in flight
+    for (int32_t i0 = lane; i0 < max(a.n_slots, a.n_pairs); i0 += 64 * kAhead) {
+      int32_t from[kAhead], to[kAhead], c[kAhead], r[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int32_t i = i0 + 64 * j;
+        from[j] = to[j] = 0;
+        c[j] = r[j] = -1;
+        if (i < a.n_slots) {
+          from[j] = a.cu[i];
+          to[j] = a.cu[i + 1];
+        }
+        if (i < a.n_pairs) {
+          c[j] = a.pairs[2 * i];
+          r[j] = a.pairs[2 * i + 1];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (to[j] < from[j]) sev = max(sev, kSevMonotone);
+        const bool unused = c[j] == -1 && r[j] == -1;
+        if (!unused && (c[j] < 0 || c[j] >= a.n_slots || r[j] < 0 || r[j] >= a.n_slots)) bad_pair = true;
+      }
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) sev = max(sev, __shfl_xor(sev, d));
@@ -93,23 +163,29 @@ __global__ __launch_bounds__(64) void preference_sums_kernel(PreferenceArgs a, i
     }
     return;
   }
+  __shared__ int32_t s_cu[kLdsSlots + 1];
   const int32_t tile = blockIdx.x;
   const int32_t t0 = tile * kTile;
   const int32_t t1 = static_cast<int32_t>(min(static_cast<int64_t>(t0) + kTile, static_cast<int64_t>(a.total)));
+  const bool in_lds = a.n_slots <= kLdsSlots;
+  Staged<4> bounds;
+  if (in_lds) bounds.issue(a.cu, a.n_slots + 1);
   float lp[kEach], rp[kEach];
   uint8_t on[kEach];
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
-    const int64_t t = static_cast<int64_t>(t0) + j * 64 + lane;
-    lp[j] = rp[j] = 0.0f;
-    on[j] = 0;
-    if (t < t1) {
-      on[j] = a.mask ? a.mask[t] : 1;
-      lp[j] = a.logp[t];
-      if (a.ref_logp) rp[j] = a.ref_logp[t];
-    }
+    const int32_t t = min(t0 + j * 64 + lane, t1 - 1);  // past the tile: a token of it again, in no piece
+    lp[j] = a.logp[t];
+    rp[j] = a.ref_logp ? a.ref_logp[t] : 0.0f;
+    on[j] = a.mask ? a.mask[t] : 1;
   }
-  each_piece(a.cu, a.n_slots, t0, t1, [&](int32_t d, int32_t begin, int32_t end) {
+  const int32_t* cu = a.cu;
+  if (in_lds) {
+    bounds.finish(s_cu, a.cu, a.n_slots + 1);
+    __syncthreads();
+    cu = s_cu;
+  }
+  each_piece(cu, a.n_slots, t0, t1, [&](int32_t d, int32_t begin, int32_t end) {
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
@@ -121,31 +197,46 @@ __global__ __launch_bounds__(64) void preference_sums_kernel(PreferenceArgs a, i
   });
 }
 
-// Sum of a document's partial sums, on the whole wave.
-__device__ __forceinline__ double document_sum(const PreferenceArgs& a, int32_t d) {
-  const int32_t begin = a.cu[d], end = a.cu[d + 1];
+// Sums of two documents' partial sums, one on each half of the wave.
+__device__ __forceinline__ HalfSums document_sums(const PreferenceArgs& a, const int32_t* cu, int32_t c, int32_t r) {
+  const int half = threadIdx.x >> 5;
+  const int32_t d = half ? r : c;
+  const int32_t begin = cu[d], end = cu[d + 1];
   double sum = 0.0;
   if (begin < end) {
-    const int32_t first = begin / kTile, last = (end - 1) / kTile;
-    for (int32_t i = first + static_cast<int32_t>(threadIdx.x); i <= last; i += 64)
-      sum += a.ws_sums[static_cast<int64_t>(i) + d];
+    constexpr int kAhead = 8;  // partial sums in flight
+    const int32_t last = (end - 1) / kTile;
+    for (int32_t i0 = begin / kTile + static_cast<int32_t>(threadIdx.x & 31); i0 <= last; i0 += 32 * kAhead) {
+      double v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int32_t i = i0 + 32 * j;
+        v[j] = a.ws_sums[static_cast<int64_t>(min(i, last)) + d];
+        if (i > last) v[j] = 0.0;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) sum += v[j];
+    }
   }
-  return wave_sum(sum);
+  return half_sums(sum);
 }
 
 __device__ __forceinline__ double softplus(double x) { return log1p(exp(-fabs(x))) + (x > 0.0 ? x : 0.0); }
 
 __global__ __launch_bounds__(64) void preference_loss_kernel(PreferenceArgs a, int32_t tiles) {
+  __shared__ int32_t s_cu[kLdsSlots + 1];
+  __shared__ int32_t s_pairs[2 * kLdsPairs];
   const int lane = threadIdx.x;
   const int32_t code = *a.ws_code;
-  if (code != THD_OK) return;
   if (static_cast<int32_t>(blockIdx.x) >= tiles) {
+    if (code != THD_OK) return;
     const int32_t i = blockIdx.x - tiles;
     const int32_t c = a.pairs[2 * i], r = a.pairs[2 * i + 1];
     double loss = 0.0, won = 0.0, lost = 0.0;
     if (c >= 0 && c < a.n_slots && r >= 0 && r < a.n_slots) {
-      won = a.beta * document_sum(a, c);
-      lost = a.beta * document_sum(a, r);
+      const HalfSums sums = document_sums(a, a.cu, c, r);
+      won = a.beta * sums.low;
+      lost = a.beta * sums.high;
       const double z = won - lost, e = a.smoothing;
       loss = 0.0;
       if (e < 1.0) loss += (1.0 - e) * softplus(-z);
@@ -164,22 +255,37 @@ __global__ __launch_bounds__(64) void preference_loss_kernel(PreferenceArgs a, i
   const int32_t tile = blockIdx.x;
   const int32_t t0 = tile * kTile;
   const int32_t t1 = static_cast<int32_t>(min(static_cast<int64_t>(t0) + kTile, static_cast<int64_t>(a.total)));
+  const bool slots_in_lds = a.n_slots <= kLdsSlots, pairs_in_lds = a.n_pairs <= kLdsPairs;
+  Staged<4> bounds, some_pairs;
+  if (slots_in_lds) bounds.issue(a.cu, a.n_slots + 1);
+  if (pairs_in_lds) some_pairs.issue(a.pairs, 2 * a.n_pairs);
   uint8_t on[kEach];
   float g[kEach];
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
-    const int64_t t = static_cast<int64_t>(t0) + j * 64 + lane;
     g[j] = 0.0f;
-    on[j] = t < t1 ? (a.mask ? a.mask[t] : 1) : 0;
+    on[j] = a.mask ? a.mask[min(t0 + j * 64 + lane, t1 - 1)] : 1;
   }
-  each_piece(a.cu, a.n_slots, t0, t1, [&](int32_t d, int32_t begin, int32_t end) {
+  if (code != THD_OK) return;
+  const int32_t* cu = a.cu;
+  const int32_t* pairs = a.pairs;
+  if (slots_in_lds) {
+    bounds.finish(s_cu, a.cu, a.n_slots + 1);
+    cu = s_cu;
+  }
+  if (pairs_in_lds) {
+    some_pairs.finish(s_pairs, a.pairs, 2 * a.n_pairs);
+    pairs = s_pairs;
+  }
+  __syncthreads();
+  each_piece(cu, a.n_slots, t0, t1, [&](int32_t d, int32_t begin, int32_t end) {
     // every pair that names the document, in order
     double coef = 0.0;
     for (int32_t p0 = 0; p0 < a.n_pairs; p0 += 64) {
       int32_t c = -1, r = -1;
       if (p0 + lane < a.n_pairs) {
-        c = a.pairs[2 * (p0 + lane)];
-        r = a.pairs[2 * (p0 + lane) + 1];
+        c = pairs[2 * (p0 + lane)];
+        r = pairs[2 * (p0 + lane) + 1];
       }
       const bool valid = c >= 0 && c < a.n_slots && r >= 0 && r < a.n_slots;
       uint64_t named = __ballot(valid && c != r && (c == d || r == d));
@@ -187,8 +293,8 @@ __global__ __launch_bounds__(64) void preference_loss_kernel(PreferenceArgs a, i
         const int l = __builtin_ctzll(named);
         named &= named - 1;
         const int32_t cc = __shfl(c, l), rr = __shfl(r, l);
-        const double z = a.beta * document_sum(a, cc) -
-                         a.beta * document_sum(a, rr);
+        const HalfSums sums = document_sums(a, cu, cc, rr);
+        const double z = a.beta * sums.low - a.beta * sums.high;
         const double slope = a.smoothing - 1.0 / (1.0 + exp(z));
         coef += cc == d ? slope : -slope;
       }

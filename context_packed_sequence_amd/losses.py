@@ -17,39 +17,31 @@ outputs are allocated too.
 
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import binding as _b
 
 _DTYPES = {torch.bfloat16: _b.THD_BF16, torch.float16: _b.THD_FP16, torch.float32: _b.THD_FP32}
-
-
-def _on(stream):
-    """Outputs and workspaces belong to the stream that writes them: memory
-    handed back to another stream's pool could be given out again too early."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+_F32, _I64, _I32, _U8 = torch.float32, torch.int64, torch.int32, torch.uint8
 
 
 def _rows_of(logits, name="logits"):
     if logits.dtype not in _DTYPES:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {logits.dtype}")
-    if logits.dim() < 2:
-        raise ValueError(f"{name} must be [rows, vocab]")
-    if logits.dim() > 2:
+    if logits.dim() != 2:
+        if logits.dim() < 2:
+            raise ValueError(f"{name} must be [rows, vocab]")
         try:
             logits = logits.view(-1, logits.shape[-1])
         except RuntimeError:
             raise ValueError(f"{name}: the leading dimensions cannot be flattened without a copy") from None
+    if not logits.is_contiguous():
+        if logits.shape[1] > 1 and logits.stride(1) != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        if logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]:
+            raise ValueError(f"{name}: rows must not overlap")
     if logits.shape[1] < 1:
         raise ValueError(f"{name} needs at least one column")
-    if logits.shape[1] > 1 and logits.stride(1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]:
-        raise ValueError(f"{name}: rows must not overlap")
     return logits
 
 
@@ -57,24 +49,40 @@ def _stride(x) -> int:
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
-def _per_row(x, name, dtype, rows, device):
+def _address(x, name, dtype, count, device, required=False):
+    """Address of a contiguous tensor after the checks the C ABI cannot make."""
     if x is None:
-        return
-    if x.dtype != dtype:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    if x.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.numel() != rows:
-        raise ValueError(f"{name} must have {rows} elements, got {x.numel()}")
-    if x.device != device:
-        raise ValueError(f"{name} must be on {device}, got {x.device}")
+    if x.numel() != count:
+        raise ValueError(f"{name} must have {count} elements, got {x.numel()}")
+    if x.get_device() != device:
+        raise ValueError(f"{name} must be on the logits' device, got {x.device}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return x.data_ptr()
 
 
 def _need_gpu(x, name):
     if not x.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if x.device.index != torch.cuda.current_device():
+    if x.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {x.device}, which is not the current device")
+
+
+def _run(call, stream):
+    """``call`` with the handle of the stream to use.  Outputs and workspaces are
+    allocated inside, on that stream: memory handed back to another stream's
+    pool could be given out again too early."""
+    if stream is None:
+        return call(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _grad_rows(logits, out):
@@ -88,19 +96,22 @@ def _grad_rows(logits, out):
         if out.shape != logits.shape:
             raise ValueError(f"out must be {tuple(logits.shape)}, got {tuple(out.shape)}")
         return out
+    if logits.is_contiguous() and logits.data_ptr() % 16 == 0:
+        return torch.empty_like(logits)
     rows, vocab = logits.shape
     size = logits.element_size()
-    per = 16 // size
     lead = logits.data_ptr() % 16 // size
-    pad = (_stride(logits) - vocab) % per
-    if not lead and not pad:
-        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    pad = (_stride(logits) - vocab) % (16 // size)
     room = torch.empty(lead + rows * (vocab + pad), dtype=logits.dtype, device=logits.device)
     return room.as_strided((rows, vocab), (vocab + pad, 1), lead)
 
 
 def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    """(tensor that keeps it alive, address)"""
+    if nbytes <= 0:
+        return None, None
+    room = torch.empty(nbytes, dtype=_U8, device=device)
+    return room, room.data_ptr()
 
 
 def _like(grad, x):
@@ -113,21 +124,26 @@ def token_logprobs(logits, labels, mask=None, stream=None):
     (logp float32 [rows], lse float32 [rows], status)."""
     z = _rows_of(logits)
     rows, vocab = z.shape
-    dev = z.device
-    if labels is None:
-        raise ValueError("labels is required")
-    _per_row(labels, "labels", torch.int64, rows, dev)
-    _per_row(mask, "mask", torch.uint8, rows, dev)
+    on = z.get_device()
+    labels_at = _address(labels, "labels", _I64, rows, on, True)
+    mask_at = _address(mask, "mask", _U8, rows, on)
     _need_gpu(z, "logits")
     dtype = _DTYPES[z.dtype]
-    with _on(stream):
-        logp = torch.empty(rows, dtype=torch.float32, device=dev)
-        lse = torch.empty(rows, dtype=torch.float32, device=dev)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-        nbytes = _b.thd_loss_workspace_bytes(rows, vocab, dtype, 0)
-        _b.thd_token_logprobs(z.data_ptr(), dtype, rows, vocab, _stride(z), labels, mask, logp, lse, status,
-                              _workspace(nbytes, dev), nbytes, stream)
-    return logp, lse, status
+    lib = _b.library()
+
+    def call(handle):
+        dev = z.device
+        logp = torch.empty(rows, dtype=_F32, device=dev)
+        lse = torch.empty(rows, dtype=_F32, device=dev)
+        status = torch.empty(1, dtype=_I32, device=dev)
+        nbytes = lib.thd_loss_workspace_bytes(rows, vocab, dtype, 0)
+        room, room_at = _workspace(nbytes, dev)
+        code = lib.thd_token_logprobs(z.data_ptr(), dtype, rows, vocab, _stride(z), labels_at, mask_at,
+                                      logp.data_ptr(), lse.data_ptr(), status.data_ptr(), room_at, nbytes, handle)
+        if code < 0:
+            raise _b.ThdError(code, "thd_token_logprobs")
+        return logp, lse, status
+    return _run(call, stream)
 
 
 def token_logprobs_backward(dlogp, logits, labels, lse, mask=None, out=None, stream=None):
@@ -136,19 +152,22 @@ def token_logprobs_backward(dlogp, logits, labels, lse, mask=None, out=None, str
     logits themselves, which are then replaced."""
     z = _rows_of(logits)
     rows, vocab = z.shape
-    dev = z.device
-    for name, x, dtype in (("dlogp", dlogp, torch.float32), ("labels", labels, torch.int64),
-                           ("lse", lse, torch.float32)):
-        if x is None:
-            raise ValueError(f"{name} is required")
-        _per_row(x, name, dtype, rows, dev)
-    _per_row(mask, "mask", torch.uint8, rows, dev)
+    on = z.get_device()
+    dlogp_at = _address(dlogp, "dlogp", _F32, rows, on, True)
+    labels_at = _address(labels, "labels", _I64, rows, on, True)
+    lse_at = _address(lse, "lse", _F32, rows, on, True)
+    mask_at = _address(mask, "mask", _U8, rows, on)
     _need_gpu(z, "logits")
-    with _on(stream):
+
+    def call(handle):
         grad = _grad_rows(z, out)
-        _b.thd_token_logprobs_backward(dlogp, z.data_ptr(), _DTYPES[z.dtype], rows, vocab, _stride(z), labels, lse,
-                                       mask, grad.data_ptr(), _stride(grad), stream)
-    return _like(grad, logits) if out is None else out
+        code = _b.library().thd_token_logprobs_backward(
+            dlogp_at, z.data_ptr(), _DTYPES[z.dtype], rows, vocab, _stride(z), labels_at, lse_at, mask_at,
+            grad.data_ptr(), _stride(grad), handle)
+        if code < 0:
+            raise _b.ThdError(code, "thd_token_logprobs_backward")
+        return _like(grad, logits) if out is None else out
+    return _run(call, stream)
 
 
 def policy_loss(logits, labels, old_logp, advantages, mask=None, ref_logp=None, weights=None, clip_low=0.2,
@@ -159,29 +178,35 @@ def policy_loss(logits, labels, old_logp, advantages, mask=None, ref_logp=None, 
     normalisation, e.g. one over the number of labelled tokens."""
     z = _rows_of(logits)
     rows, vocab = z.shape
-    dev = z.device
-    for name, x, dtype in (("labels", labels, torch.int64), ("old_logp", old_logp, torch.float32),
-                           ("advantages", advantages, torch.float32)):
-        if x is None:
-            raise ValueError(f"{name} is required")
-        _per_row(x, name, dtype, rows, dev)
-    _per_row(mask, "mask", torch.uint8, rows, dev)
-    _per_row(ref_logp, "ref_logp", torch.float32, rows, dev)
-    _per_row(weights, "weights", torch.float32, rows, dev)
+    on = z.get_device()
+    labels_at = _address(labels, "labels", _I64, rows, on, True)
+    old_at = _address(old_logp, "old_logp", _F32, rows, on, True)
+    adv_at = _address(advantages, "advantages", _F32, rows, on, True)
+    mask_at = _address(mask, "mask", _U8, rows, on)
+    ref_at = _address(ref_logp, "ref_logp", _F32, rows, on)
+    weights_at = _address(weights, "weights", _F32, rows, on)
     if kl_coef and ref_logp is None:
         raise ValueError("a KL term needs ref_logp")
     _need_gpu(z, "logits")
     dtype = _DTYPES[z.dtype]
-    with _on(stream):
+    lib = _b.library()
+
+    def call(handle):
+        dev = z.device
         grad = _grad_rows(z, out)
-        loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        logp = torch.empty(rows, dtype=torch.float32, device=dev)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-        nbytes = _b.thd_loss_workspace_bytes(rows, vocab, dtype, 1)
-        _b.thd_policy_loss(z.data_ptr(), dtype, rows, vocab, _stride(z), labels, mask, old_logp, ref_logp, advantages,
-                           weights, clip_low, clip_high, kl_coef, loss, logp, grad.data_ptr(), _stride(grad), status,
-                           _workspace(nbytes, dev), nbytes, stream)
-    return loss, logp, _like(grad, logits) if out is None else out, status
+        loss = torch.empty(rows, dtype=_F32, device=dev)
+        logp = torch.empty(rows, dtype=_F32, device=dev)
+        status = torch.empty(1, dtype=_I32, device=dev)
+        nbytes = lib.thd_loss_workspace_bytes(rows, vocab, dtype, 1)
+        room, room_at = _workspace(nbytes, dev)
+        code = lib.thd_policy_loss(z.data_ptr(), dtype, rows, vocab, _stride(z), labels_at, mask_at, old_at, ref_at,
+                                   adv_at, weights_at, clip_low, clip_high, kl_coef, loss.data_ptr(),
+                                   logp.data_ptr(), grad.data_ptr(), _stride(grad), status.data_ptr(), room_at,
+                                   nbytes, handle)
+        if code < 0:
+            raise _b.ThdError(code, "thd_policy_loss")
+        return loss, logp, _like(grad, logits) if out is None else out, status
+    return _run(call, stream)
 
 
 def distill_topk(logits, teacher_logits, teacher_ids, mask=None, weights=None, temperature=1.0, out=None,
@@ -192,10 +217,10 @@ def distill_topk(logits, teacher_logits, teacher_ids, mask=None, weights=None, t
     columns."""
     z = _rows_of(logits)
     rows, vocab = z.shape
-    dev = z.device
+    on = z.get_device()
     if teacher_logits is None or teacher_ids is None:
         raise ValueError("teacher_logits and teacher_ids are required")
-    if teacher_ids.dtype not in (torch.int32, torch.int64):
+    if teacher_ids.dtype not in (_I32, _I64):
         raise ValueError(f"teacher_ids must be int32 or int64, got {teacher_ids.dtype}")
     t = _rows_of(teacher_logits, "teacher_logits")
     k = t.shape[1]
@@ -204,23 +229,29 @@ def distill_topk(logits, teacher_logits, teacher_ids, mask=None, weights=None, t
     for name, x in (("teacher_logits", t), ("teacher_ids", teacher_ids)):
         if x.numel() != rows * k or x.shape[-1] != k:
             raise ValueError(f"{name} must be [{rows}, {k}]")
-        if x.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {x.device}")
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _per_row(mask, "mask", torch.uint8, rows, dev)
-    _per_row(weights, "weights", torch.float32, rows, dev)
+    teacher_at = _address(t, "teacher_logits", t.dtype, rows * k, on)
+    ids_at = _address(teacher_ids, "teacher_ids", teacher_ids.dtype, rows * k, on)
+    mask_at = _address(mask, "mask", _U8, rows, on)
+    weights_at = _address(weights, "weights", _F32, rows, on)
     _need_gpu(z, "logits")
     dtype = _DTYPES[z.dtype]
-    with _on(stream):
+    lib = _b.library()
+
+    def call(handle):
+        dev = z.device
         grad = _grad_rows(z, out)
-        loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-        nbytes = _b.thd_loss_workspace_bytes(rows, vocab, dtype, k)
-        _b.thd_distill_topk(z.data_ptr(), dtype, rows, vocab, _stride(z), t.data_ptr(), _DTYPES[t.dtype],
-                            teacher_ids.data_ptr(), teacher_ids.element_size(), k, k, mask, weights, temperature,
-                            loss, grad.data_ptr(), _stride(grad), status, _workspace(nbytes, dev), nbytes, stream)
-    return loss, _like(grad, logits) if out is None else out, status
+        loss = torch.empty(rows, dtype=_F32, device=dev)
+        status = torch.empty(1, dtype=_I32, device=dev)
+        nbytes = lib.thd_loss_workspace_bytes(rows, vocab, dtype, k)
+        room, room_at = _workspace(nbytes, dev)
+        code = lib.thd_distill_topk(z.data_ptr(), dtype, rows, vocab, _stride(z), teacher_at, _DTYPES[t.dtype],
+                                    ids_at, teacher_ids.element_size(), k, k, mask_at, weights_at, temperature,
+                                    loss.data_ptr(), grad.data_ptr(), _stride(grad), status.data_ptr(), room_at,
+                                    nbytes, handle)
+        if code < 0:
+            raise _b.ThdError(code, "thd_distill_topk")
+        return loss, _like(grad, logits) if out is None else out, status
+    return _run(call, stream)
 
 
 def preference_loss(logp, ref_logp, pairs, cu_seqlens_padded, mask=None, beta=0.1, label_smoothing=0.0, scale=1.0,
@@ -234,28 +265,35 @@ def preference_loss(logp, ref_logp, pairs, cu_seqlens_padded, mask=None, beta=0.
     if logp is None or pairs is None or cu_seqlens_padded is None:
         raise ValueError("logp, pairs and cu_seqlens_padded are required")
     total = logp.numel()
-    dev = logp.device
-    _per_row(logp, "logp", torch.float32, total, dev)
-    _per_row(ref_logp, "ref_logp", torch.float32, total, dev)
-    _per_row(mask, "mask", torch.uint8, total, dev)
-    _per_row(cu_seqlens_padded, "cu_seqlens_padded", torch.int32, cu_seqlens_padded.numel(), dev)
+    on = logp.get_device()
     if pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError("pairs must be [pairs, 2]")
     n_pairs = pairs.shape[0]
-    _per_row(pairs, "pairs", torch.int32, 2 * n_pairs, dev)
     if n_pairs > _b.THD_MAX_PAIRS:
         raise ValueError(f"at most {_b.THD_MAX_PAIRS} pairs, got {n_pairs}")
     n_slots = cu_seqlens_padded.numel() - 1
     if n_slots < 0:
         raise ValueError("cu_seqlens_padded needs at least one boundary")
+    logp_at = _address(logp, "logp", _F32, total, on)
+    ref_at = _address(ref_logp, "ref_logp", _F32, total, on)
+    mask_at = _address(mask, "mask", _U8, total, on)
+    cu_at = _address(cu_seqlens_padded, "cu_seqlens_padded", _I32, n_slots + 1, on)
+    pairs_at = _address(pairs, "pairs", _I32, 2 * n_pairs, on)
     _need_gpu(logp, "logp")
-    with _on(stream):
-        loss = torch.empty(n_pairs, dtype=torch.float32, device=dev)
-        rewards = torch.empty((n_pairs, 2), dtype=torch.float32, device=dev)
-        dlogp = torch.empty(total, dtype=torch.float32, device=dev)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-        nbytes = _b.thd_preference_workspace_bytes(total, n_slots)
-        _b.thd_preference_loss(logp, ref_logp, mask, cu_seqlens_padded, n_slots, total, pairs, n_pairs, beta,
-                               label_smoothing, scale, loss, rewards, dlogp, status, _workspace(nbytes, dev), nbytes,
-                               stream)
-    return loss, rewards, dlogp, status
+    lib = _b.library()
+
+    def call(handle):
+        dev = logp.device
+        loss = torch.empty(n_pairs, dtype=_F32, device=dev)
+        rewards = torch.empty((n_pairs, 2), dtype=_F32, device=dev)
+        dlogp = torch.empty(total, dtype=_F32, device=dev)
+        status = torch.empty(1, dtype=_I32, device=dev)
+        nbytes = lib.thd_preference_workspace_bytes(total, n_slots)
+        room, room_at = _workspace(nbytes, dev)
+        code = lib.thd_preference_loss(logp_at, ref_at, mask_at, cu_at, n_slots, total, pairs_at, n_pairs, beta,
+                                       label_smoothing, scale, loss.data_ptr(), rewards.data_ptr(),
+                                       dlogp.data_ptr(), status.data_ptr(), room_at, nbytes, handle)
+        if code < 0:
+            raise _b.ThdError(code, "thd_preference_loss")
+        return loss, rewards, dlogp, status
+    return _run(call, stream)

@@ -121,10 +121,10 @@ def test_workspace(lib, logp, policy, distill):
         assert need(*bad) == -1
     # two rows of a large vocabulary are cut into parts: without a workspace the calls refuse
     for call, targets in ((logp, 0), (policy, 1), (distill, 16)):
-        n = need(2, 32000, thd.THD_BF16, targets)
+        n = need(2, 131072, thd.THD_BF16, targets)
         assert n > 0
         for bad in (dict(ws=None, ws_bytes=n), dict(ws=WS, ws_bytes=n - 1), dict(ws=WS + 4, ws_bytes=n)):
-            assert call(rows=2, **bad) == thd.THD_ERR_ARG
+            assert call(rows=2, vocab=131072, stride=131072, **bad) == thd.THD_ERR_ARG
 
 
 def test_wrappers_refuse_before_any_device_call():
