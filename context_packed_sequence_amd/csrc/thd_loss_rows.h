@@ -8,6 +8,7 @@
 
 namespace thdcp {
 
+constexpr int kMostHeld = 1024 * (18 + 8);
 constexpr int kRestWords = 4;  // words in flight of a row's part beyond the registers
 
 // kWords words of a row per thread in registers, kLds more in LDS.  Up to 8 words
@@ -18,6 +19,8 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   constexpr int kPer = Elem<T>::kPer;
   constexpr int kStep = 16 * kThreads;  // bytes from one of a thread's words to the next
   constexpr int kHeld = kWords + kLds;
+  // the largest form takes rows of any length: what it cannot hold is read twice
+  constexpr bool kAnyLength = kHeld * kThreads == kMostHeld;
   // words absorbed at a time, whose elements share one rescale
   constexpr int kJoinWords = kWords <= 8 ? 1 : 2;
   static_assert(kWords % kJoinWords == 0 && kHeld <= kRestBit);
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
       absorb(fast, f, scale);
     }
   }
-  for (int32_t b = at0 + kHeld * kStep; b < words.bytes; b += kRestWords * kStep) {
+  for (int32_t b = at0 + kHeld * kStep; kAnyLength && b < words.bytes; b += kRestWords * kStep) {
     Word4 y[kRestWords];
 #pragma unroll
     for (int j = 0; j < kRestWords; ++j) y[j] = words.load(b + j * kStep);
@@ -218,7 +221,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
     here += kStep;
     __builtin_amdgcn_sched_barrier(0);
   }
-  for (int32_t b = at0 + kHeld * kStep, k = kHeld; b < words.bytes; b += kRestWords * kStep, k += kRestWords) {
+  for (int32_t b = at0 + kHeld * kStep, k = kHeld; kAnyLength && b < words.bytes; b += kRestWords * kStep, k += kRestWords) {
     Word4 y[kRestWords];
 #pragma unroll
     for (int j = 0; j < kRestWords; ++j) y[j] = words.load(b + j * kStep);

@@ -284,6 +284,42 @@ def test_many_rows(torch, thd, dtype, vocab):
     _check_distill(case, thd, ids64=False, teacher_dtype=_dtype(torch, dtype))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("words", [256, 512, 1024, 2048, 4096, 8192, 12288, 16384, 26624])
+def test_rows_that_just_fit(torch, thd, dtype, words):
+    # rows on whole lines that fill a form's registers (and LDS), and a word more
+    per = 8 if dtype == "bf16" else 4
+    for vocab in (words * per, words * per + per):
+        say("full registers", dtype, vocab)
+        case = Case(torch, 18, 3, 70, vocab, dtype)
+        _check_policy(case, thd)
+        case = Case(torch, 18, 3, 70, vocab, dtype, k=33)
+        _check_distill(case, thd)
+
+
+@pytest.mark.parametrize("rows", [5, 1100])
+@pytest.mark.parametrize("out", ["new", "in place"])
+def test_logits_of_any_size(torch, thd, rows, out):
+    # a row's logits may lie far from zero: only their distances count. 32-bit
+    # steps at 2^k are 2^(k-23), so the distances are whole numbers of those.
+    say("far from zero", rows, out)
+    for at in (0.0, 4e8, -4e8, 6.2e8, -6.3e8, 1.5e9, -3e9, 1e20, 2.5e38, -2.5e38):
+        case = Case(torch, 19, 5, rows, 3001, "fp32", k=9)
+        step = float(np.spacing(np.float32(max(abs(at), 1.0))))
+        case.z = at - step * np.random.default_rng(3).integers(0, 4, (5, 3001)) if at else case.z
+        case.z = case.z.astype(np.float32).astype(np.float64)
+        case.logits.copy_(torch.from_numpy(case.z).float().cuda()[torch.from_numpy(case.pick).cuda()])
+        logp, _ = O.token_logprobs(case.z, case.labels)
+        case.old = (np.maximum(logp, -60) + 0.05).astype(np.float32)
+        case.ref = (np.maximum(logp, -60) - 0.1).astype(np.float32)
+        live = logp > -60        # labels further off have a ratio of zero, and a KL term beyond 32 bits
+        case.mask[:] = live
+        _check_policy(case, thd, out=out, kl=0.1)
+        case.logits.copy_(torch.from_numpy(case.z).float().cuda()[torch.from_numpy(case.pick).cuda()])
+        case.mask[:] = 1
+        _check_distill(case, thd, out=out, tau=1.5)
+
+
 @pytest.mark.parametrize("vocab", [200003, 300007])
 def test_rows_longer_than_the_registers(torch, thd, vocab):
     say("long rows", vocab)
