@@ -1,5 +1,10 @@
 // Label log-probabilities and their gradient, and the two-pass form of the
 // losses for few rows (each row cut into parts over many workgroups).
+//
+// The log-probabilities read the logits once and write 8 bytes a row: 256
+// threads stream a row with 8 words each in flight, the maximum and sum held
+// as they go (32768 x 32000 bf16, a tenth masked: 275 us, 6.9 TB/s; a pure read
+// stream 7.3).
 #include <atomic>
 
 #include "thd_loss_device.h"
@@ -9,6 +14,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 16 * kThreads;  // bytes from one of a thread's words to the next
+// The gradient of the log-probabilities has everything it needs with the row: a
+// copy with an exponential per element.  8 KiB tiles (2 words a thread) in
+// chunks of 16 tiles per XCD run at 6.4 TB/s, 95 % of a plain copy (16384 x
+// 65536 bf16 637 us; 4 KiB tiles 709-716, 16 KiB 686-727, 32 KiB 714-730; plain
+// order 666).
 constexpr int kGradAhead = 2;
 constexpr int kBackwardTurns = 2;
 constexpr int kBackwardChunkShift = 4;

@@ -1,7 +1,24 @@
 // One workgroup per row of logits: the policy loss and the distillation in one
 // pass.  The row is read once into registers, its maximum and sum are formed as
 // the words arrive, the gradient is computed from the registers and stored:
-// one read and one write of the logits, the least the operation can move.
+// one read and one write of the logits, the least the operation can move, and
+// what the memory counters show (8192 x 131072 bf16, a tenth of the rows
+// masked: 1.93 GB read, 2.15 GB written).
+//
+// What bounds it is memory.  A plain copy runs at 6.8 TB/s here; a workgroup
+// that loads a whole row, waits, and stores it, with no arithmetic at all, at
+// 5.7-6.3 TB/s (64-256 KiB rows), and this kernel at 6.1-6.5 TB/s for rows of
+// up to 64 KiB, 5.6-5.9 for longer ones, where one or two workgroups fill a
+// compute unit's registers.  Vector instructions are busy for about half of that
+// time: 11 issue slots an element (two exponentials take four of them).
+//
+// Tried and slower: workgroups that stay and load their next row into the
+// registers as these are stored (loads and stores of a wave are counted in one
+// order, so that the next row's words waited for this row's stores: 836 us
+// against 748 for 8192 x 131072); starting the compute units apart from each
+// other (no change); 512 threads with 32 words each (403 us against 380 for
+// 4096 x 131072); a row's rest from cache instead of LDS (2047 x 200003: 341 us
+// against 293).
 #pragma once
 
 #include "thd_loss_device.h"
@@ -12,7 +29,9 @@ constexpr int kMostHeld = 1024 * (18 + 8);
 constexpr int kRestWords = 4;  // words in flight of a row's part beyond the registers
 
 // kWords words of a row per thread in registers, kLds more in LDS.  Up to 8 words
-// leave room for 8 waves per SIMD.
+// leave room for 8 waves per SIMD, which runs faster than 4 waves of 16 words
+// (8388 x 64000 bf16 356 us against 368); waves skip turns in which they have no
+// word, so that a form serves any shorter row (134217 x 2000: 376 us without).
 template <typename T, int kThreads, int kWords, int kLds, LossKind kKind>
 __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel(LogitRows r, LossArgs a, int32_t row0,
                                                                int32_t chunk_shift) {
@@ -339,7 +358,9 @@ __global__ __launch_bounds__(256) void row_loss_apart_kernel(LogitRows r, LossAr
   }
 }
 
-// Rows per chunk of an XCD's order: about 1 MiB, and at least 16 rows.
+// Rows per chunk of an XCD's order: about 1 MiB, and at least 16 rows.  Against
+// plain order: 67108 x 8000 bf16 354 us and 384, 16777 x 32000 365 and 377,
+// 4096 x 131072 382 and 396; chunks of 4 rows are slower there (421 us).
 inline int32_t row_chunk_shift(const LogitRows& r) {
   const int64_t bytes = static_cast<int64_t>(r.vocab) * (r.dtype == THD_FP32 ? 4 : 2);
   int32_t shift = 4;
@@ -374,6 +395,10 @@ hipError_t launch_rows(const LogitRows& r, const LossArgs& a, hipStream_t stream
   // rows that do not all start on a 128-byte line are shifted by up to 7 words
   const bool lines = reinterpret_cast<uintptr_t>(r.out) % 128 == 0 && pitch % 128 == 0;
   const int32_t words = r.vocab / Elem<T>::kPer + (lines ? 0 : 7);
+  // 4 words a thread while 1024 threads hold the row (65536 x 4096 bf16 164 us,
+  // with 8 words 177; 8388 x 32000 176 us with 4, 184 with 8 on half the
+  // threads); then as many as it takes, two workgroups to a compute unit as long
+  // as they fit (LDS from 8192 words on), then one.
   if (words <= 64 * 4) return launch_rows_as<T, 64, 4, 0, kKind>(r, a, stream);
   if (words <= 128 * 4) return launch_rows_as<T, 128, 4, 0, kKind>(r, a, stream);
   if (words <= 256 * 4) return launch_rows_as<T, 256, 4, 0, kKind>(r, a, stream);

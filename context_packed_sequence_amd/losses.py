@@ -9,10 +9,11 @@ through autograd: a model's backward starts from it with
 
 Logits are [rows, vocab] (leading dimensions are flattened where that takes no
 copy) in bfloat16, float16 or float32, their last dimension contiguous; rows
-may be strided, as in a view of the first columns of a padded vocabulary.  Every
-call returns a device ``status`` word (int32 [1]) to look at when the host next
-waits, and runs on ``stream`` (the current one if none is given), on which its
-outputs are allocated too.
+may be strided, as in a view of the first columns of a padded vocabulary.  The forward
+calls return a device ``status`` word (int32 [1]) to look at when the host next
+waits.  A call runs on ``stream`` (the current one if none is given), on which
+its outputs are allocated too; work that made its inputs on another stream has
+to be ordered before it, and they have to live until it is done.
 """
 
 from __future__ import annotations

@@ -1,8 +1,13 @@
 """What the loss calls refuse, on the host, before any device work (CPU)."""
 
+import os
+import shutil
+import subprocess
+
 import pytest
 
 import context_packed_sequence_amd as thd
+from conftest import ROOT
 
 # addresses far apart; nothing is read through them
 Z, G, LAB, MASK, OLD, REF, ADV, W, LOSS, LOGP, STATUS, WS, T, ID = (i << 32 for i in range(1, 15))
@@ -161,3 +166,18 @@ def test_wrappers_refuse_before_any_device_call():
             ("must live on the GPU", lambda: thd.preference_loss(f, f, pairs, cu))):
         with pytest.raises(ValueError, match=text):
             call()
+
+
+def test_header_is_plain_c(tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "uses_header.c"
+    src.write_text('#include "thd_loss.h"\n'
+                   "int main(void) { return thd_loss_workspace_bytes(2, 131072, THD_BF16, 1) > 0 ? 0 : 1; }\n")
+    pkg = os.path.join(ROOT, "context_packed_sequence_amd")
+    exe = str(tmp_path / "uses_header")
+    res = subprocess.run([cc, "-std=c11", "-Wall", "-Wextra", "-Werror", f"-I{ROOT}/include", str(src), "-o", exe,
+                          f"-L{pkg}", "-lthdcp", f"-Wl,-rpath,{pkg}"], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    assert subprocess.run([exe], timeout=60).returncode == 0
