@@ -18,6 +18,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch  # noqa: F401  before the library: the HIP runtime torch brings has to be the process's only one
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libthdcp.so")
 

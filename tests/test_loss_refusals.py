@@ -3,6 +3,7 @@
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -181,3 +182,13 @@ def test_header_is_plain_c(tmp_path):
                           f"-L{pkg}", "-lthdcp", f"-Wl,-rpath,{pkg}"], capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
     assert subprocess.run([exe], timeout=60).returncode == 0
+
+
+def test_one_hip_runtime_whatever_is_imported_first():
+    # the library's HIP runtime and torch's are different files of one name:
+    # with both in a process, each has devices of its own
+    code = ("import context_packed_sequence_amd, torch\n"
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))\n")
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert res.returncode == 0, res.stderr
+    assert res.stdout.split()[-1] == "1"
