@@ -518,6 +518,7 @@ __device__ __forceinline__ void read_teacher(TeacherRaw& raw, const LossArgs& a,
     raw.id_low[j] = ~0u;
     raw.id_high[j] = ~0u;
     raw.logit[j] = 0;
+    if (64 * j >= a.k) continue;
     if (i < a.k) {
       raw.id_low[j] = ids[i * wide];
       if (a.ids64) raw.id_high[j] = ids[i * wide + 1];
@@ -552,6 +553,10 @@ __device__ __forceinline__ void list_targets(TargetList<kThreads>& l, const Teac
   float top = kNegInf;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
+    id[j] = -1;
+    t[j] = kNegInf;
+    z[j] = 0.0f;
+    if (64 * j >= a.k) continue;
     const int32_t low = static_cast<int32_t>(raw.id_low[j]);
     const int32_t high = a.ids64 ? static_cast<int32_t>(raw.id_high[j]) : low >> 31;
     const bool unused = low == -1 && high == -1;
@@ -559,7 +564,6 @@ __device__ __forceinline__ void list_targets(TargetList<kThreads>& l, const Teac
     if (!unused && !column) bad = true;
     id[j] = column ? low : -1;
     t[j] = column ? teacher_logit(raw.logit[j], a.teacher_dtype) : kNegInf;
-    z[j] = 0.0f;
     if (id[j] >= 0) z[j] = z_saved ? z_saved[row * a.k + lane + 64 * j] : Elem<T>::load(in + id[j]);
     top = fmaxf(top, t[j]);
   }
@@ -571,7 +575,8 @@ __device__ __forceinline__ void list_targets(TargetList<kThreads>& l, const Teac
   const float base = base_of(wave_max(top));
   float ts = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) ts += exp2_fast((t[j] - base) * a.inv_temperature * kLog2e);
+  for (int j = 0; j < kMine; ++j)
+    if (64 * j < a.k) ts += exp2_fast((t[j] - base) * a.inv_temperature * kLog2e);
   ts = wave_add(ts);
   const float ln_ts = logf(ts);
   const float inv_ts = 1.0f / ts;
