@@ -194,6 +194,10 @@ struct RowWords {
   __device__ __forceinline__ Word4 load(int32_t at) const {
     return __builtin_bit_cast(Word4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, kStreamLoad));
   }
+  // words that are read again soon: not past the caches
+  __device__ __forceinline__ Word4 load_cached(int32_t at) const {
+    return __builtin_bit_cast(Word4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
+  }
   __device__ __forceinline__ void store(int32_t at, Word4 v) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, at, 0, kStreamStorePolicy);
   }
