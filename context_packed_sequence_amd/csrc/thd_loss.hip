@@ -91,6 +91,14 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
   const Word4 nothing = {Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord};
   const int32_t begin = part * p.turns * kStep - 16 * line_shift(in + cut.head);
   const int32_t end = min(begin + p.turns * kStep, words.bytes);
+  // the label's column stays out of the sum until the end
+  int32_t label_at = -1, label_place = 0;
+  if constexpr (kKind != kLossDistill) {
+    const int32_t w = cut.word_of(static_cast<int32_t>(label));
+    if (w >= 0) label_at = 16 * w;
+    label_place = cut.place_of(static_cast<int32_t>(label));
+    if (part == 0 && tid < cut.edge && cut.edge_column(tid) == label) edge[0] = kNegInf;
+  }
   Stat st;
   for (int32_t b0 = begin; b0 < end; b0 += kStatsAhead * kStep) {
     Word4 x[kStatsAhead];
@@ -109,6 +117,7 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         Elem<T>::unpack(x[k + j], one);
+        if (kKind != kLossDistill && b + (k + j) * kStep == label_at) drop(one, label_place);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) f[j * kPer + e] = one[e];
       }
@@ -122,9 +131,8 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
     p.stats[row * p.parts + part] = make_float2(st.m, st.s);
     if (kKind != kLossDistill && part == 0) p.targets[row] = z_label;
   } else {
-    const float ln_s = logf(st.s);
-    a.logp[row] = (z_label - st.m) - ln_s;
-    a.lse[row] = st.m + ln_s;
+    a.logp[row] = join_label(st, z_label, scale).logp;
+    a.lse[row] = st.m + logf(st.s);
   }
 }
 
@@ -150,10 +158,9 @@ __global__ __launch_bounds__(64) void logp_join_kernel(LogitRows r, LossArgs a, 
     logp = lse = __builtin_nanf("");
     if (a.status && threadIdx.x == 0) *a.status = THD_ERR_LABEL;
   } else if (live) {
-    const Stat st = join_parts(p, row, kLog2e);
-    const float ln_s = logf(st.s);
-    logp = (p.targets[row] - st.m) - ln_s;
-    lse = st.m + ln_s;
+    Stat st = join_parts(p, row, kLog2e);
+    logp = join_label(st, p.targets[row], kLog2e).logp;
+    lse = st.m + logf(st.s);
   }
   if (threadIdx.x == 0) {
     a.logp[row] = logp;
@@ -230,22 +237,25 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
 
   const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
   float base, coef, amount;
+  float label_gradient = 0.0f;
   if constexpr (kKind == kLossLogp) {
     base = base_of(a.lse_in[row]);
     amount = -a.dlogp[row];
     coef = amount;
   } else {
-    const Stat st = join_parts(p, row, scale);
-    base = base_of(st.m);
+    Stat st = join_parts(p, row, scale);
     if constexpr (kKind == kLossPolicy) {
-      const float logp = (p.targets[row] - st.m) - logf(st.s);
-      const PolicyRow pr = policy_row(a, values, logp);
+      const LabelJoin joined = join_label(st, p.targets[row], scale);
+      base = base_of(st.m);
+      const PolicyRow pr = policy_row(a, values, joined.logp);
       amount = -pr.dlogp;
+      label_gradient = pr.dlogp * joined.not_q;
       if (part == 0 && tid == 0) {
         a.loss[row] = pr.loss;
-        a.logp[row] = logp;
+        a.logp[row] = joined.logp;
       }
     } else {
+      base = base_of(st.m);
       const float w = a.weights ? a.weights[row] : 1.0f;
       amount = a.temperature * w;
       if (part == 0 && tid < 64) {
@@ -253,9 +263,12 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
         if (tid == 0) a.loss[row] = loss;
       }
     }
-    coef = amount / st.s;
+    coef = amount * reciprocal(st.s);
   }
 
+  // the label's element: from the sum of the others where that is known, else
+  // the difference to its own probability
+  const auto at_label = [&](float g) { return kKind == kLossPolicy ? label_gradient : g - amount; };
   uint32_t hit = 0;
   if constexpr (kKind == kLossDistill) hit = s_list.hit[tid];
   if (same_place(in, out)) {
@@ -280,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
           if (at == label_at) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
-              if (e == label_place) g[e] -= amount;
+              if (e == label_place) g[e] = at_label(g[e]);
           }
         } else {
           const int bit = min((at - begin) / kStep, kRestBit);
@@ -293,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
       const int32_t v = cut.edge_column(tid);
       float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
       if constexpr (kKind != kLossDistill) {
-        if (v == label) g -= amount;
+        if (v == label) g = at_label(g);
       } else {
         if ((hit >> kEdgeBit) & 1u) g = take_edge_target<T, kThreads>(s_list, cut, amount, g);
       }
@@ -308,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
   const int32_t to_v = part == p.parts - 1 ? r.vocab : static_cast<int32_t>(min(v1, static_cast<int64_t>(r.vocab)));
   for (int32_t v = from + tid; v < to_v; v += kThreads) {
     float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
-    if (kKind != kLossDistill && v == label) g -= amount;
+    if (kKind != kLossDistill && v == label) g = at_label(g);
     out[v] = Elem<T>::round(g);
   }
   if constexpr (kKind == kLossDistill) {

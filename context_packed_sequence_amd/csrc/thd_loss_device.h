@@ -18,6 +18,12 @@
 // the rounding of top cancel.  It does not hold logits of any size: rows whose
 // top is beyond kHuge take the first form.
 //
+// A label's probability is near 1 for the tokens a model is sure of, and both
+// ln q_y and 1 - q_y would be what is left of a difference: its column is kept
+// out of the sum, rest = sum over v != y, and joins it at the end:
+//   own = exp(c (z_y - M)),  ln q_y = -ln(1 + rest / own) where own >= rest,
+//   1 - q_y = rest / (rest + own).
+//
 // A gradient row has the form g_v = coef (q_v - sum_k p_k [v = id_k]): one
 // target with p = 1 for the label losses, k targets for the distillation.
 #pragma once
@@ -39,7 +45,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
+// Single instructions, within one step of the result.
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }
 
 struct Bf16 {
   uint16_t bits;
@@ -362,13 +370,55 @@ __device__ __forceinline__ S join_block(S st, float scale, float2* s_red) {
   return join_lanes<true>(other, scale);
 }
 
-// Maximum and sum of a whole row in the first form, element by element: rows
-// beyond kHuge.  Every thread of the workgroup calls it.
+// The label's column joining the sum of the others.
+struct LabelJoin {
+  float logp, not_q;  // ln q_y, 1 - q_y
+  float sum;          // of all columns, relative to the joined top
+};
+
+// ln(1 + x) for small x as ln(u) x / (u - 1) with u = 1 + x rounded (Kahan): the
+// factor takes back what the rounding did to x.
+__device__ __forceinline__ LabelJoin label_join(float rest, float own, float exponent) {
+  const float sum = rest + own;
+  const float x = rest * reciprocal(own), u = 1.0f + x;
+  const float ln = logf(own >= rest ? u : sum);
+  const float ln_1px = u == 1.0f ? x : ln * (x * reciprocal(u - 1.0f));
+  return LabelJoin{own >= rest ? -ln_1px : exponent * kLn2 - ln, rest * reciprocal(sum), sum};
+}
+
+__device__ __forceinline__ LabelJoin join_label(FastStat& st, float z, float scale) {
+  const float top = fmaxf(st.top, z * scale);
+  const float rest = st.s * exp2_fast(st.top - top);
+  const float exponent = fmaf(z, scale, -top);
+  const LabelJoin j = label_join(rest, exp2_fast(exponent), exponent);
+  st = FastStat{top, j.sum};
+  return j;
+}
+
+__device__ __forceinline__ LabelJoin join_label(Stat& st, float z, float scale) {
+  const float m = fmaxf(st.m, z);
+  const float b = base_of(m);
+  const float rest = st.s * exp2_fast((st.m - b) * scale);
+  const float exponent = (z - b) * scale;
+  const LabelJoin j = label_join(rest, exp2_fast(exponent), exponent);
+  st = Stat{m, j.sum};
+  return j;
+}
+
+// Takes one element of a word out of the sum.
+template <int N>
+__device__ __forceinline__ void drop(float (&f)[N], int32_t place) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = e == place ? kNegInf : f[e];
+}
+
+// Maximum and sum of a whole row in the first form, element by element, without
+// column `skip`: rows beyond kHuge.  Every thread of the workgroup calls it.
 template <typename T, int kThreads>
-__device__ __forceinline__ Stat row_stat(const T* in, int32_t vocab, float scale, float2* s_red) {
+__device__ __forceinline__ Stat row_stat(const T* in, int32_t vocab, int64_t skip, float scale, float2* s_red) {
   Stat st;
   for (int32_t v = threadIdx.x; v < vocab; v += kThreads) {
-    const float f[1] = {Elem<T>::load(in + v)};
+    const float f[1] = {v == skip ? kNegInf : Elem<T>::load(in + v)};
     absorb(st, f, scale);
   }
   __syncthreads();  // s_red may still be read

@@ -107,6 +107,15 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
                                         shift, true);
   }
 
+  int32_t label_turn = -1, label_thread = -1, label_place = 0;
+  if constexpr (kKind == kLossPolicy) {
+    const int32_t w = cut.word_of(label);
+    if (w >= 0) {
+      label_turn = (w + shift) / kThreads;
+      label_thread = (w + shift) % kThreads;
+      label_place = cut.place_of(label);
+    }
+  }
   const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
   const Word4 nothing = {Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord, Elem<T>::kNegInfWord};
   FastStat fast;
@@ -127,6 +136,8 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
 #pragma unroll
       for (int e = 0; e < kPer; ++e) f[j * kPer + e] = one[e];
     }
+    if (label_turn >= k && label_turn < k + kJoinWords && tid == label_thread)
+      drop(f, (label_turn - k) * kPer + label_place);
     absorb(fast, f, scale);
   }
   if constexpr (kLds > 0) {
@@ -136,10 +147,11 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
       if (kWords + k >= turns) continue;
       float f[kPer];
       Elem<T>::unpack(at0 + (kWords + k) * kStep < words.bytes ? s_row[k * kThreads + tid] : nothing, f);
+      if (kWords + k == label_turn && tid == label_thread) drop(f, label_place);
       absorb(fast, f, scale);
     }
   }
-  for (int32_t b = at0 + kHeld * kStep; kAnyLength && b < words.bytes; b += kRestWords * kStep) {
+  for (int32_t b = at0 + kHeld * kStep, k = kHeld; kAnyLength && b < words.bytes; b += kRestWords * kStep, k += kRestWords) {
     Word4 y[kRestWords];
 #pragma unroll
     for (int j = 0; j < kRestWords; ++j) y[j] = words.load_cached(b + j * kStep);
@@ -147,12 +159,13 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
     for (int j = 0; j < kRestWords; ++j) {
       float f[kPer];
       Elem<T>::unpack(b + j * kStep < words.bytes ? y[j] : nothing, f);
+      if (k + j == label_turn && tid == label_thread) drop(f, label_place);
       absorb(fast, f, scale);
     }
   }
   const float edge[1] = {decode<T>(edge_raw)};
-  const float z_label = decode<T>(label_raw);
-  absorb(fast, edge, scale);
+  const bool label_on_edge = kKind == kLossPolicy && tid < cut.edge && cut.edge_column(tid) == label;
+  absorb(fast, {label_on_edge ? kNegInf : edge[0]}, scale);
   if constexpr (kKind == kLossDistill) {
     if (tid < 64) store_logits(s_list.z, z_teacher, a.k);
   }
@@ -165,47 +178,41 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
 
   // a row beyond the fast form: its sum, and below its gradient, are taken
   // element by element from memory
+  LabelJoin joined;
+  if constexpr (kKind == kLossPolicy) joined = join_label(fast, decode<T>(label_raw), scale);
   const bool huge = !(fabsf(fast.top) < kHuge);
   Stat st;
-  if (huge) st = row_stat<T, kThreads>(in, r.vocab, scale, s_red);
+  if (huge) {
+    st = row_stat<T, kThreads>(in, r.vocab, kKind == kLossPolicy ? label : -1, scale, s_red);
+    if constexpr (kKind == kLossPolicy) joined = join_label(st, decode<T>(label_raw), scale);
+  }
   const float sum = huge ? st.s : fast.s;
-  const float ln_s = logf(sum);
   const float base = base_of(st.m);
-  // scale times the distance from the maximum
-  const auto exponent = [&](float z) { return huge ? (z - base) * scale : fmaf(z, scale, -fast.top); };
   float amount;  // factor of the targets
   int32_t state = kRowLive;
   if constexpr (kKind == kLossPolicy) {
-    const float logp = exponent(z_label) * kLn2 - ln_s;
-    const PolicyRow p = policy_row(a, value, logp);
+    const PolicyRow p = policy_row(a, value, joined.logp);
     if (tid == 0) {
       a.loss[row] = p.loss;
-      a.logp[row] = logp;
+      a.logp[row] = joined.logp;
     }
     amount = -p.dlogp;
   } else {
     state = __builtin_amdgcn_readfirstlane(s_list.state);
     if (tid < 64 && state == kRowLive) {
-      const float loss = distill_loss(s_list, a, value.weight, exponent, ln_s);
+      // scale times the distance from the maximum
+      const auto exponent = [&](float z) { return huge ? (z - base) * scale : fmaf(z, scale, -fast.top); };
+      const float loss = distill_loss(s_list, a, value.weight, exponent, logf(sum));
       if (tid == 0) a.loss[row] = loss;
     }
     amount = a.temperature * value.weight;
   }
-  const float coef = amount / sum;  // factor of the exponentials
+  const float coef = amount * reciprocal(sum);  // factor of the exponentials
   // in a row beyond the fast form no word is stored from the registers
   const RowWords<T> to(out + cut.head, huge ? 0 : cut.words);
 
   uint32_t hit = 0;
   if constexpr (kKind == kLossDistill) hit = s_list.hit[tid];
-  int32_t label_turn = -1, label_thread = -1, label_place = 0;
-  if constexpr (kKind == kLossPolicy) {
-    const int32_t w = cut.word_of(label);
-    if (w >= 0) {
-      label_turn = (w + shift) / kThreads;
-      label_thread = (w + shift) % kThreads;
-      label_place = cut.place_of(label);
-    }
-  }
   const auto gradient = [&](Word4 word, int32_t b, int32_t k, int bit) {
     float f[kPer], g[kPer];
     Elem<T>::unpack(word, f);
@@ -215,7 +222,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
       if (k == label_turn && tid == label_thread) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
-          if (e == label_place) g[e] -= amount;
+          if (e == label_place) g[e] = -amount * joined.not_q;
       }
     } else {
       if ((hit >> bit) & 1u) take_targets<T, kThreads>(s_list, cut, b / 16, amount, g);
@@ -252,7 +259,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
     const int32_t v = cut.edge_column(tid);
     float g = coef * exp2_fast(fmaf(edge[0], scale, -fast.top));
     if constexpr (kKind == kLossPolicy) {
-      if (v == label) g -= amount;
+      if (label_on_edge) g = -amount * joined.not_q;
     } else {
       if ((hit >> kEdgeBit) & 1u) g = take_edge_target<T, kThreads>(s_list, cut, amount, g);
     }
@@ -261,7 +268,7 @@ __global__ __launch_bounds__(kThreads, kWords <= 8 ? 8 : 4) void row_loss_kernel
   if (huge && state == kRowLive) {
     for (int32_t v = tid; v < r.vocab; v += kThreads) {
       float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
-      if (kKind == kLossPolicy && v == label) g -= amount;
+      if (kKind == kLossPolicy && v == label) g = -amount * joined.not_q;
       out[v] = Elem<T>::round(g);
     }
     if constexpr (kKind == kLossDistill) {
@@ -320,20 +327,15 @@ __global__ __launch_bounds__(256) void row_loss_apart_kernel(LogitRows r, LossAr
       }
     } else {
       const float scale = kKind == kLossDistill ? a.inv_temperature * kLog2e : kLog2e;
-      Stat st;
-      for (int32_t v = tid; v < r.vocab; v += kThreads) {
-        const float f[1] = {Elem<T>::load(in + v)};
-        absorb(st, f, scale);
-      }
-      st = join_block<kThreads>(st, scale, s_red);
-      const float base = base_of(st.m);
+      Stat st = row_stat<T, kThreads>(in, r.vocab, kKind == kLossPolicy ? label : -1, scale, s_red);
       float amount;
+      LabelJoin joined;
       if constexpr (kKind == kLossPolicy) {
-        const float logp = (Elem<T>::load(in + label) - st.m) - logf(st.s);
-        const PolicyRow p = policy_row(a, policy_values(a, row), logp);
+        joined = join_label(st, Elem<T>::load(in + label), scale);
+        const PolicyRow p = policy_row(a, policy_values(a, row), joined.logp);
         if (tid == 0) {
           a.loss[row] = p.loss;
-          a.logp[row] = logp;
+          a.logp[row] = joined.logp;
         }
         amount = -p.dlogp;
       } else {
@@ -344,10 +346,11 @@ __global__ __launch_bounds__(256) void row_loss_apart_kernel(LogitRows r, LossAr
         }
         amount = a.temperature * w;
       }
-      const float coef = amount / st.s;
+      const float coef = amount * reciprocal(st.s);
+      const float base = base_of(st.m);
       for (int32_t v = tid; v < r.vocab; v += kThreads) {
         float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
-        if (kKind == kLossPolicy && v == label) g -= amount;
+        if (kKind == kLossPolicy && v == label) g = -amount * joined.not_q;
         out[v] = Elem<T>::round(g);
       }
       if constexpr (kKind == kLossDistill) {

@@ -320,6 +320,33 @@ def test_logits_of_any_size(torch, thd, rows, out):
         _check_distill(case, thd, out=out, tau=1.5)
 
 
+@pytest.mark.parametrize("rows", [5, 40, 1100])
+@pytest.mark.parametrize("vocab", [2, 9, 1003, 70001])
+def test_labels_near_certainty(torch, thd, rows, vocab):
+    # ln q and 1 - q of a label far above the rest keep their relative precision:
+    # the sum's, and 6 u of the gap from the exponentials' arguments
+    say("near certainty", rows, vocab)
+    case = Case(torch, 20, 5, rows, vocab, "fp32")
+    case.mask[:] = 1
+    case.labels[:] = [0, vocab - 1, vocab // 2, min(3, vocab - 1), vocab - 2]
+    top = case.z.max(1)
+    case.z[np.arange(5), case.labels] = np.float32(top + [5, 10, 15, 20, 25])
+    case.logits.copy_(torch.from_numpy(case.z).float().cuda()[torch.from_numpy(case.pick).cuda()])
+    gap = np.array([5, 10, 15, 20, 25]) + 30
+    rel = _sum_error(vocab) + (6 * gap + 12) * U
+    logp, lse, _ = thd.token_logprobs(case.logits, case.dev(case.labels))
+    want, _ = O.token_logprobs(case.z, case.labels)
+    _within(_host(logp), case.whole(want), case.whole(rel * np.abs(want) + 1e-15), "logp")
+    # the policy that the batch was drawn with: the gradient is A (q - [y])
+    old = want.astype(np.float32)
+    loss, got, g, _ = thd.policy_loss(case.logits, case.dev(case.labels), case.dev(old),
+                                      torch.ones(rows, device="cuda"), clip_high=0.5)
+    _within(_host(got), case.whole(want), case.whole(rel * np.abs(want) + 1e-15), "logp of the policy loss")
+    at = g[torch.arange(rows, device="cuda"), case.dev(case.labels)]
+    not_q = -np.expm1(want)
+    _within(_host(at), case.whole(-not_q), case.whole((rel + 4 * U) * not_q + 1e-15), "label's gradient")
+
+
 @pytest.mark.parametrize("vocab", [200003, 300007])
 def test_rows_longer_than_the_registers(torch, thd, vocab):
     say("long rows", vocab)
