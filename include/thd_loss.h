@@ -98,8 +98,9 @@ int thd_token_logprobs_backward(const float* dlogp, const void* logits, int32_t 
  * kl_coef is 0 (it is not read then).  weights: float [rows] w, NULL: 1.
  * 0 <= clip_low <= 1, clip_high >= 0, all three finite.
  * loss, logp: float [rows] (outputs).  The logits are read once and the
- * gradient written once (rows longer than a compute unit's registers hold, and
- * rows cut into parts, are read twice).
+ * gradient written once (rows cut into parts, and what of a row is beyond a
+ * compute unit's registers and LDS, from 26624 16-byte words on, are read
+ * twice).
  */
 int thd_policy_loss(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
                     const int64_t* labels, const uint8_t* mask, const float* old_logp, const float* ref_logp,

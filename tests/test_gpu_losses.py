@@ -380,6 +380,57 @@ def test_strides_and_places(torch, thd, rows, out, dtype, vocab, stride, offset)
             assert torch.isnan(pad).all() and torch.isnan(case.room[:offset]).all()
 
 
+@pytest.mark.parametrize("rows", [4, 700])
+def test_calls_of_the_c_names(torch, thd, rows):
+    # caller-owned outputs and workspaces, teacher rows with a stride of their own
+    say("c names", rows)
+    case = Case(torch, 21, 4, rows, 70001, "bf16", k=6)
+    v, z = case.vocab, case.logits
+    labels, mask, old, adv = (case.dev(x) for x in (case.labels, case.mask, case.old, case.adv))
+    f = lambda *n: torch.full(n, 7.0, device="cuda")
+    st = torch.full((1,), 99, dtype=torch.int32, device="cuda")
+    g = torch.empty_like(z)
+
+    def room(targets):
+        n = thd.thd_loss_workspace_bytes(rows, v, thd.THD_BF16, targets)
+        assert (n > 0) == (rows == 4)
+        return torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda"), n
+    ws, n = room(0)
+    logp, lse = f(rows), f(rows)
+    thd.thd_token_logprobs(z.data_ptr(), thd.THD_BF16, rows, v, v, labels, mask, logp, lse, st, ws, n)
+    want = thd.token_logprobs(z, labels, mask=mask)
+    assert torch.equal(logp, want[0]) and torch.equal(lse, want[1]) and int(st.item()) == 0
+    thd.thd_token_logprobs_backward(adv, z.data_ptr(), thd.THD_BF16, rows, v, v, labels, lse, mask, g.data_ptr(), v)
+    assert torch.equal(g, thd.token_logprobs_backward(adv, z, labels, lse, mask=mask))
+    ws, n = room(1)
+    loss = f(rows)
+    thd.thd_policy_loss(z.data_ptr(), thd.THD_BF16, rows, v, v, labels, mask, old, None, adv, None, 0.2, 0.3, 0.0, loss,
+                        logp, g.data_ptr(), v, st, ws, n)
+    want = thd.policy_loss(z, labels, old, adv, mask=mask, clip_high=0.3)
+    assert torch.equal(loss, want[0]) and torch.equal(logp, want[1]) and torch.equal(g, want[2])
+    # no status word, no mask
+    thd.thd_policy_loss(z.data_ptr(), thd.THD_BF16, rows, v, v, labels, None, old, None, adv, None, 0.2, 0.3, 0.0, loss,
+                        logp, g.data_ptr(), v, None, ws, n)
+    assert torch.equal(g, thd.policy_loss(z, labels, old, adv, clip_high=0.3)[2])
+    ws, n = room(6)
+    teacher, ids = case.dev(case.teacher).contiguous(), case.dev(case.ids).to(torch.int32).contiguous()
+    wide_t = torch.full((rows, 11), float("nan"), device="cuda")
+    wide_i = torch.full((rows, 11), -77, dtype=torch.int32, device="cuda")
+    wide_t[:, :6], wide_i[:, :6] = teacher, ids
+    thd.thd_distill_topk(z.data_ptr(), thd.THD_BF16, rows, v, v, wide_t.data_ptr(), thd.THD_FP32, wide_i.data_ptr(), 4,
+                         6, 11, mask, None, 1.5, loss, g.data_ptr(), v, st, ws, n)
+    want = thd.distill_topk(z, teacher, ids, mask=mask, temperature=1.5)
+    assert torch.equal(loss, want[0]) and torch.equal(g, want[1]) and int(st.item()) == 0
+    cu = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+    pairs = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    n = thd.thd_preference_workspace_bytes(rows, 2)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    loss, rewards, d = f(1), f(1, 2), f(rows)
+    thd.thd_preference_loss(logp, old, mask, cu, 2, rows, pairs, 1, 0.1, 0.0, 1.0, loss, rewards, d, st, ws, n)
+    want = thd.preference_loss(logp, old, pairs, cu, mask=mask)
+    assert torch.equal(loss, want[0]) and torch.equal(rewards, want[1]) and torch.equal(d, want[2])
+
+
 def test_new_gradient_has_the_logits_shape(torch, thd):
     z = torch.randn((2, 3, 37), device="cuda", dtype=torch.bfloat16)
     y = torch.zeros((2, 3), dtype=torch.int64, device="cuda")
