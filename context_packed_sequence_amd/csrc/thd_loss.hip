@@ -314,16 +314,17 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
     }
     return;
   }
-  // a gradient row at another place within 16 bytes: element by element
-  const int64_t v0 = static_cast<int64_t>(part) * p.turns * kThreads * kPer + cut.head - shift * kPer;
-  const int64_t v1 = v0 + static_cast<int64_t>(p.turns) * kThreads * kPer;
-  const int32_t from = part == 0 ? 0 : static_cast<int32_t>(max(v0, static_cast<int64_t>(0)));
-  const int32_t to_v = part == p.parts - 1 ? r.vocab : static_cast<int32_t>(min(v1, static_cast<int64_t>(r.vocab)));
-  for (int32_t v = from + tid; v < to_v; v += kThreads) {
+  // a gradient row at another place within 16 bytes: element by element. Every
+  // element has one owner: the part that holds its word, or part 0 for the row's
+  // edge, head and tail, whose targets it lists.
+  const auto store = [&](int32_t v) {
     float g = coef * exp2_fast((Elem<T>::load(in + v) - base) * scale);
     if (kKind != kLossDistill && v == label) g = at_label(g);
     out[v] = Elem<T>::round(g);
-  }
+  };
+  const int32_t to_v = cut.head + end / 16 * kPer;
+  for (int32_t v = cut.head + max(begin, 0) / 16 * kPer + tid; v < to_v; v += kThreads) store(v);
+  if (part == 0 && tid < cut.edge) store(cut.edge_column(tid));
   if constexpr (kKind == kLossDistill) {
     __syncthreads();  // a target's element is stored again, after the first time
     put_targets<T, kThreads>(s_list, out, coef, base, scale, amount);
