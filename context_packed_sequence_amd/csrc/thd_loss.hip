@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(LogitRows r, LossAr
     if (kKind != kLossDistill && part == 0) p.targets[row] = z_label;
   } else {
     a.logp[row] = join_label(st, z_label, scale).logp;
-    a.lse[row] = st.m + logf(st.s);
+    a.lse[row] = log_sum_exp(st);
   }
 }
 
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(64) void logp_join_kernel(LogitRows r, LossArgs a, 
   } else if (live) {
     Stat st = join_parts(p, row, kLog2e);
     logp = join_label(st, p.targets[row], kLog2e).logp;
-    lse = st.m + logf(st.s);
+    lse = log_sum_exp(st);
   }
   if (threadIdx.x == 0) {
     a.logp[row] = logp;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
   float base, coef, amount;
   float label_gradient = 0.0f;
   if constexpr (kKind == kLossLogp) {
-    base = base_of(a.lse_in[row]);
+    base = a.lse_in[row];  // NaN where the row has no softmax
     amount = -a.dlogp[row];
     coef = amount;
   } else {

@@ -405,6 +405,12 @@ __device__ __forceinline__ LabelJoin join_label(Stat& st, float z, float scale) 
   return j;
 }
 
+// Log-sum-exp of a whole row.  A row of nothing but -inf has no softmax: NaN, not
+// the -inf of the formula, which would make its gradient look like one.
+__device__ __forceinline__ float log_sum_exp(Stat st) {
+  return st.m == kNegInf ? __builtin_nanf("") : st.m + logf(st.s);
+}
+
 // Takes one element of a word out of the sum.
 template <int N>
 __device__ __forceinline__ void drop(float (&f)[N], int32_t place) {

@@ -81,7 +81,7 @@ int thd_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t 
 /*
  * thd_token_logprobs_backward -- gradient of sum_t dlogp[t] logp[t]:
  *   dlogits[t][v] = dlogp[t] ([v = y_t] - exp(z_v - lse_t)),
- * with lse as thd_token_logprobs wrote it.  One launch.
+ * with lse as thd_token_logprobs wrote it (NaN makes the row NaN).  One launch.
  */
 int thd_token_logprobs_backward(const float* dlogp, const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                                 int64_t row_stride, const int64_t* labels, const float* lse, const uint8_t* mask,
