@@ -482,7 +482,14 @@ struct PolicyRow {
   float loss, dlogp;
 };
 
-__device__ __forceinline__ float exp_minus_1_minus(float u) {
+// The KL term's exp(u) - 1 - u and its slope exp(u) - 1.  Each is formed on its
+// own: for u far below 0 the term is -u, and the slope, which is -1 there, would
+// not be found again in the term plus u.
+struct KlTerm {
+  float value, slope;
+};
+
+__device__ __forceinline__ KlTerm kl_term(float u) {
   if (fabsf(u) < 0.5f) {
     // u^2/2! + u^3/3! + ... + u^9/9!: the rest is below 2^-28 of the sum
     float t = 1.0f / 362880.0f;
@@ -493,9 +500,11 @@ __device__ __forceinline__ float exp_minus_1_minus(float u) {
     t = fmaf(t, u, 1.0f / 24.0f);
     t = fmaf(t, u, 1.0f / 6.0f);
     t = fmaf(t, u, 0.5f);
-    return t * u * u;
+    const float value = t * u * u;
+    return KlTerm{value, value + u};
   }
-  return exp2_fast(u * kLog2e) - 1.0f - u;
+  const float slope = exp2_fast(u * kLog2e) - 1.0f;
+  return KlTerm{slope - u, slope};
 }
 
 // What a row brings to it.
@@ -521,10 +530,9 @@ __device__ __forceinline__ PolicyRow policy_row(const LossArgs& a, const PolicyV
   float loss = -(clipped ? edge : ratio) * adv;
   float g = clipped ? 0.0f : -ratio * adv;
   if (a.ref_logp) {
-    const float u = v.ref_logp - logp;
-    const float k = exp_minus_1_minus(u);
-    loss = fmaf(a.kl_coef, k, loss);
-    g = fmaf(-a.kl_coef, k + u, g);
+    const KlTerm k = kl_term(v.ref_logp - logp);
+    loss = fmaf(a.kl_coef, k.value, loss);
+    g = fmaf(-a.kl_coef, k.slope, g);
   }
   return PolicyRow{v.weight * loss, v.weight * g};
 }

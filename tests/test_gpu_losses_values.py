@@ -34,3 +34,38 @@ def test_rows_without_a_softmax_stay_nan(torch, thd, rows, vocab, dtype):
         assert bool(torch.isnan(grad[i::5].float()).all())
     for i in (0, 4):
         assert bool(torch.isfinite(lse[i::5]).all()) and bool(torch.isfinite(grad[i::5].float()).all())
+
+
+@pytest.mark.parametrize("rows,vocab", SHAPES)
+def test_reference_without_probability(torch, thd, rows, vocab):
+    # u = ref - logp towards -inf: exp(u) - 1 goes to -1 however large the loss
+    say("reference", rows, vocab)
+    case = Case(torch, 41, 5, rows, vocab, "fp32")
+    case.mask[:] = 1
+    kl = 0.3
+    logp, _ = O.token_logprobs(case.z, case.labels)
+    case.ref = np.array([-np.inf, -3e38, -1e9, logp[3] - 40, logp[4] - 0.6], dtype=np.float32)
+    loss, got, grad, _ = thd.policy_loss(
+        case.logits, case.dev(case.labels), case.dev(case.old), case.dev(case.adv), ref_logp=case.dev(case.ref),
+        weights=case.dev(case.w), clip_low=0.2, clip_high=0.3, kl_coef=kl)
+    want = O.policy_loss(case.z, case.labels, case.old, case.adv, None, case.ref, case.w, 0.2, 0.3, kl)
+    assert np.isinf(want[0][0]) and np.isfinite(want[2]).all()
+    e_logp, _ = _logp_error(case.z, case.labels)
+    _within(_host(got), case.whole(want[1]), case.whole(e_logp), "logp")
+    r = np.exp(want[1] - case.old)
+    e_ratio = np.abs(case.adv) * r * (e_logp + (np.abs(want[1] - case.old) * 4 + 6) * U)
+    u = case.ref.astype(np.float64) - want[1]
+    with np.errstate(invalid="ignore"):
+        e_exp = np.where(u < -300, 0.0, np.exp(u) * (e_logp + (6 + 4 * np.abs(u)) * U))
+    e_d = case.w * (e_ratio + kl * (e_exp + 2 * U)) + 6 * U * case.w * (np.abs(case.adv) * r + kl)
+    e_loss = case.w * (e_ratio + 4 * U * 1.3 * np.abs(case.adv) + kl * (e_exp + e_logp)) + 8 * U * np.abs(want[0])
+    _within(_host(loss), case.whole(want[0]), case.whole(e_loss), "loss")
+    d = np.array([O.loss_oracle.policy_terms(want[1][t], case.old[t], case.adv[t], case.ref[t], case.w[t], 0.2, 0.3,
+                                             kl)[1] for t in range(5)])
+    z = case.z
+    soft = np.exp(z - z.max(1, keepdims=True))
+    soft /= soft.sum(1, keepdims=True)
+    label = np.arange(vocab) == case.labels[:, None]
+    rel = _sum_error(vocab) + (5 * np.abs(z - z.max(1, keepdims=True)) + 6) * U
+    bound = np.abs(d)[:, None] * (soft * rel + 8 * U * label) + e_d[:, None] * (soft + label) + U * np.abs(want[2])
+    _check_matrix(case, grad, want[2], bound + 2.0 ** -126, "gradient")
