@@ -736,7 +736,9 @@ __device__ __forceinline__ float distill_loss(const TargetList<kThreads>& l, con
     const float ln_q = exponent(l.z[i]) * kLn2 - ln_s;
     loss += l.p[i] * (l.ln_p[i] - ln_q);
   }
-  return a.temperature * a.temperature * w * wave_add(loss);
+  // tau goes in on both sides of the sum: its square may lie outside 32 bits
+  // where the loss does not
+  return a.temperature * w * wave_add(loss) * a.temperature;
 }
 
 // Takes a gradient word's targets from it: g[e] -= amount * sum.

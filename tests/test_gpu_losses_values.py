@@ -69,3 +69,24 @@ def test_reference_without_probability(torch, thd, rows, vocab):
     rel = _sum_error(vocab) + (5 * np.abs(z - z.max(1, keepdims=True)) + 6) * U
     bound = np.abs(d)[:, None] * (soft * rel + 8 * U * label) + e_d[:, None] * (soft + label) + U * np.abs(want[2])
     _check_matrix(case, grad, want[2], bound + 2.0 ** -126, "gradient")
+
+
+@pytest.mark.parametrize("rows,vocab", SHAPES)
+@pytest.mark.parametrize("tau,weight", [(2.0 ** -80, 2.0 ** 60), (2.0 ** 80, 2.0 ** -100)])
+def test_temperatures_whose_square_leaves_32_bits(torch, thd, rows, vocab, tau, weight):
+    # tau^2 itself is 2^-160 or 2^160; tau^2 w (ln p - ln q) is an ordinary number
+    say("temperature", rows, vocab, tau)
+    case = Case(torch, 42, 5, rows, vocab, "fp32", k=4)
+    case.mask[:] = 1
+    if tau < 1:
+        # far below any distance of two logits: p and q are the largest's alone
+        case.ids[:, 0] = case.z.argmin(1)
+        case.teacher[:, 0] = 9
+    case.w[:] = weight
+    loss, _, status = thd.distill_topk(case.logits, case.dev(case.teacher).contiguous(),
+                                       case.dev(case.ids).contiguous(), weights=case.dev(case.w), temperature=tau)
+    assert int(status.item()) == 0
+    want, _ = O.distill_topk(case.z, case.teacher.astype(np.float64), case.ids, None, case.w, tau)
+    assert (want > 2.0 ** -30).all() and (want < 2.0 ** 100).all()
+    # a sum of k terms, ln q of size ln V or |z - max| / tau, the sum behind it
+    _within(_host(loss), case.whole(want), case.whole((_sum_error(vocab) + 40 * U) * np.abs(want)), "loss")
