@@ -212,7 +212,8 @@ int thd_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vo
   if (k < 1 || k > THD_MAX_TOPK || (id_bytes != 4 && id_bytes != 8)) return THD_ERR_ARG;
   const auto tau = static_cast<float>(temperature);
   const auto inv = static_cast<float>(1.0 / temperature);
-  if (!(tau > 0.0f) || !std::isfinite(tau) || !std::isfinite(inv) || !(inv > 0.0f))
+  // the kernels multiply logits by log2(e) / tau
+  if (!(tau > 0.0f) || !std::isfinite(tau) || !std::isfinite(inv * 1.4426950408889634f) || !(inv > 0.0f))
     return THD_ERR_ARG;
   if (rows == 0) return init_status(status, stream);
   const int es = element_bytes(dtype);

@@ -118,7 +118,8 @@ int thd_policy_loss(const void* logits, int32_t dtype, int64_t rows, int64_t voc
  * (id_bytes 4) or int64 (id_bytes 8), rows teacher_stride elements apart in
  * both.  An id of -1, or a teacher logit of -inf, has no part in the sum; a row
  * without any part is as a masked one.  An id may occur more than once.
- * 1 <= k <= THD_MAX_TOPK, temperature > 0 and finite.
+ * 1 <= k <= THD_MAX_TOPK, temperature > 0 and finite, log2(e) / temperature finite
+ * in 32 bits (temperatures from 4.3e-39 on).
  * weights: float [rows] w, NULL: 1.  loss: float [rows] (output).
  */
 int thd_distill_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
