@@ -5,7 +5,9 @@ Rows are token positions of a packed stream, in natural or zigzag order;
 write (``shifted[j - 1]`` and ``mask[j]`` for shift j), documents the slots of
 ``cu_seqlens_padded``.  The gradient is returned beside the loss rather than
 through autograd: a model's backward starts from it with
-``logits.backward(dlogits)``.
+``logits.backward(dlogits)``.  ``out`` receives it where one is given; it may be
+the logits themselves, as long as no earlier operation needs them for its own
+backward (a cap by ``tanh`` does: autograd raises then).
 
 Logits are [rows, vocab] (leading dimensions are flattened where that takes no
 copy) in bfloat16, float16 or float32, their last dimension contiguous; rows
@@ -115,8 +117,13 @@ def _workspace(nbytes, device):
     return room, room.data_ptr()
 
 
-def _like(grad, x):
-    """The gradient in the logits' own shape."""
+def _hand_back(grad, x, out):
+    """The gradient in the logits' own shape, or ``out``, written through its
+    address: autograd is told, so that an operation which kept ``out`` for its
+    own backward reports that it has changed, as for any in-place operation."""
+    if out is not None:
+        torch.autograd.graph.increment_version(out)
+        return out
     return grad if x.dim() == 2 else grad.unflatten(0, x.shape[:-1])
 
 
@@ -167,7 +174,7 @@ def token_logprobs_backward(dlogp, logits, labels, lse, mask=None, out=None, str
             grad.data_ptr(), _stride(grad), handle)
         if code < 0:
             raise _b.ThdError(code, "thd_token_logprobs_backward")
-        return _like(grad, logits) if out is None else out
+        return _hand_back(grad, logits, out)
     return _run(call, stream)
 
 
@@ -206,7 +213,7 @@ def policy_loss(logits, labels, old_logp, advantages, mask=None, ref_logp=None, 
                                    nbytes, handle)
         if code < 0:
             raise _b.ThdError(code, "thd_policy_loss")
-        return loss, logp, _like(grad, logits) if out is None else out, status
+        return loss, logp, _hand_back(grad, logits, out), status
     return _run(call, stream)
 
 
@@ -251,7 +258,7 @@ def distill_topk(logits, teacher_logits, teacher_ids, mask=None, weights=None, t
                                     nbytes, handle)
         if code < 0:
             raise _b.ThdError(code, "thd_distill_topk")
-        return loss, _like(grad, logits) if out is None else out, status
+        return loss, _hand_back(grad, logits, out), status
     return _run(call, stream)
 
 

@@ -90,3 +90,26 @@ def test_temperatures_whose_square_leaves_32_bits(torch, thd, rows, vocab, tau, 
     assert (want > 2.0 ** -30).all() and (want < 2.0 ** 100).all()
     # a sum of k terms, ln q of size ln V or |z - max| / tau, the sum behind it
     _within(_host(loss), case.whole(want), case.whole((_sum_error(vocab) + 40 * U) * np.abs(want)), "loss")
+
+
+def test_gradient_in_place_of_saved_logits(torch, thd):
+    # an operation that keeps its result for its own backward notices that the
+    # gradient has replaced it
+    say("in place and autograd")
+    x = torch.randn((12, 500), device="cuda", requires_grad=True)
+    y = torch.zeros(12, dtype=torch.int64, device="cuda")
+    f = torch.zeros(12, device="cuda")
+    t, ids = torch.zeros((12, 2), device="cuda"), torch.zeros((12, 2), dtype=torch.int32, device="cuda")
+    for call in (lambda z: thd.policy_loss(z, y, f, f + 1, out=z)[2],
+                 lambda z: thd.distill_topk(z, t, ids, out=z)[1],
+                 lambda z: thd.token_logprobs_backward(f + 1, z, y, f + 7, out=z)):
+        capped = 30 * torch.tanh(x / 30)          # the product keeps nothing of its result
+        capped.backward(call(capped.detach()))
+        kept = torch.tanh(x)                      # its backward needs the result
+        grad = call(kept.detach())
+        assert grad.data_ptr() == kept.data_ptr()
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            kept.backward(grad)
+    with torch.inference_mode():
+        z = torch.randn((12, 500), device="cuda")
+        assert thd.policy_loss(z, y, f, f + 1, out=z)[2] is z
