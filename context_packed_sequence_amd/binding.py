@@ -1,9 +1,11 @@
 """ctypes binding of libthdcp (include/thd_cp.h).
 
 Argument marshalling only: every step of the route build, the swap, the label
-roll and the losses (include/thd_loss.h) runs in the library's HIP kernels.  Torch is used for device
-memory and streams: tensors are passed as their ``data_ptr()``, streams as
-``torch.cuda.current_stream().cuda_stream`` unless one is given.
+roll and the losses (include/thd_loss.h) runs in the library's HIP kernels.
+Torch is used for device memory and streams, where it is installed: tensors are
+passed as their ``data_ptr()``, streams as
+``torch.cuda.current_stream().cuda_stream`` unless one is given.  It is loaded
+before the library, whose HIP runtime is then torch's.
 
 The functions keep the C names.  Negative return codes raise ``ThdError``;
 ``thd_swap`` returns ``THD_IDENTITY`` (1) when nothing was written.
@@ -18,7 +20,12 @@ import ctypes
 import os
 
 import numpy as np
-import torch  # noqa: F401  before the library: the HIP runtime torch brings has to be the process's only one
+
+try:  # before the library: the HIP runtime torch brings has to be the process's only one
+    import torch  # noqa: F401
+except ModuleNotFoundError as e:  # a process without torch: addresses and a stream of the caller's own
+    if e.name != "torch":
+        raise
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libthdcp.so")
 
