@@ -182,8 +182,6 @@ struct RowCut {
   __device__ __forceinline__ int32_t edge_of(int32_t v) const { return v < head ? v : v - words * Elem<T>::kPer; }
 };
 
-__device__ __forceinline__ Word4 load_word(const Word4* p) { return __builtin_nontemporal_load(p); }
-
 // The words of a row behind a buffer resource of exactly their size: a load
 // past either end gives zeros and a store there is dropped, both in hardware,
 // so that the loops over a thread's words have no branches and every load of a
