@@ -314,7 +314,8 @@ __global__ __launch_bounds__(kThreads) void part_grad_kernel(LogitRows r, LossAr
     }
     return;
   }
-  // a gradient row at another place within 16 bytes: element by element. Every
+  // a gradient row at another place within 16 bytes: element by element (of the
+  // log-probabilities, 8192 x 50257 bf16: 554 us against 271 for rows alike). Every
   // element has one owner: the part that holds its word, or part 0 for the row's
   // edge, head and tail, whose targets it lists.
   const auto store = [&](int32_t v) {

@@ -81,7 +81,11 @@ int thd_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t 
 /*
  * thd_token_logprobs_backward -- gradient of sum_t dlogp[t] logp[t]:
  *   dlogits[t][v] = dlogp[t] ([v = y_t] - exp(z_v - lse_t)),
- * with lse as thd_token_logprobs wrote it (NaN makes the row NaN).  One launch.
+ * with lse as thd_token_logprobs wrote it (NaN makes the row NaN).  The softmax is
+ * taken against lse as it is given, a 32-bit number: the label's element is off by
+ * up to about 2^-24 (|lse| + 4) |dlogp|, which is all of it for a label within that
+ * of certainty (thd_policy_loss keeps the relative precision of 1 - q_y).  One
+ * launch.
  */
 int thd_token_logprobs_backward(const float* dlogp, const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                                 int64_t row_stride, const int64_t* labels, const float* lse, const uint8_t* mask,
@@ -150,6 +154,11 @@ int64_t thd_preference_workspace_bytes(int64_t total_tokens, int32_t n_slots);
  * THD_ERR_CU_MONOTONE, THD_ERR_CU_TOTAL: nothing else is written then), or
  * THD_ERR_PAIR if a pair names no slot: its loss and rewards are NaN and it has
  * no part in dlogp.  Two launches.
+ * Cost: a few bytes a token for documents of up to some 100000 tokens in a few
+ * pairs each.  Beyond, each 512 tokens of a document add up the partial sums of
+ * both documents of each of its pairs again, and every piece of a document within
+ * 512 tokens looks through all pairs: the time grows with the square of a
+ * document's length times its pairs, and with documents times pairs.
  */
 int thd_preference_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
                         const int32_t* cu_seqlens_padded, int32_t n_slots, int64_t total_tokens,
