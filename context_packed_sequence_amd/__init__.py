@@ -41,6 +41,7 @@ from .binding import (  # noqa: F401
     THD_FP32,
     THD_IDENTITY,
     THD_MAX_BATCH,
+    THD_MAX_HEAD_DIM,
     THD_MAX_PAIRS,
     THD_MAX_TOPK,
     THD_MAX_VOCAB,
@@ -50,9 +51,14 @@ from .binding import (  # noqa: F401
     THD_OK,
     THD_ZIGZAG_TO_CONTIGUOUS,
     ThdError,
+    thd_attention,
+    thd_attention_backward,
+    thd_attention_shape,
+    thd_attention_workspace_bytes,
     thd_build_route,
     thd_copy,
     thd_distill_topk,
+    thd_heads,
     thd_loss_workspace_bytes,
     thd_policy_loss,
     thd_preference_loss,
@@ -248,6 +254,7 @@ def pack(tokens, pad_id: int, eod_id: int, align: int, capacity: int, max_docs: 
 
 
 try:
+    from .attention import packed_attention, packed_attention_backward  # noqa: F401
     from .losses import (  # noqa: F401
         distill_topk,
         policy_loss,

@@ -64,6 +64,7 @@ THD_FP32 = 2
 THD_MAX_VOCAB = 268435456
 THD_MAX_TOPK = 256
 THD_MAX_PAIRS = 65536
+THD_MAX_HEAD_DIM = 128
 
 EXPORTS = (
     "thd_route_create", "thd_route_destroy", "thd_build_route", "thd_swap", "thd_roll_labels",
@@ -72,7 +73,21 @@ EXPORTS = (
     "thd_route_launch_shape", "thd_read_stream", "thd_write_stream", "thd_pack_noalloc",
     "thd_loss_workspace_bytes", "thd_token_logprobs", "thd_token_logprobs_backward", "thd_policy_loss",
     "thd_distill_topk", "thd_preference_workspace_bytes", "thd_preference_loss",
+    "thd_attention_workspace_bytes", "thd_attention", "thd_attention_backward",
 )
+
+
+class thd_heads(ctypes.Structure):
+    """One [rows][heads][dim] tensor: address, elements from row to row and from head to head."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class thd_attention_shape(ctypes.Structure):
+    """What a forward call and its backward call have in common (include/thd_attention.h)."""
+    _fields_ = [*[(name, ctypes.c_int32) for name in ("dtype", "heads", "kv_heads", "dim", "causal", "window",
+                                                      "cp_size", "rank", "n_slots")],
+                ("total_tokens", ctypes.c_int64), ("scale", ctypes.c_double), ("cap", ctypes.c_double),
+                ("cu_seqlens_padded", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p)]
 
 
 class ThdError(RuntimeError):
@@ -90,6 +105,7 @@ def _load() -> ctypes.CDLL:
     c_i32, c_i64, c_p, c_f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
     logits = [c_p, c_i32, c_i64, c_i64, c_i64]       # pointer, dtype, rows, vocab, row_stride
     work = [c_p, c_i64, c_p]                         # workspace, workspace_bytes, stream
+    shape, heads = ctypes.POINTER(thd_attention_shape), ctypes.POINTER(thd_heads)
     sig = {
         "thd_route_create": (ctypes.c_int, [c_i32, c_i32, c_i64, ctypes.POINTER(c_p)]),
         "thd_route_destroy": (None, [c_p]),
@@ -124,6 +140,10 @@ def _load() -> ctypes.CDLL:
         "thd_preference_workspace_bytes": (ctypes.c_int64, [c_i64, c_i32]),
         "thd_preference_loss": (ctypes.c_int, [c_p, c_p, c_p, c_p, c_i32, c_i64, c_p, c_i32, c_f64, c_f64, c_f64,
                                                c_p, c_p, c_p, c_p, *work]),
+        "thd_attention_workspace_bytes": (ctypes.c_int64, [shape, c_i32]),
+        "thd_attention": (ctypes.c_int, [shape, heads, heads, heads, heads, c_p, c_p, *work]),
+        "thd_attention_backward": (ctypes.c_int, [shape, heads, heads, heads, heads, c_p, heads, heads, heads, heads,
+                                                  c_p, *work]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -340,6 +360,27 @@ def thd_preference_loss(logp, ref_logp, mask, cu_seqlens_padded, n_slots: int, t
                                            total_tokens, _ptr(pairs), n_pairs, beta, label_smoothing, scale,
                                            _ptr(loss), _ptr(rewards), _ptr(dlogp), _ptr(status), _ptr(workspace),
                                            workspace_bytes, _stream(stream)), "thd_preference_loss")
+
+
+# ---- attention (include/thd_attention.h), same names --------------------------
+# Shapes and tensors are the structures above: views may be strided.
+
+def thd_attention_workspace_bytes(shape, backward: int) -> int:
+    return int(_lib.thd_attention_workspace_bytes(ctypes.byref(shape), backward))
+
+
+def thd_attention(shape, q, k, v, out, lse, status, workspace, workspace_bytes: int, stream=None) -> int:
+    ref = ctypes.byref
+    return _check(_lib.thd_attention(ref(shape), ref(q), ref(k), ref(v), ref(out), _ptr(lse), _ptr(status),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)), "thd_attention")
+
+
+def thd_attention_backward(shape, q, k, v, out, lse, dout, dq, dk, dv, status, workspace, workspace_bytes: int,
+                           stream=None) -> int:
+    ref = ctypes.byref
+    return _check(_lib.thd_attention_backward(ref(shape), ref(q), ref(k), ref(v), ref(out), _ptr(lse), ref(dout),
+                                              ref(dq), ref(dk), ref(dv), _ptr(status), _ptr(workspace),
+                                              workspace_bytes, _stream(stream)), "thd_attention_backward")
 
 
 def library():

@@ -1,0 +1,442 @@
+// Gradients of the attention inside documents.  With p as in the forward pass
+// (formed again from q, k and the row's log-sum-exp):
+//   dp_ij = dout_i . v_j,   delta_i = sum_j p_ij dp_ij = dout_i . out_i
+//   dz_ij = p_ij (dp_ij - delta_i) (1 - (z_ij / cap)^2)       (cap > 0)
+//   dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i dz_ij q_i,  dq_i = scale sum_j dz_ij k_j
+//
+// Query gradients and key gradients come from two kernels, each of which owns
+// its rows and adds in a fixed order; scores and dp are formed in both, seven
+// products instead of five, against atomic additions into 32-bit sums whose order
+// would change the results.  Both hold a wave's own 32 rows (queries and dout, or
+// keys and values) in registers as B operands, so that p and dz come out of the
+// products as operands of the next ones, and move the other side's rows
+// through LDS, 64 at a time.
+//
+// fp16: p times 2^10 and dz times a power of two for which no dz passes the
+// type's range (from the largest norms of a dout row and of a v row) keep small
+// factors out of the subnormals; the sums are scaled back.
+#include "thd_attn_device.h"
+
+namespace thdcp {
+
+namespace {
+
+constexpr float kProbabilityScale = 1024.0f;  // of fp16 probabilities
+
+// Power of two by which fp16 score gradients are held: |dz| <= 2 |dout| |v|.
+__device__ __forceinline__ float gradient_scale(const AttnPlan& p) {
+  const float bound = 2.0f * __builtin_bit_cast(float, p.header[kAttnMaxGrad]) *
+                      __builtin_bit_cast(float, p.header[kAttnMaxValue]);
+  if (!(bound > 0.0f) || !(bound < kAttnInf)) return 1.0f;
+  return ldexpf(1.0f, 14 - ilogbf(bound) - 1);  // bound times it is below 2^14
+}
+
+// 16 lanes add up.
+__device__ __forceinline__ float add_row16(float x) {
+#pragma unroll
+  for (int i = 1; i < 16; i <<= 1) x += __shfl_xor(x, i);
+  return x;
+}
+
+// delta of a tile's rows, 16 lanes a row, and the largest norms for fp16.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t query_blocks) {
+  __shared__ float s_most[4];
+  const int32_t l = threadIdx.x & 63, word = l & 15;
+  float most = 0.0f;
+  if (static_cast<int32_t>(blockIdx.x) < query_blocks) {
+    const int32_t index = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    if (index >= a.plan.header[kAttnQueryTiles]) return;
+    const QueryTile tile = a.plan.query_tiles[index];
+    const RowsRead o(head_rows(a.out, tile.row, head), static_cast<int32_t>(2 * a.out.row), tile.valid, a.dim);
+    const RowsRead g(head_rows(a.dout, tile.row, head), static_cast<int32_t>(2 * a.dout.row), tile.valid, a.dim);
+    float* delta = a.plan.delta + static_cast<int64_t>(head) * a.rows + tile.row;
+#pragma unroll
+    for (int i = 0; i < kAttnRows / 16; ++i) {
+      const int32_t row = 16 * i + (threadIdx.x >> 4);
+      const U32x4 x = o.load(row, word, a.dim), y = g.load(row, word, a.dim);
+      float dot = 0.0f, square = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t u = x[k], v = y[k];
+        dot = fmaf(T::low(u), T::low(v), dot);
+        dot = fmaf(T::high(u), T::high(v), dot);
+        if constexpr (T::kNarrow) {
+          square = fmaf(T::low(v), T::low(v), square);
+          square = fmaf(T::high(v), T::high(v), square);
+        }
+      }
+      dot = add_row16(dot);
+      if (word == 0 && row < tile.valid) delta[row] = dot;
+      if constexpr (T::kNarrow) most = fmaxf(most, add_row16(square));
+    }
+  } else if constexpr (T::kNarrow) {
+    const int32_t b = blockIdx.x - query_blocks;
+    const int32_t index = b / a.kv_heads, head = b % a.kv_heads;
+    if (index >= a.plan.header[kAttnKeyTiles]) return;
+    const KeyTile tile = a.plan.key_tiles[index];
+    const RowsRead v(head_rows(a.v, static_cast<int64_t>(tile.doc) + tile.key, head),
+                     static_cast<int32_t>(2 * a.v.row), tile.valid, a.dim);
+#pragma unroll
+    for (int i = 0; i < kAttnKeys / 16; ++i) {
+      const U32x4 x = v.load(16 * i + (threadIdx.x >> 4), word, a.dim);
+      float square = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t u = x[k];
+        square = fmaf(T::low(u), T::low(u), square);
+        square = fmaf(T::high(u), T::high(u), square);
+      }
+      most = fmaxf(most, add_row16(square));
+    }
+  }
+  if constexpr (T::kNarrow) {
+#pragma unroll
+    for (int i = 16; i < 64; i <<= 1) most = fmaxf(most, __shfl_xor(most, i));
+    if (l == 0) s_most[threadIdx.x >> 6] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      most = sqrtf(fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3])));
+      // not negative: floats order as their bits do, and a maximum has no order
+      const bool query = static_cast<int32_t>(blockIdx.x) < query_blocks;
+      if (most > 0.0f)
+        atomicMax(a.plan.header + (query ? kAttnMaxGrad : kAttnMaxValue), __builtin_bit_cast(int32_t, most));
+    }
+  }
+}
+
+// What both kernels make of a block of scores and dp (32 x 32, one row a
+// register): p, and dz times `held`.  lse and delta are the registers' or the
+// lane's, by the caller's functions of the register; scores not seen have p 0.
+template <typename T, bool kCap, typename Lse, typename Delta, typename Visible>
+__device__ __forceinline__ void score_gradients(const AttnArgs& a, F32x16& s, F32x16& dp, float held, Lse lse,
+                                                Delta delta, Visible visible, U32x4 (&p16)[2], U32x4 (&dz16)[2]) {
+  const float factor = (kCap ? a.cap : a.scale) * kAttnLog2e;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float z = s[r], slope = held;
+    if constexpr (kCap) {
+      z = attn_tanh(z * (a.scale / a.cap));
+      slope = held * fmaf(-z, z, 1.0f);
+    }
+    const float p = visible(r) ? attn_exp2(fmaf(z, factor, -lse(r))) : 0.0f;
+    s[r] = T::kNarrow ? p * kProbabilityScale : p;
+    dp[r] = p * (dp[r] - delta(r)) * slope;
+  }
+#pragma unroll
+  for (int r = 0; r < 16; r += 2) {
+    p16[r >> 3][(r & 7) >> 1] = T::pack(s[r], s[r + 1]);
+    dz16[r >> 3][(r & 7) >> 1] = T::pack(dp[r], dp[r + 1]);
+  }
+}
+
+// acc [dim][32] += (rows [row, row + 32) of the tile)^T b
+template <typename T, int kDim>
+__device__ __forceinline__ void add_transposed(F32x16 (&acc)[kDim / 32], const char* tile,
+                                               const int32_t (&at)[kDim / 32][2], const U32x4 (&b)[2]) {
+#pragma unroll
+  for (int t = 0; t < kDim / 32; ++t)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const U32x2 x = lds_read_transposed(tile + at[t][0] + j * 16 * 2 * kDim);
+      const U32x2 y = lds_read_transposed(tile + at[t][1] + j * 16 * 2 * kDim);
+      acc[t] = T::mfma(U32x4{x[0], x[1], y[0], y[1]}, b[j], acc[t]);
+    }
+}
+
+template <typename T, int kDim>
+__device__ __forceinline__ F32x16 product(const char* tile, const int32_t (&at)[kDim / 16],
+                                          const U32x4 (&b)[kDim / 16]) {
+  F32x16 c = zero16();
+#pragma unroll
+  for (int i = 0; i < kDim / 16; ++i) c = T::mfma(lds_read(tile, at[i]), b[i], c);
+  return c;
+}
+
+// Query gradients: 128 query rows of one head a workgroup, as in the forward
+// pass.
+template <typename T, int kDim, bool kCap>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
+  constexpr int kTile = kAttnStep * 2 * kDim;
+  __shared__ __attribute__((aligned(16))) char s_keys0[kTile], s_values0[kTile], s_keys1[kTile], s_values1[kTile];
+  const AttnPlace place(blockIdx.x, a.kv_heads, a.group);
+  if (place.tile >= a.plan.header[kAttnQueryTiles]) return;
+  const QueryTile tile = a.plan.query_tiles[place.tile];
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t l = threadIdx.x & 63, c = l & 31, h = l >> 5;
+  const int32_t own_rows = min(32, max(0, tile.rows - 32 * wave));
+  const int32_t own_valid = min(32, max(0, tile.valid - 32 * wave));
+  const int32_t pos = tile.pos + 32 * wave;
+  const float held = T::kNarrow ? gradient_scale(a.plan) : 1.0f;
+
+  F32x16 dq[kDim / 32];
+#pragma unroll
+  for (int t = 0; t < kDim / 32; ++t) dq[t] = zero16();
+  if (tile.valid > 0) {
+    U32x4 q[kDim / 16], g[kDim / 16];
+    int32_t row_at[kDim / 16], column_at[kDim / 32][2];
+    const RowsRead queries(head_rows(a.q, tile.row + 32 * wave, place.head), static_cast<int32_t>(2 * a.q.row),
+                           own_valid, a.dim);
+    const RowsRead grads(head_rows(a.dout, tile.row + 32 * wave, place.head), static_cast<int32_t>(2 * a.dout.row),
+                         own_valid, a.dim);
+#pragma unroll
+    for (int i = 0; i < kDim / 16; ++i) {
+      q[i] = queries.load(c, 2 * i + h, a.dim);
+      g[i] = grads.load(c, 2 * i + h, a.dim);
+      row_at[i] = lds_word<kDim>(c, 2 * i + h);
+    }
+#pragma unroll
+    for (int t = 0; t < kDim / 32; ++t) {
+      column_at[t][0] = transposed_at<kDim>(t, 0);
+      column_at[t][1] = transposed_at<kDim>(t, 1);
+    }
+    float lse = kAttnInf, delta = 0.0f;  // of a row that sees nothing: p 0
+    if (c < own_valid) {
+      const int64_t at = static_cast<int64_t>(place.head) * a.rows + tile.row + 32 * wave + c;
+      const float x = a.lse[at] * kAttnLog2e;
+      lse = x == -kAttnInf ? kAttnInf : x;
+      delta = a.plan.delta[at];
+    }
+    const Seen first(a, tile.pos, tile.real), last(a, tile.pos + tile.valid - 1, tile.real);
+    const int32_t end = last.low + static_cast<int32_t>(last.span);
+    int32_t key = first.low & ~(kAttnStep - 1);
+    const Seen seen(a, pos + c, tile.real);
+    const auto load = [&](char* keys, char* values, int32_t at) {
+      const int32_t n = min(kAttnStep, tile.real - at);
+      load_tile<kDim>(keys, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+                                     static_cast<int32_t>(2 * a.k.row), n, a.dim), a.dim);
+      load_tile<kDim>(values, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+                                       static_cast<int32_t>(2 * a.v.row), n, a.dim), a.dim);
+    };
+    const auto turn = [&](const char* keys, const char* values, char* next_keys, char* next_values) {
+      lds_arrived();
+      __syncthreads();
+      if (key + kAttnStep < end) load(next_keys, next_values, key + kAttnStep);
+#pragma unroll
+      for (int b = 0; b < kAttnStep / 32; ++b) {
+        const int32_t k0 = key + 32 * b, at = 32 * b * 2 * kDim;
+        if (own_valid <= 0 || !sees_any(a, pos, own_valid, k0, 32, tile.real)) continue;
+        F32x16 s = product<T, kDim>(keys + at, row_at, q);
+        F32x16 dp = product<T, kDim>(values + at, row_at, g);
+        U32x4 p16[2], dz16[2];
+        const bool all = sees_all(a, pos, 32, k0, 32, tile.real);
+        const auto lane_lse = [&](int) { return lse; };
+        const auto lane_delta = [&](int) { return delta; };
+        if (all)
+          score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta, [](int) { return true; }, p16, dz16);
+        else
+          score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta,
+                                   [&](int r) { return seen(k0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
+        add_transposed<T, kDim>(dq, keys + at, column_at, dz16);
+      }
+      key += kAttnStep;
+    };
+    load(s_keys0, s_values0, key);
+    while (key < end) {
+      turn(s_keys0, s_values0, s_keys1, s_values1);
+      if (key >= end) break;
+      turn(s_keys1, s_values1, s_keys0, s_values0);
+    }
+    __syncthreads();
+  }
+  char* own = wave == 0 ? s_keys0 : wave == 1 ? s_values0 : wave == 2 ? s_keys1 : s_values1;
+  store_rows<T, kDim>(own, dq, a.scale / held, const_cast<char*>(head_rows(a.dq, tile.row + 32 * wave, place.head)),
+                      2 * a.dq.row, own_rows, own_valid, a.dim);
+}
+
+// The query rows that a key tile's gradients come from: for each head of the
+// group, of each of the document's chunks the rows that see the tile, 64 at a
+// time.
+struct QueryWalk {
+  int32_t head, chunk, row, end;    // row, end: within the chunk
+  int32_t first_head, heads, chunks;
+  __device__ __forceinline__ void range(const AttnArgs& a, const KeyTile& k) {
+    const int32_t pos = position(a, k);
+    const int32_t valid = max(0, min(k.chunk, k.real - pos));
+    const int32_t low = a.causal ? k.key : a.window ? max(0, k.key - a.window + 1) : 0;
+    const int64_t high = a.window ? static_cast<int64_t>(k.key) + k.valid + a.window - 1 : k.real;
+    row = max(0, low - pos);
+    end = static_cast<int32_t>(max<int64_t>(0, min<int64_t>(valid, high - pos)));
+  }
+  __device__ __forceinline__ int32_t position(const AttnArgs& a, const KeyTile& k) const {
+    return a.cp == 1 ? 0 : chunk ? (2 * a.cp - 1 - a.rank) * k.chunk : a.rank * k.chunk;
+  }
+  __device__ __forceinline__ bool done() const { return head >= first_head + heads; }
+  __device__ __forceinline__ void settle(const AttnArgs& a, const KeyTile& k) {
+    while (!done() && row >= end) {
+      if (++chunk == chunks) {
+        chunk = 0;
+        if (++head >= first_head + heads) return;
+      }
+      range(a, k);
+    }
+  }
+  __device__ __forceinline__ QueryWalk(const AttnArgs& a, const KeyTile& k, int32_t kv_head)
+      : head(kv_head * a.group), chunk(0), first_head(kv_head * a.group), heads(a.group), chunks(a.cp == 1 ? 1 : 2) {
+    range(a, k);
+    settle(a, k);
+  }
+  __device__ __forceinline__ void next(const AttnArgs& a, const KeyTile& k) {
+    row += kAttnStep;
+    settle(a, k);
+  }
+};
+
+// Key and value gradients: 128 keys of one key head a workgroup, 32 a wave.
+template <typename T, int kDim, bool kCap>
+__global__ __launch_bounds__(256, kDim == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
+  constexpr int kTile = kAttnStep * 2 * kDim;
+  __shared__ __attribute__((aligned(16))) char s_queries0[kTile], s_grads0[kTile], s_queries1[kTile], s_grads1[kTile];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][kAttnStep], s_delta[2][kAttnStep];
+  const AttnPlace place(blockIdx.x, a.kv_heads, 1);
+  if (place.tile >= a.plan.header[kAttnKeyTiles]) return;
+  const KeyTile tile = a.plan.key_tiles[place.tile];
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t l = threadIdx.x & 63, c = l & 31, h = l >> 5;
+  const int32_t own_keys = min(32, max(0, tile.keys - 32 * wave));
+  const int32_t own_valid = min(32, max(0, tile.valid - 32 * wave));
+  const int32_t key = tile.key + 32 * wave;
+  const int64_t stream = static_cast<int64_t>(tile.doc) + key;
+  const float held = T::kNarrow ? gradient_scale(a.plan) : 1.0f;
+
+  F32x16 dk[kDim / 32], dv[kDim / 32];
+#pragma unroll
+  for (int t = 0; t < kDim / 32; ++t) dk[t] = dv[t] = zero16();
+  if (tile.valid > 0) {
+    U32x4 k[kDim / 16], v[kDim / 16];
+    int32_t row_at[kDim / 16], column_at[kDim / 32][2];
+    const RowsRead keys(head_rows(a.k, stream, place.kv_head), static_cast<int32_t>(2 * a.k.row), own_valid, a.dim);
+    const RowsRead values(head_rows(a.v, stream, place.kv_head), static_cast<int32_t>(2 * a.v.row), own_valid, a.dim);
+#pragma unroll
+    for (int i = 0; i < kDim / 16; ++i) {
+      k[i] = keys.load(c, 2 * i + h, a.dim);
+      v[i] = values.load(c, 2 * i + h, a.dim);
+      row_at[i] = lds_word<kDim>(c, 2 * i + h);
+    }
+#pragma unroll
+    for (int t = 0; t < kDim / 32; ++t) {
+      column_at[t][0] = transposed_at<kDim>(t, 0);
+      column_at[t][1] = transposed_at<kDim>(t, 1);
+    }
+    QueryWalk walk(a, tile, place.kv_head);
+    // positions that see key key + c
+    const Seen seen(a.causal ? key + c : a.window ? key + c - a.window + 1 : 0,
+                    a.window ? (a.causal ? a.window : 2u * a.window - 1u) : 0x7fffffffu);
+    float next_lse = kAttnInf, next_delta = 0.0f;
+    const auto load = [&](char* queries, char* grads) {
+      const int32_t n = min(kAttnStep, walk.end - walk.row);
+      const int64_t row = static_cast<int64_t>(tile.first) + walk.chunk * tile.chunk + walk.row;
+      load_tile<kDim>(queries, RowsRead(head_rows(a.q, row, walk.head), static_cast<int32_t>(2 * a.q.row), n, a.dim),
+                      a.dim);
+      load_tile<kDim>(grads, RowsRead(head_rows(a.dout, row, walk.head), static_cast<int32_t>(2 * a.dout.row), n,
+                                      a.dim), a.dim);
+      next_lse = kAttnInf;  // rows past the range: p 0
+      next_delta = 0.0f;
+      if (static_cast<int32_t>(threadIdx.x) < n) {
+        const int64_t at = static_cast<int64_t>(walk.head) * a.rows + row + threadIdx.x;
+        const float x = a.lse[at] * kAttnLog2e;
+        next_lse = x == -kAttnInf ? kAttnInf : x;
+        next_delta = a.plan.delta[at];
+      }
+    };
+    const auto turn = [&](const char* queries, const char* grads, int32_t mine, char* next_queries,
+                          char* next_grads) {
+      if (threadIdx.x < kAttnStep) {
+        s_lse[mine][threadIdx.x] = next_lse;
+        s_delta[mine][threadIdx.x] = next_delta;
+      }
+      lds_arrived();
+      __syncthreads();
+      const int32_t n = min(kAttnStep, walk.end - walk.row);
+      const int32_t pos = walk.position(a, tile) + walk.row;
+      walk.next(a, tile);
+      if (!walk.done()) load(next_queries, next_grads);
+#pragma unroll
+      for (int b = 0; b < kAttnStep / 32; ++b) {
+        const int32_t p0 = pos + 32 * b, at = 32 * b * 2 * kDim;
+        if (32 * b >= n || own_valid <= 0 || !sees_any(a, p0, min(32, n - 32 * b), key, own_valid, tile.real)) continue;
+        F32x16 s = product<T, kDim>(queries + at, row_at, k);
+        F32x16 dp = product<T, kDim>(grads + at, row_at, v);
+        float lse[16], delta[16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_lse[mine][32 * b + 8 * g + 4 * h]);
+          const float4 y = *reinterpret_cast<const float4*>(&s_delta[mine][32 * b + 8 * g + 4 * h]);
+          lse[4 * g] = x.x, lse[4 * g + 1] = x.y, lse[4 * g + 2] = x.z, lse[4 * g + 3] = x.w;
+          delta[4 * g] = y.x, delta[4 * g + 1] = y.y, delta[4 * g + 2] = y.z, delta[4 * g + 3] = y.w;
+        }
+        U32x4 p16[2], dz16[2];
+        const auto row_lse = [&](int r) { return lse[r]; };
+        const auto row_delta = [&](int r) { return delta[r]; };
+        // pads among the keys are other lanes' and are not stored
+        if (sees_all(a, p0, 32, key, 32, INT32_MAX))
+          score_gradients<T, kCap>(a, s, dp, held, row_lse, row_delta, [](int) { return true; }, p16, dz16);
+        else
+          score_gradients<T, kCap>(a, s, dp, held, row_lse, row_delta,
+                                   [&](int r) { return seen(p0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
+        add_transposed<T, kDim>(dv, grads + at, column_at, p16);
+        add_transposed<T, kDim>(dk, queries + at, column_at, dz16);
+      }
+    };
+    if (!walk.done()) load(s_queries0, s_grads0);
+    while (!walk.done()) {
+      turn(s_queries0, s_grads0, 0, s_queries1, s_grads1);
+      if (walk.done()) break;
+      turn(s_queries1, s_grads1, 1, s_queries0, s_grads0);
+    }
+    __syncthreads();
+  }
+  char* own = wave == 0 ? s_queries0 : wave == 1 ? s_grads0 : wave == 2 ? s_queries1 : s_grads1;
+  store_rows<T, kDim>(own, dk, a.scale / held, const_cast<char*>(head_rows(a.dk, stream, place.kv_head)),
+                      2 * a.dk.row, own_keys, own_valid, a.dim);
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  store_rows<T, kDim>(own, dv, T::kNarrow ? 1.0f / kProbabilityScale : 1.0f,
+                      const_cast<char*>(head_rows(a.dv, stream, place.kv_head)), 2 * a.dv.row, own_keys, own_valid,
+                      a.dim);
+}
+
+template <typename T>
+hipError_t delta(const AttnArgs& a, hipStream_t stream) {
+  const int32_t query_blocks = a.plan.max_query_tiles * a.heads;
+  const int32_t blocks = query_blocks + (T::kNarrow ? a.plan.max_key_tiles * a.kv_heads : 0);
+  attn_delta_kernel<T><<<blocks, 256, 0, stream>>>(a, query_blocks);
+  return hipGetLastError();
+}
+
+template <typename T, int kDim>
+hipError_t dq(const AttnArgs& a, hipStream_t stream) {
+  const int32_t units = a.plan.max_query_tiles * a.kv_heads;
+  const dim3 grid((units + 7) / 8 * 8 * a.group);
+  if (a.cap > 0.0f) attn_dq_kernel<T, kDim, true><<<grid, 256, 0, stream>>>(a);
+  else attn_dq_kernel<T, kDim, false><<<grid, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int kDim>
+hipError_t dkv(const AttnArgs& a, hipStream_t stream) {
+  const int32_t units = a.plan.max_key_tiles * a.kv_heads;
+  const dim3 grid((units + 7) / 8 * 8);
+  if (a.cap > 0.0f) attn_dkv_kernel<T, kDim, true><<<grid, 256, 0, stream>>>(a);
+  else attn_dkv_kernel<T, kDim, false><<<grid, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {
+  return a.dtype == THD_BF16 ? delta<AttnBf16>(a, stream) : delta<AttnFp16>(a, stream);
+}
+
+hipError_t launch_attn_dq(const AttnArgs& a, hipStream_t stream) {
+  if (a.dtype == THD_BF16) return a.dim <= 64 ? dq<AttnBf16, 64>(a, stream) : dq<AttnBf16, 128>(a, stream);
+  return a.dim <= 64 ? dq<AttnFp16, 64>(a, stream) : dq<AttnFp16, 128>(a, stream);
+}
+
+hipError_t launch_attn_dkv(const AttnArgs& a, hipStream_t stream) {
+  if (a.dtype == THD_BF16) return a.dim <= 64 ? dkv<AttnBf16, 64>(a, stream) : dkv<AttnBf16, 128>(a, stream);
+  return a.dim <= 64 ? dkv<AttnFp16, 64>(a, stream) : dkv<AttnFp16, 128>(a, stream);
+}
+
+}  // namespace thdcp

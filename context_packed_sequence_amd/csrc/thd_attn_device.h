@@ -1,0 +1,260 @@
+// Device code shared by the attention kernels: matrix fragments, tiles in LDS
+// and the part of a document that a row sees.
+//
+// Fragments of v_mfma_f32_32x32x16 (lane l, h = l / 32, c = l mod 32):
+//   A [32 rows][16]: lane holds row c, columns 8 h .. 8 h + 7
+//   B [16][32 cols]: lane holds column c, rows 8 h .. 8 h + 7
+//   C [32][32]:      lane holds column c, register r row (r & 3) + 8 (r >> 2) + 4 h
+// A product's C is rounded and becomes the next product's B without leaving its
+// lane: the sum over the shared index may run in any order, so register 8 j + e
+// of C is called element e of B's block j, and the other operand is read in the
+// same order: elements 0..3 from rows 16 j + 4 h.., 4..7 from 16 j + 8 + 4 h...
+// ds_read_b64_tr_b16 gives just that: of 4 rows of 16 elements that 16 lanes
+// point to, lane i gets column i.
+//
+// LDS tiles are rows of kDim 16-bit elements in 16-byte words, word w of row r at
+// place w ^ f(r).  f gives any 16 rows different places (reads of one word of 32
+// rows, as A needs) and any 4 rows different quarters of the banks (transposing
+// reads: 64 bytes of each of 4 rows), so neither read has bank conflicts.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "thd_attn_internal.h"
+#include "thd_device.h"
+
+namespace thdcp {
+
+typedef unsigned int U32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int U32x2 __attribute__((ext_vector_type(2)));
+typedef float F32x16 __attribute__((ext_vector_type(16)));
+typedef float F32x2 __attribute__((ext_vector_type(2)));
+typedef short I16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 Bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 Bf16p __attribute__((ext_vector_type(2)));
+typedef _Float16 F16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 F16p __attribute__((ext_vector_type(2)));
+
+constexpr float kAttnLog2e = 1.4426950408889634f;
+constexpr float kAttnLn2 = 0.6931471805599453f;
+constexpr float kAttnInf = __builtin_huge_valf();
+
+struct AttnBf16 {
+  static __device__ __forceinline__ F32x16 mfma(U32x4 a, U32x4 b, F32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(Bf16x8, a), __builtin_bit_cast(Bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  // rounded to nearest even
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const F32x2 f = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, Bf16p));
+  }
+  static __device__ __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+  static constexpr bool kNarrow = false;
+};
+
+struct AttnFp16 {
+  static __device__ __forceinline__ F32x16 mfma(U32x4 a, U32x4 b, F32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(F16x8, a), __builtin_bit_cast(F16x8, b), c, 0, 0,
+                                                  0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const F32x2 f = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, F16p));
+  }
+  static __device__ __forceinline__ float low(uint32_t w) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w)));
+  }
+  static __device__ __forceinline__ float high(uint32_t w) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w >> 16)));
+  }
+  // 5 exponent bits: gradients of scores are held scaled by a power of two
+  static constexpr bool kNarrow = true;
+};
+
+__device__ __forceinline__ F32x16 zero16() {
+  F32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
+__device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// tanh(x) = 1 - 2 / (1 + e^(2x)), its ends included
+__device__ __forceinline__ float attn_tanh(float x) {
+  return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + attn_exp2(2.0f * kAttnLog2e * x));
+}
+
+// Value of lane l ^ 32, combined.
+__device__ __forceinline__ float max_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])),
+               __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, static_cast<uint32_t>(r[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(r[1]));
+}
+
+template <int kDim>
+__device__ __forceinline__ int32_t lds_swizzle(int32_t row) {
+  if constexpr (kDim == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  else return ((row & 2) << 1) | ((row >> 2) & 3);  // two rows share a line of banks
+}
+
+// Byte address in a tile of word w of a row.
+template <int kDim>
+__device__ __forceinline__ int32_t lds_word(int32_t row, int32_t w) {
+  return row * (2 * kDim) + ((w ^ lds_swizzle<kDim>(row)) << 4);
+}
+
+__device__ __forceinline__ U32x4 lds_read(const char* tile, int32_t at) {
+  return *reinterpret_cast<const U32x4*>(tile + at);
+}
+
+// A of a transposed tile: rows [row, row + 16) of the tile are the summed index
+// (in the order above), columns 32 t .. 32 t + 31 the 32 rows of A.  `at` is this
+// lane's transposed_at<kDim>(t, second).
+template <int kDim>
+__device__ __forceinline__ int32_t transposed_at(int32_t t, int32_t second) {
+  const int32_t l = threadIdx.x & 63, i = l & 15;
+  const int32_t row = 4 * (l >> 5) + (i >> 2) + 8 * second;
+  const int32_t col = 32 * t + 16 * ((l >> 4) & 1) + 4 * (i & 3);
+  return lds_word<kDim>(row, col >> 3) + 2 * (col & 7);
+}
+__device__ __forceinline__ U32x2 lds_read_transposed(const char* at) {
+  typedef __attribute__((address_space(3))) I16x4 LdsI16x4;
+  const I16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      reinterpret_cast<LdsI16x4*>(reinterpret_cast<uintptr_t>(at)));
+  return __builtin_bit_cast(U32x2, r);
+}
+
+// Rows [0, valid) of one head, from `base` on, behind a buffer resource of
+// exactly their size: a word past the last row, or past the head's elements, is
+// read as zeros.  The resource is built anew for each tile, so that offsets stay
+// within 32 bits however long the stream is.
+struct RowsRead {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int32_t stride;  // bytes
+  __device__ __forceinline__ RowsRead(const void* base, int32_t stride_bytes, int32_t valid, int32_t dim)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                               valid > 0 ? (valid - 1) * stride_bytes + 2 * dim : 0, kBufferWord3)),
+        stride(stride_bytes) {}
+  __device__ __forceinline__ int32_t at(int32_t row, int32_t w, int32_t dim) const {
+    return 8 * w < dim ? row * stride + 16 * w : static_cast<int32_t>(0x80000000u);
+  }
+  __device__ __forceinline__ U32x4 load(int32_t row, int32_t w, int32_t dim) const {
+    return __builtin_bit_cast(U32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at(row, w, dim), 0, 0));
+  }
+};
+
+// First address of a head's rows, uniform over the workgroup.
+__device__ __forceinline__ const char* head_rows(const AttnTensor& t, int64_t row, int32_t head) {
+  return static_cast<const char*>(t.data) + 2 * (row * t.row + static_cast<int64_t>(head) * t.head);
+}
+
+// Moves kAttnStep rows into an LDS tile, 16 bytes a lane and turn straight from
+// memory (no registers in between); the caller waits (lds_arrived) before the
+// barrier after which the tile is read.
+template <int kDim>
+__device__ __forceinline__ void load_tile(char* tile, const RowsRead& r, int32_t dim) {
+  constexpr int kWords = kDim / 8;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int j = 0; j < kAttnStep * kWords / 256; ++j) {
+    const int32_t s = j * 256 + threadIdx.x;
+    const int32_t row = s / kWords;
+    const int32_t w = (s % kWords) ^ lds_swizzle<kDim>(row);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r.rsrc,
+        reinterpret_cast<__attribute__((address_space(3))) void*>(
+            reinterpret_cast<uintptr_t>(tile + (j * 256 + wave * 64) * 16)),
+        16, r.at(row, w, dim), 0, 0, 0);
+  }
+}
+__device__ __forceinline__ void lds_arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
+// Keys [low, low + span) of its document are what position `pos` sees.
+struct Seen {
+  int32_t low;
+  uint32_t span;
+  __device__ __forceinline__ Seen(const AttnArgs& a, int32_t pos, int32_t real) {
+    low = a.window ? max(0, pos - a.window + 1) : 0;
+    int32_t end = real;
+    if (a.causal) end = min(real, pos + 1);
+    else if (a.window) end = static_cast<int32_t>(min(int64_t{real}, int64_t{pos} + a.window));
+    span = end > low ? static_cast<uint32_t>(end - low) : 0u;
+  }
+  __device__ __forceinline__ Seen(int32_t first, uint32_t n) : low(first), span(n) {}
+  __device__ __forceinline__ bool operator()(int32_t key) const {
+    return static_cast<uint32_t>(key) - static_cast<uint32_t>(low) < span;
+  }
+};
+
+// Whether positions [p, p + np) see all, or any, of keys [k, k + nk).
+__device__ __forceinline__ bool sees_all(const AttnArgs& a, int32_t p, int32_t np, int32_t k, int32_t nk,
+                                         int32_t real) {
+  if (k + nk > real) return false;
+  if (a.causal && k + nk - 1 > p) return false;
+  if (a.window && p + np - 1 - k >= a.window) return false;
+  return !(a.window && !a.causal && k + nk - 1 - p >= a.window);
+}
+__device__ __forceinline__ bool sees_any(const AttnArgs& a, int32_t p, int32_t np, int32_t k, int32_t nk,
+                                         int32_t real) {
+  if (k >= real || (a.causal && k > p + np - 1)) return false;
+  if (a.window && p - (k + nk - 1) >= a.window) return false;
+  return !(a.window && !a.causal && k - (p + np - 1) >= a.window);
+}
+
+// Tile and head of workgroup b, which runs on XCD b mod 8: the heads of a group
+// read the same keys, and stay on one XCD one after the other; tiles of a key
+// head are dealt out so that, with 8 key heads, each XCD keeps to one of them.
+struct AttnPlace {
+  int32_t tile, kv_head, head;
+  __device__ __forceinline__ AttnPlace(int32_t b, int32_t kv_heads, int32_t group) {
+    const int32_t j = b >> 3;
+    const int32_t unit = (j / group) * 8 + (b & 7);
+    tile = unit / kv_heads;
+    kv_head = unit % kv_heads;
+    head = kv_head * group + j % group;
+  }
+};
+
+// Four waves' accumulators [kDim][32 rows] (rows are lanes) as rows of 16-bit
+// elements, through LDS so that whole lines are stored; row r of the wave is
+// multiplied by `factor` of its lane.  Rows from `valid` on are zero; rows from
+// `rows` on, and columns from dim on, are not stored.
+template <typename T, int kDim>
+__device__ __forceinline__ void store_rows(char* lds, const F32x16 (&acc)[kDim / 32], float factor, char* base,
+                                           int64_t stride_bytes, int32_t rows, int32_t valid, int32_t dim) {
+  const int32_t l = threadIdx.x & 63, c = l & 31, h = l >> 5;
+  const float f = c < valid ? factor : 0.0f;
+#pragma unroll
+  for (int t = 0; t < kDim / 32; ++t) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      U32x2 w;
+      w[0] = T::pack(acc[t][4 * g] * f, acc[t][4 * g + 1] * f);
+      w[1] = T::pack(acc[t][4 * g + 2] * f, acc[t][4 * g + 3] * f);
+      if (c >= valid) w[0] = w[1] = 0u;  // whatever the pad's lane holds
+      *reinterpret_cast<U32x2*>(lds + lds_word<kDim>(c, 4 * t + g) + 8 * h) = w;
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  constexpr int kWords = kDim / 8;
+#pragma unroll
+  for (int j = 0; j < kWords / 2; ++j) {
+    const int32_t s = j * 64 + l;
+    const int32_t row = s / kWords, w = (s % kWords) ^ lds_swizzle<kDim>(row);
+    const U32x4 x = lds_read(lds, s * 16);
+    if (row < rows && 8 * w < dim) *reinterpret_cast<U32x4*>(base + row * stride_bytes + 16 * w) = x;
+  }
+}
+
+}  // namespace thdcp

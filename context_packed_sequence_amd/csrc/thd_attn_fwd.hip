@@ -1,0 +1,187 @@
+// Attention inside documents: out = softmax(z) v and its log-sum-exp.
+//
+// One pass over the keys with the running maximum and sum of the softmax.  A
+// workgroup owns 128 query rows of one head, a wave 32 of them, and the four
+// waves walk through the keys together, 64 at a time, moved straight from memory
+// to LDS while the 64 before are worked on.  Scores are formed transposed, S^T =
+// K Q^T, so that a lane holds one query (its column) and 32 of the 64 keys: the
+// softmax needs one exchange between the two halves of a wave, the output's
+// rescaling is by a lane's own factor, and the rounded probabilities are the
+// second product's operand as they lie (O^T += V^T P^T, V read transposed).
+//
+// The output is rescaled only when some row's maximum grew by more than 2^8 since
+// the reference it is relative to: probabilities up to 256 lose nothing in 32-bit
+// sums, nor rounded to 16 bits.
+#include "thd_attn_device.h"
+
+namespace thdcp {
+
+namespace {
+
+constexpr float kGrowth = 8.0f;  // in powers of two
+
+template <typename T, int kDim, bool kCap>
+struct ForwardWave {
+  U32x4 q[kDim / 16];        // B: 32 queries
+  F32x16 o[kDim / 32];       // [dim][query]
+  float top = -kAttnInf;     // reference of the row's exponents, in powers of two
+  float sum = 0.0f;          // of this lane's keys
+  int32_t key_at[kDim / 16]; // this lane's places in a tile
+  int32_t value_at[kDim / 32][2];
+
+  __device__ __forceinline__ ForwardWave() {
+    const int32_t l = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kDim / 16; ++i) key_at[i] = lds_word<kDim>(l & 31, 2 * i + (l >> 5));
+#pragma unroll
+    for (int t = 0; t < kDim / 32; ++t) {
+      value_at[t][0] = transposed_at<kDim>(t, 0);
+      value_at[t][1] = transposed_at<kDim>(t, 1);
+      o[t] = zero16();
+    }
+  }
+
+  // Keys key0 .. key0 + 63; `partly`: the rows do not see all of them.
+  __device__ __forceinline__ void step(const AttnArgs& a, const char* keys, const char* values, int32_t key0,
+                                       bool partly, const Seen& seen) {
+    const int32_t h = (threadIdx.x & 63) >> 5;
+    F32x16 s[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      s[b] = zero16();
+#pragma unroll
+      for (int i = 0; i < kDim / 16; ++i)
+        s[b] = T::mfma(lds_read(keys, key_at[i] + b * 32 * 2 * kDim), q[i], s[b]);
+    }
+    // scores in powers of two: z log2(e) = s factor
+    float factor = a.scale * kAttnLog2e;
+    if constexpr (kCap) {
+      const float in = a.scale / a.cap;
+      factor = a.cap * kAttnLog2e;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[b][r] = attn_tanh(s[b][r] * in);
+    }
+    if (partly) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int32_t key = key0 + 4 * h + 32 * b + (r & 3) + 8 * (r >> 2);
+          s[b][r] = seen(key) ? s[b][r] : -kAttnInf;
+        }
+    }
+    float m = s[0][0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) m = fmaxf(m, s[0][r]);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) m = fmaxf(m, s[1][r]);
+    m = max_halves(m) * factor;
+    if (__any(m > top + kGrowth)) {
+      const float to = fmaxf(top, m);
+      const float shrink = to == -kAttnInf ? 1.0f : attn_exp2(top - to);
+      top = to;
+      sum *= shrink;
+#pragma unroll
+      for (int t = 0; t < kDim / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[t][r] *= shrink;
+    }
+    const float base = top == -kAttnInf ? 0.0f : top;
+    U32x4 p[4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const float x = attn_exp2(fmaf(s[b][r], factor, -base));
+        const float y = attn_exp2(fmaf(s[b][r + 1], factor, -base));
+        sum += x + y;
+        p[2 * b + (r >> 3)][(r & 7) >> 1] = T::pack(x, y);
+      }
+#pragma unroll
+    for (int t = 0; t < kDim / 32; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const U32x2 x = lds_read_transposed(values + value_at[t][0] + j * 16 * 2 * kDim);
+        const U32x2 y = lds_read_transposed(values + value_at[t][1] + j * 16 * 2 * kDim);
+        o[t] = T::mfma(U32x4{x[0], x[1], y[0], y[1]}, p[j], o[t]);
+      }
+  }
+};
+
+template <typename T, int kDim, bool kCap>
+__global__ __launch_bounds__(256, 2) void attn_forward_kernel(AttnArgs a) {
+  constexpr int kTile = kAttnStep * 2 * kDim;  // bytes
+  __shared__ __attribute__((aligned(16))) char s_keys0[kTile], s_values0[kTile], s_keys1[kTile], s_values1[kTile];
+  const AttnPlace place(blockIdx.x, a.kv_heads, a.group);
+  if (place.tile >= a.plan.header[kAttnQueryTiles]) return;
+  const QueryTile tile = a.plan.query_tiles[place.tile];
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t l = threadIdx.x & 63, c = l & 31;
+  const int32_t own_rows = min(32, max(0, tile.rows - 32 * wave));     // of this wave
+  const int32_t own_valid = min(32, max(0, tile.valid - 32 * wave));
+  const int32_t pos = tile.pos + 32 * wave;
+
+  ForwardWave<T, kDim, kCap> w;
+  if (tile.valid > 0) {
+    const RowsRead queries(head_rows(a.q, tile.row + 32 * wave, place.head), static_cast<int32_t>(2 * a.q.row),
+                           own_valid, a.dim);
+#pragma unroll
+    for (int i = 0; i < kDim / 16; ++i) w.q[i] = queries.load(c, 2 * i + (l >> 5), a.dim);
+
+    const Seen first(a, tile.pos, tile.real), last(a, tile.pos + tile.valid - 1, tile.real);
+    const int32_t end = last.low + static_cast<int32_t>(last.span);
+    int32_t key = first.low & ~(kAttnStep - 1);
+    const Seen seen(a, pos + c, tile.real);
+    const auto load = [&](char* keys, char* values, int32_t at) {
+      const int32_t n = min(kAttnStep, tile.real - at);
+      load_tile<kDim>(keys, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+                                     static_cast<int32_t>(2 * a.k.row), n, a.dim), a.dim);
+      load_tile<kDim>(values, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+                                       static_cast<int32_t>(2 * a.v.row), n, a.dim), a.dim);
+    };
+    const auto turn = [&](const char* keys, const char* values, char* next_keys, char* next_values) {
+      lds_arrived();
+      __syncthreads();  // the tile is there, and nobody reads the one before
+      if (key + kAttnStep < end) load(next_keys, next_values, key + kAttnStep);
+      if (own_valid > 0 && sees_any(a, pos, own_valid, key, kAttnStep, tile.real))
+        w.step(a, keys, values, key, !sees_all(a, pos, 32, key, kAttnStep, tile.real), seen);
+      key += kAttnStep;
+    };
+    load(s_keys0, s_values0, key);
+    while (key < end) {
+      turn(s_keys0, s_values0, s_keys1, s_values1);
+      if (key >= end) break;
+      turn(s_keys1, s_values1, s_keys0, s_values0);
+    }
+    __syncthreads();
+  }
+  const float sum = add_halves(w.sum);
+  const float inverse = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
+  char* own = wave == 0 ? s_keys0 : wave == 1 ? s_values0 : wave == 2 ? s_keys1 : s_values1;
+  store_rows<T, kDim>(own, w.o, inverse, const_cast<char*>(head_rows(a.out, tile.row + 32 * wave, place.head)),
+                      2 * a.out.row, own_rows, own_valid, a.dim);
+  if (l < own_rows)
+    a.lse[static_cast<int64_t>(place.head) * a.rows + tile.row + 32 * wave + l] =
+        l < own_valid ? (w.top + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -kAttnInf;
+}
+
+template <typename T, int kDim>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+  const int32_t units = a.plan.max_query_tiles * a.kv_heads;
+  const dim3 grid((units + 7) / 8 * 8 * a.group);
+  if (a.cap > 0.0f) attn_forward_kernel<T, kDim, true><<<grid, 256, 0, stream>>>(a);
+  else attn_forward_kernel<T, kDim, false><<<grid, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream) {
+  if (a.dtype == THD_BF16)
+    return a.dim <= 64 ? launch<AttnBf16, 64>(a, stream) : launch<AttnBf16, 128>(a, stream);
+  return a.dim <= 64 ? launch<AttnFp16, 64>(a, stream) : launch<AttnFp16, 128>(a, stream);
+}
+
+}  // namespace thdcp

@@ -1,0 +1,84 @@
+// Internal declarations of the attention on packed streams.  Not part of the
+// public ABI (that is include/thd_attention.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "thd_attention.h"
+#include "thd_internal.h"
+
+namespace thdcp {
+
+constexpr int kAttnRows = 128;   // query rows of a workgroup: 32 in each of its 4 waves
+constexpr int kAttnKeys = 128;   // keys of a workgroup that computes their gradients
+constexpr int kAttnStep = 64;    // keys (or query rows) that a workgroup moves through LDS at a time
+
+// Query rows of one workgroup: a run of rows of one document's share.  Rows
+// [valid, rows) are pads.
+struct QueryTile {
+  int32_t row;       // first row of the share
+  int32_t rows;      // 1..kAttnRows
+  int32_t valid;     // rows that hold tokens
+  int32_t pos;       // position in the document of the first row
+  int32_t doc;       // stream row of the document's first token
+  int32_t real;      // the document's tokens
+  int32_t unused[2];
+};
+
+// Keys of one workgroup of the key gradients, and where the share holds the
+// document's queries: `first` is the share's first row of the document, chunk
+// the length of each of its two zigzag chunks (the whole document if cp is 1).
+struct KeyTile {
+  int32_t key;       // position in the document of the first key
+  int32_t keys;      // 1..kAttnKeys
+  int32_t valid;
+  int32_t doc;
+  int32_t real;
+  int32_t first;
+  int32_t chunk;
+  int32_t unused;
+};
+
+// Workspace, written by the plan kernel.
+enum AttnHeader : int { kAttnCode = 0, kAttnQueryTiles = 1, kAttnKeyTiles = 2, kAttnMaxGrad = 3, kAttnMaxValue = 4,
+                        kAttnHeaderWords = 16 };
+
+struct AttnPlan {
+  int32_t* header;         // [kAttnHeaderWords]
+  int32_t* query_first;    // [slots + 1] tiles of the slots before
+  int32_t* key_first;      // [slots + 1], null without key tiles
+  QueryTile* query_tiles;  // heaviest first
+  KeyTile* key_tiles;
+  float* delta;            // [heads][rows], backward only
+  int32_t max_query_tiles;
+  int32_t max_key_tiles;
+};
+
+// Elements between rows and heads of a [rows][heads][dim] tensor.
+struct AttnTensor {
+  void* data;
+  int64_t row, head;
+};
+
+struct AttnArgs {
+  AttnTensor q, k, v, out, dout, dq, dk, dv;
+  float* lse;              // [heads][rows]
+  const int32_t* cu_padded;
+  const int32_t* cu_real;  // or null
+  int32_t* status;         // or null
+  int32_t n_slots, total, rows;
+  int32_t heads, kv_heads, group, dim, dtype;
+  int32_t causal, window;  // window 0: none
+  int32_t cp, rank;
+  float scale, cap;        // cap 0: none
+  AttnPlan plan;
+};
+
+hipError_t launch_attn_plan(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_dq(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_dkv(const AttnArgs& a, hipStream_t stream);
+
+}  // namespace thdcp
