@@ -5,8 +5,11 @@ Low level: the C entry points of libthdcp under their own names
 ``binding.py`` and ``include/thd_cp.h``.
 
 High level: ``Route`` (one per micro-batch: build once, swap many times),
-``roll_labels`` and the losses on packed streams (``losses.py``:
-``token_logprobs``, ``policy_loss``, ``preference_loss``, ``distill_topk``).
+``roll_labels``, the losses on packed streams (``losses.py``:
+``token_logprobs``, ``policy_loss``, ``preference_loss``, ``distill_topk``),
+attention inside documents (``attention.py``: ``packed_attention``), and the
+embedding table and gradients of a step (``params.py``: ``embedding``,
+``clip_gradients``).
 They only allocate output tensors with torch and hand pointers to the library;
 the work runs in the library's HIP kernels.
 """
@@ -30,12 +33,14 @@ from .binding import (  # noqa: F401
     THD_ERR_HIP,
     THD_ERR_INTEGRITY,
     THD_ERR_LABEL,
+    THD_ERR_NORM,
     THD_ERR_NOT_BUILT,
     THD_ERR_PACK_CAPACITY,
     THD_ERR_PACK_DOCS,
     THD_ERR_PAIR,
     THD_ERR_REAL_GT_PADDED,
     THD_ERR_SHAPE,
+    THD_ERR_TOKEN,
     THD_BF16,
     THD_FP16,
     THD_FP32,
@@ -43,8 +48,10 @@ from .binding import (  # noqa: F401
     THD_MAX_BATCH,
     THD_MAX_HEAD_DIM,
     THD_MAX_PAIRS,
+    THD_MAX_TENSORS,
     THD_MAX_TOPK,
     THD_MAX_VOCAB,
+    THD_MAX_WIDTH,
     THD_PACK_MAX_SEQ,
     THD_MAX_CP,
     THD_MAX_SHIFT,
@@ -56,8 +63,14 @@ from .binding import (  # noqa: F401
     thd_attention_shape,
     thd_attention_workspace_bytes,
     thd_build_route,
+    thd_clip_gradients,
     thd_copy,
     thd_distill_topk,
+    thd_embedding,
+    thd_embedding_backward,
+    thd_embedding_workspace_bytes,
+    thd_gradient_norm,
+    thd_gradients_workspace_bytes,
     thd_heads,
     thd_loss_workspace_bytes,
     thd_policy_loss,
@@ -262,6 +275,7 @@ try:
         token_logprobs,
         token_logprobs_backward,
     )
+    from .params import clip_gradients, embedding, embedding_backward, gradient_norm  # noqa: F401
 except ModuleNotFoundError as e:  # without torch there are no tensors to call them with; the C names stand
     if e.name != "torch":
         raise

@@ -49,6 +49,8 @@ THD_ERR_PACK_DOCS = -16
 THD_ERR_PACK_CAPACITY = -17
 THD_ERR_LABEL = -18
 THD_ERR_PAIR = -19
+THD_ERR_TOKEN = -20
+THD_ERR_NORM = -21
 
 THD_ZIGZAG_TO_CONTIGUOUS = 0
 THD_CONTIGUOUS_TO_ZIGZAG = 1
@@ -65,6 +67,8 @@ THD_MAX_VOCAB = 268435456
 THD_MAX_TOPK = 256
 THD_MAX_PAIRS = 65536
 THD_MAX_HEAD_DIM = 128
+THD_MAX_WIDTH = 1048576
+THD_MAX_TENSORS = 65536
 
 EXPORTS = (
     "thd_route_create", "thd_route_destroy", "thd_build_route", "thd_swap", "thd_roll_labels",
@@ -74,6 +78,8 @@ EXPORTS = (
     "thd_loss_workspace_bytes", "thd_token_logprobs", "thd_token_logprobs_backward", "thd_policy_loss",
     "thd_distill_topk", "thd_preference_workspace_bytes", "thd_preference_loss",
     "thd_attention_workspace_bytes", "thd_attention", "thd_attention_backward",
+    "thd_embedding", "thd_embedding_workspace_bytes", "thd_embedding_backward",
+    "thd_gradients_workspace_bytes", "thd_gradient_norm", "thd_clip_gradients",
 )
 
 
@@ -144,6 +150,14 @@ def _load() -> ctypes.CDLL:
         "thd_attention": (ctypes.c_int, [shape, heads, heads, heads, heads, c_p, c_p, *work]),
         "thd_attention_backward": (ctypes.c_int, [shape, heads, heads, heads, heads, c_p, heads, heads, heads, heads,
                                                   c_p, *work]),
+        "thd_embedding": (ctypes.c_int, [c_p, c_p, c_i64, c_p, c_i32, c_i64, c_i64, c_i64, c_f64, c_p, c_i64, c_p,
+                                         c_p]),
+        "thd_embedding_workspace_bytes": (ctypes.c_int64, [c_i64, c_i64, c_i64]),
+        "thd_embedding_backward": (ctypes.c_int, [c_p, c_i32, c_p, c_p, c_i64, c_i64, c_i64, c_i64, c_f64, c_i32, c_p,
+                                                  c_i32, c_i64, c_p, *work]),
+        "thd_gradients_workspace_bytes": (ctypes.c_int64, [c_i32]),
+        "thd_gradient_norm": (ctypes.c_int, [c_p, c_p, c_p, c_i32, c_f64, c_p, c_p, *work]),
+        "thd_clip_gradients": (ctypes.c_int, [c_p, c_p, c_p, c_p, c_p, c_i32, c_f64, c_f64, c_p, c_p, c_p, *work]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -381,6 +395,56 @@ def thd_attention_backward(shape, q, k, v, out, lse, dout, dq, dk, dv, status, w
     return _check(_lib.thd_attention_backward(ref(shape), ref(q), ref(k), ref(v), ref(out), _ptr(lse), ref(dout),
                                               ref(dq), ref(dk), ref(dv), _ptr(status), _ptr(workspace),
                                               workspace_bytes, _stream(stream)), "thd_attention_backward")
+
+
+# ---- embedding and gradients (include/thd_params.h), same names ----------------
+# Tables, rows and gradients are passed as addresses: their rows may be strided.
+
+def thd_embedding(ids, mask, rows: int, table: int, dtype: int, vocab: int, width: int, table_stride: int,
+                  scale: float, out: int, out_stride: int, status, stream=None) -> int:
+    return _check(_lib.thd_embedding(_ptr(ids), _ptr(mask), rows, table, dtype, vocab, width, table_stride, scale, out,
+                                     out_stride, _ptr(status), _stream(stream)), "thd_embedding")
+
+
+def thd_embedding_workspace_bytes(rows: int, vocab: int, width: int) -> int:
+    return int(_lib.thd_embedding_workspace_bytes(rows, vocab, width))
+
+
+def thd_embedding_backward(drows: int, dtype: int, ids, mask, rows: int, vocab: int, width: int, row_stride: int,
+                           scale: float, accumulate: int, dtable: int, out_dtype: int, table_stride: int, status,
+                           workspace, workspace_bytes: int, stream=None) -> int:
+    return _check(_lib.thd_embedding_backward(drows, dtype, _ptr(ids), _ptr(mask), rows, vocab, width, row_stride,
+                                              scale, accumulate, dtable, out_dtype, table_stride, _ptr(status),
+                                              _ptr(workspace), workspace_bytes, _stream(stream)),
+                  "thd_embedding_backward")
+
+
+def thd_gradients_workspace_bytes(n_tensors: int) -> int:
+    return int(_lib.thd_gradients_workspace_bytes(n_tensors))
+
+
+def _list(values, dtype):
+    """A host array and its address (the array has to live through the call)."""
+    array = np.array(values, dtype=dtype)
+    return array, array.ctypes.data
+
+
+def thd_gradient_norm(grads, elements, dtypes, scale: float, norm, status, workspace, workspace_bytes: int,
+                      stream=None) -> int:
+    """grads, elements, dtypes: sequences of addresses, numbers of elements and element types."""
+    (a, at), (n, n_at), (d, d_at) = _list(grads, np.uint64), _list(elements, np.int64), _list(dtypes, np.int32)
+    return _check(_lib.thd_gradient_norm(at, n_at, d_at, len(a), scale, _ptr(norm), _ptr(status), _ptr(workspace),
+                                         workspace_bytes, _stream(stream)), "thd_gradient_norm")
+
+
+def thd_clip_gradients(grads, outs, elements, dtypes, out_dtypes, max_norm: float, scale: float, norm_in, norm,
+                       status, workspace, workspace_bytes: int, stream=None) -> int:
+    """grads, outs, elements, dtypes, out_dtypes: sequences as in thd_gradient_norm."""
+    (a, at), (o, o_at) = _list(grads, np.uint64), _list(outs, np.uint64)
+    (n, n_at), (d, d_at), (e, e_at) = _list(elements, np.int64), _list(dtypes, np.int32), _list(out_dtypes, np.int32)
+    return _check(_lib.thd_clip_gradients(at, o_at, n_at, d_at, e_at, len(a), max_norm, scale, _ptr(norm_in),
+                                          _ptr(norm), _ptr(status), _ptr(workspace), workspace_bytes,
+                                          _stream(stream)), "thd_clip_gradients")
 
 
 def library():

@@ -30,7 +30,8 @@ ARCH = "gfx950"
 
 SOURCES = ["thd_route.hip", "thd_swap.hip", "thd_roll.hip", "thd_pack.hip", "thd_stream.hip", "thd_api.hip",
            "thd_loss.hip", "thd_loss_policy.hip", "thd_loss_distill.hip", "thd_preference.hip", "thd_loss_api.hip",
-           "thd_attn_plan.hip", "thd_attn_fwd.hip", "thd_attn_bwd.hip", "thd_attn_api.hip"]
+           "thd_attn_plan.hip", "thd_attn_fwd.hip", "thd_attn_bwd.hip", "thd_attn_api.hip",
+           "thd_embed.hip", "thd_clip.hip", "thd_params_api.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

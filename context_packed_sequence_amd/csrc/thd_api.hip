@@ -100,6 +100,8 @@ const char* thd_strerror(int32_t code) {
     case THD_ERR_PACK_CAPACITY: return "padded documents exceed the token budget";
     case THD_ERR_LABEL: return "a label or teacher column is outside the vocabulary";
     case THD_ERR_PAIR: return "a preference pair names a slot that does not exist";
+    case THD_ERR_TOKEN: return "a token id is not a row of the table";
+    case THD_ERR_NORM: return "the gradients' norm is not finite";
     default: return "unknown code";
   }
 }

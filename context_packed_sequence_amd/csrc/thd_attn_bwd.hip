@@ -254,9 +254,9 @@ struct QueryWalk {
     const int32_t pos = position(a, k);
     const int32_t valid = max(0, min(k.chunk, k.real - pos));
     const int32_t low = a.causal ? k.key : a.window ? max(0, k.key - a.window + 1) : 0;
-    const int64_t high = a.window ? static_cast<int64_t>(k.key) + k.valid + a.window - 1 : k.real;
+    const int32_t high = a.window ? window_end(a, k.key + k.valid, k.real) : k.real;
     row = max(0, low - pos);
-    end = static_cast<int32_t>(max<int64_t>(0, min<int64_t>(valid, high - pos)));
+    end = max(0, min(valid, high - pos));
   }
   __device__ __forceinline__ int32_t position(const AttnArgs& a, const KeyTile& k) const {
     return a.cp == 1 ? 0 : chunk ? (2 * a.cp - 1 - a.rank) * k.chunk : a.rank * k.chunk;

@@ -178,6 +178,13 @@ __device__ __forceinline__ void load_tile(char* tile, const RowsRead& r, int32_t
 }
 __device__ __forceinline__ void lds_arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
+// End, within a document, of the positions that a window of one that ends at `end`
+// reaches (in 32 bits without a sign: both are below 2^31).
+__device__ __forceinline__ int32_t window_end(const AttnArgs& a, int32_t end, int32_t real) {
+  const uint32_t to = static_cast<uint32_t>(end) + static_cast<uint32_t>(a.window) - 1u;
+  return static_cast<int32_t>(to < static_cast<uint32_t>(real) ? to : static_cast<uint32_t>(real));
+}
+
 // Keys [low, low + span) of its document are what position `pos` sees.
 struct Seen {
   int32_t low;
@@ -186,7 +193,7 @@ struct Seen {
     low = a.window ? max(0, pos - a.window + 1) : 0;
     int32_t end = real;
     if (a.causal) end = min(real, pos + 1);
-    else if (a.window) end = static_cast<int32_t>(min(int64_t{real}, int64_t{pos} + a.window));
+    else if (a.window) end = window_end(a, pos + 1, real);
     span = end > low ? static_cast<uint32_t>(end - low) : 0u;
   }
   __device__ __forceinline__ Seen(int32_t first, uint32_t n) : low(first), span(n) {}

@@ -75,9 +75,7 @@ __device__ KeyTile key_tile(const AttnArgs& a, const Slot& s, int32_t t, int32_t
   int32_t rows = 0;
   if (k.valid > 0) {
     const int32_t low = a.causal ? k.key : a.window ? max(0, k.key - a.window + 1) : 0;
-    const int32_t high = a.window ? static_cast<int32_t>(min<int64_t>(s.real, static_cast<int64_t>(k.key) + k.valid +
-                                                                                 a.window - 1))
-                                  : s.real;
+    const int32_t high = a.window ? window_end(a, k.key + k.valid, s.real) : s.real;
     for (int second = 0; second < (a.cp == 1 ? 1 : 2); ++second) {
       const int32_t pos = a.cp == 1 ? 0 : second ? (2 * a.cp - 1 - a.rank) * s.chunk : a.rank * s.chunk;
       rows += max(0, min(high, pos + s.chunk) - max(low, pos));

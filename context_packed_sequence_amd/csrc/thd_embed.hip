@@ -1,0 +1,553 @@
+// Embedding lookup on a packed stream, and the gradient of its table.
+//
+// The lookup is a copy of rows: every thread moves 16-byte words, four in flight.
+//
+// The gradient of row v of the table is the sum of drows[t] over the rows t that
+// hold token v.  Atomic additions would add in an order of their own on each run, so
+// the stream's rows are sorted by token first, stably, with digits of up to 9 bits:
+// a wave finds a digit's rank among its 64 lanes from ballots, one per bit, and
+// the counts of waves, workgroups and digits before it make it a place.  Then units
+// of 32 or 64 sorted rows are summed, one thread per 16-byte column of a unit, in
+// order: balanced however often a token occurs (the commonest of a text makes
+// thousands of rows).  A token whose rows lie within one unit is stored at once;
+// where its run passes a unit's border the sums go to a workspace, and the thread
+// of the unit in which the run begins adds them up, in order, in the last launch.
+// The launch that sums also writes the rows of tokens that do not occur.
+#include "thd_loss_device.h"
+#include "thd_params_internal.h"
+
+namespace thdcp {
+
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+
+// 16 bytes at any element's alignment: the hardware takes them as they lie.
+struct __attribute__((packed, aligned(2))) LooseWord {
+  uint32_t x[4];
+};
+__device__ __forceinline__ Word4 load_loose(const void* p) {
+  const LooseWord w = *static_cast<const LooseWord*>(p);
+  return Word4{w.x[0], w.x[1], w.x[2], w.x[3]};
+}
+__device__ __forceinline__ void store_loose(void* p, Word4 v) {
+  *static_cast<LooseWord*>(p) = LooseWord{{v[0], v[1], v[2], v[3]}};
+}
+
+// Place of thread i of a workgroup that takes `each` of n x words places from
+// `from` on: the row and the word, with one long division a workgroup.
+struct FlatPlace {
+  int64_t row0;
+  int32_t rest;
+  FastDiv by;
+  __device__ __forceinline__ FlatPlace(int64_t from, int32_t words, FastDiv d) : by(d) {
+    row0 = from / words;
+    rest = static_cast<int32_t>(from - row0 * words);
+  }
+  __device__ __forceinline__ void operator()(int32_t i, int32_t words, int64_t* row, int32_t* word) const {
+    const int32_t at = rest + i, r = by(at);
+    *row = row0 + r;
+    *word = at - r * words;
+  }
+};
+
+// ---- lookup -----------------------------------------------------------------
+
+constexpr int kLookupEach = 4;  // words of a thread
+
+template <typename T>
+__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int32_t words, FastDiv by_words, int64_t row_blocks) {
+  constexpr int kPer = Elem<T>::kPer;
+  if (static_cast<int64_t>(blockIdx.x) == row_blocks) {  // the workgroup that looks through all ids
+    __shared__ int s_bad;
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int32_t t = threadIdx.x; t < a.rows; t += 256) {
+      const int64_t id = a.ids[t];
+      if (id < 0 || id >= a.vocab) bad |= !a.mask || a.mask[t] != 0;
+    }
+    if (bad) s_bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = s_bad ? THD_ERR_TOKEN : THD_OK;
+    return;
+  }
+  const FlatPlace place(static_cast<int64_t>(blockIdx.x) * (256 * kLookupEach), words, by_words);
+  int64_t row[kLookupEach], id[kLookupEach];
+  int32_t word[kLookupEach];
+  bool live[kLookupEach];
+#pragma unroll
+  for (int i = 0; i < kLookupEach; ++i) {
+    place(i * 256 + threadIdx.x, words, &row[i], &word[i]);
+    const bool in = row[i] < a.rows;
+    live[i] = in && (!a.mask || a.mask[row[i]] != 0);
+    id[i] = in ? a.ids[row[i]] : 0;
+  }
+  Word4 x[kLookupEach];
+#pragma unroll
+  for (int i = 0; i < kLookupEach; ++i) {
+    x[i] = Word4{0, 0, 0, 0};
+    if (!live[i]) continue;
+    const bool good = id[i] >= 0 && id[i] < a.vocab;
+    if (!good) {
+      x[i] = Word4{Elem<T>::kNanWord, Elem<T>::kNanWord, Elem<T>::kNanWord, Elem<T>::kNanWord};
+      if (!a.scan && a.status) *a.status = THD_ERR_TOKEN;
+      continue;
+    }
+    const T* from = static_cast<const T*>(a.table) + id[i] * a.in_stride + word[i] * kPer;
+    if (word[i] * kPer + kPer <= a.width) {
+      x[i] = load_loose(from);
+    } else {
+      float v[kPer] = {};
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (word[i] * kPer + j < a.width) v[j] = Elem<T>::load(from + j);
+      x[i] = Elem<T>::pack(v);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kLookupEach; ++i) {
+    if (row[i] >= a.rows) continue;
+    float v[kPer];
+    Elem<T>::unpack(x[i], v);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] *= a.scale;
+    T* to = static_cast<T*>(a.out) + row[i] * a.out_stride + word[i] * kPer;
+    if (word[i] * kPer + kPer <= a.width) {
+      store_loose(to, Elem<T>::pack(v));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (word[i] * kPer + j < a.width) to[j] = Elem<T>::round(v[j]);
+    }
+  }
+}
+
+// ---- sort -------------------------------------------------------------------
+
+// Row t as it enters the sort: rows that do not count come last.
+__device__ __forceinline__ TokenRow token_row(const EmbedArgs& a, int32_t t, bool* bad) {
+  TokenRow r{static_cast<uint32_t>(a.vocab), static_cast<uint32_t>(t)};
+  if (a.mask && a.mask[t] == 0) return r;
+  const int64_t id = a.ids[t];
+  if (id < 0 || id >= a.vocab) *bad = true;
+  else r.key = static_cast<uint32_t>(id);
+  return r;
+}
+
+// Ranks of a workgroup's items among those with the same digit: on return
+// rank[i] counts the earlier ones of the thread's wave, and count[wave][digit] those
+// of the waves before; total of each digit in s_total.  Item i of a thread is item
+// (wave kEach + i) 64 + lane of the workgroup; `in` says whether it exists.
+template <int kEach>
+__device__ __forceinline__ void rank_digits(const uint32_t (&digit)[kEach], const bool (&in)[kEach], int32_t bits,
+                                            int32_t (*s_count)[kSortBins], int32_t* s_total, int32_t (&rank)[kEach]) {
+  const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int32_t i = threadIdx.x; i < kSortWaves * kSortBins; i += kSortThreads) (&s_count[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    uint64_t peers = __ballot(in[i]);
+    for (int32_t b = 0; b < bits; ++b) {
+      const bool one = (digit[i] >> b) & 1;
+      const uint64_t ones = __ballot(one);
+      peers &= one ? ones : ~ones;
+    }
+    const int32_t lower = __popcll(peers & ((uint64_t{1} << lane) - 1));
+    const int32_t before = s_count[wave][digit[i]];
+    rank[i] = before + lower;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (in[i] && lower == 0) s_count[wave][digit[i]] = before + __popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  __syncthreads();
+  for (int32_t d = threadIdx.x; d < kSortBins; d += kSortThreads) {
+    int32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int32_t n = s_count[w][d];
+      s_count[w][d] = sum;
+      sum += n;
+    }
+    s_total[d] = sum;
+  }
+  __syncthreads();
+}
+
+// Up to kSortBlock rows: one workgroup, all passes in LDS.
+__global__ __launch_bounds__(kSortThreads) void embed_sort_block_kernel(EmbedArgs a, EmbedSort s) {
+  constexpr int kEach = kSortBlock / kSortThreads;
+  __shared__ int32_t s_count[kSortWaves][kSortBins];
+  __shared__ int32_t s_total[kSortBins];
+  __shared__ int32_t s_wave[kSortWaves + 1];
+  __shared__ int s_bad;
+  __shared__ TokenRow s_item[kSortBlock];
+  const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (threadIdx.x == 0) s_bad = 0;
+  TokenRow item[kEach];
+  bool in[kEach], bad = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int32_t t = (wave * kEach + i) * 64 + lane;
+    in[i] = t < a.rows;
+    item[i] = in[i] ? token_row(a, t, &bad) : TokenRow{0, 0};
+  }
+  for (int32_t p = 0; p < s.passes; ++p) {
+    uint32_t digit[kEach];
+    int32_t rank[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) digit[i] = (item[i].key >> (p * s.bits)) & ((1u << s.bits) - 1);
+    rank_digits<kEach>(digit, in, s.bits, s_count, s_total, rank);
+    int32_t all;
+    const int32_t n = threadIdx.x < kSortBins ? s_total[threadIdx.x] : 0;
+    const int32_t first = block_exclusive_scan<kSortThreads>(n, s_wave, &all);
+    if (threadIdx.x < kSortBins) s_total[threadIdx.x] = first;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (in[i]) s_item[s_total[digit[i]] + s_count[wave][digit[i]] + rank[i]] = item[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int32_t t = (wave * kEach + i) * 64 + lane;
+      if (in[i]) item[i] = s_item[t];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int32_t t = (wave * kEach + i) * 64 + lane;
+    if (in[i]) s.a[t] = item[i];
+  }
+  if (bad) s_bad = 1;
+  __syncthreads();
+  if (threadIdx.x == 0 && a.status) *a.status = s_bad ? THD_ERR_TOKEN : THD_OK;
+}
+
+// One pass over more rows: each workgroup's digits counted ...
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedArgs a, EmbedSort s, const TokenRow* from,
+                                                                   int32_t shift) {
+  __shared__ int32_t s_count[kSortBins];
+  __shared__ int s_bad;
+  if (threadIdx.x < kSortBins) s_count[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  // below 2^32: the first row is one
+  const uint32_t first = blockIdx.x * static_cast<uint32_t>(s.turns) * kSortTile;
+  const uint32_t end = min(static_cast<uint32_t>(a.rows), first + static_cast<uint32_t>(s.turns) * kSortTile);
+  bool bad = false;
+  for (uint32_t t = first + threadIdx.x; t < end; t += kSortThreads) {
+    const TokenRow r = from ? from[t] : token_row(a, static_cast<int32_t>(t), &bad);
+    atomicAdd(&s_count[(r.key >> shift) & ((1u << s.bits) - 1)], 1);
+  }
+  if (bad) s_bad = 1;
+  __syncthreads();
+  if (threadIdx.x < kSortBins) s.counts[blockIdx.x * kSortBins + threadIdx.x] = s_count[threadIdx.x];
+  if (threadIdx.x == 0 && !from) s.counts[kSortBlocks * kSortBins + blockIdx.x] = s_bad;
+}
+
+// ... and its rows placed: a digit's first place is that of all smaller digits
+// and of the workgroups before, which every workgroup adds up for itself.
+__global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedArgs a, EmbedSort s, const TokenRow* from,
+                                                                   TokenRow* to, int32_t shift) {
+  constexpr int kEach = kSortTile / kSortThreads;
+  __shared__ int32_t s_count[kSortWaves][kSortBins];
+  __shared__ int32_t s_total[kSortBins], s_first[kSortBins];
+  __shared__ int32_t s_wave[kSortWaves + 1];
+  __shared__ int s_bad;
+  const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (!from && a.status && blockIdx.x == 0) {
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    if (static_cast<int32_t>(threadIdx.x) < s.blocks && s.counts[kSortBlocks * kSortBins + threadIdx.x]) s_bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = s_bad ? THD_ERR_TOKEN : THD_OK;
+  }
+  int32_t before = 0, all = 0;
+  if (threadIdx.x < kSortBins) {
+#pragma unroll 8
+    for (int32_t b = 0; b < s.blocks; ++b) {
+      const int32_t n = s.counts[b * kSortBins + threadIdx.x];
+      all += n;
+      if (b < static_cast<int32_t>(blockIdx.x)) before += n;
+    }
+  }
+  int32_t sum;
+  const int32_t smaller = block_exclusive_scan<kSortThreads>(all, s_wave, &sum);
+  if (threadIdx.x < kSortBins) s_first[threadIdx.x] = smaller + before;
+  __syncthreads();
+  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(s.turns) * kSortTile;
+  bool bad = false;
+  for (int32_t turn = 0; turn < s.turns; ++turn) {
+    TokenRow item[kEach];
+    uint32_t digit[kEach];
+    bool in[kEach];
+    int32_t rank[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t t = begin + static_cast<uint32_t>(turn) * kSortTile + (wave * kEach + i) * 64 + lane;
+      in[i] = t < static_cast<uint32_t>(a.rows);
+      item[i] = !in[i] ? TokenRow{0, 0} : from ? from[t] : token_row(a, static_cast<int32_t>(t), &bad);
+      digit[i] = (item[i].key >> shift) & ((1u << s.bits) - 1);
+    }
+    rank_digits<kEach>(digit, in, s.bits, s_count, s_total, rank);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (in[i]) to[s_first[digit[i]] + s_count[wave][digit[i]] + rank[i]] = item[i];
+    __syncthreads();
+    if (threadIdx.x < kSortBins) s_first[threadIdx.x] += s_total[threadIdx.x];
+    __syncthreads();
+  }
+}
+
+// ---- sums -------------------------------------------------------------------
+
+// Stores columns [kPer word, ...) of row v of the gradient, or adds to them.
+template <typename TI, typename TO>
+__device__ __forceinline__ void finish_row(const EmbedArgs& a, uint32_t v, int32_t word,
+                                           const float (&acc)[Elem<TI>::kPer]) {
+  constexpr int kPer = Elem<TI>::kPer, kOut = Elem<TO>::kPer;
+  TO* to = static_cast<TO*>(a.dtable) + static_cast<int64_t>(v) * a.out_stride + word * kPer;
+  if (word * kPer + kPer <= a.width) {
+#pragma unroll
+    for (int part = 0; part < kPer; part += kOut) {
+      float y[kOut];
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) y[j] = a.scale * acc[part + j];
+      if (a.accumulate) {
+        float old[kOut];
+        Elem<TO>::unpack(load_loose(to + part), old);
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) y[j] += old[j];
+      }
+      store_loose(to + part, Elem<TO>::pack(y));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (word * kPer + j < a.width) {
+      float y = a.scale * acc[j];
+      if (a.accumulate) y += Elem<TO>::load(to + j);
+      to[j] = Elem<TO>::round(y);
+    }
+}
+
+// Partial sums: [unit][0: run from the unit before, 1: run into the next][width].
+template <int kPer>
+__device__ __forceinline__ void store_partial(const EmbedArgs& a, const EmbedSort& s, int32_t unit, int32_t slot,
+                                              int32_t word, const float (&acc)[kPer]) {
+  float* to = s.partial + (2 * static_cast<int64_t>(unit) + slot) * a.width + word * kPer;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (word * kPer + j < a.width) to[j] = acc[j];
+}
+
+template <typename TI, typename TO>
+__global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort s, int32_t words, FastDiv by_words,
+                                                         int32_t unit_blocks, int32_t table_rows) {
+  constexpr int kPer = Elem<TI>::kPer;
+  const auto none = static_cast<uint32_t>(a.vocab);
+  if (static_cast<int32_t>(blockIdx.x) >= unit_blocks) {
+    // rows of the table without a token: table_rows of them a workgroup
+    constexpr int kOut = Elem<TO>::kPer;
+    __shared__ bool s_absent[256];
+    const int32_t r0 = (static_cast<int32_t>(blockIdx.x) - unit_blocks) * table_rows;
+    const int32_t n = min(table_rows, a.vocab - r0);
+    if (static_cast<int32_t>(threadIdx.x) < n) {
+      const auto v = static_cast<uint32_t>(r0 + threadIdx.x);
+      int32_t low = 0, high = a.rows;  // first place whose key is not below v
+      while (low < high) {
+        const int32_t mid = low + ((high - low) >> 1);
+        if (s.a[mid].key < v) low = mid + 1;
+        else high = mid;
+      }
+      s_absent[threadIdx.x] = low == a.rows || s.a[low].key != v;
+    }
+    __syncthreads();
+    const int32_t out_words = (a.width + kOut - 1) / kOut;
+    for (int32_t r = 0; r < n; ++r) {
+      if (!s_absent[r]) continue;
+      TO* to = static_cast<TO*>(a.dtable) + static_cast<int64_t>(r0 + r) * a.out_stride;
+      for (int32_t w = threadIdx.x; w < out_words; w += 256) {
+        if (w * kOut + kOut <= a.width) store_loose(to + w * kOut, Word4{0, 0, 0, 0});
+        else
+          for (int j = w * kOut; j < a.width; ++j) to[j] = Elem<TO>::round(0.0f);
+      }
+    }
+    return;
+  }
+  const FlatPlace place(static_cast<int64_t>(blockIdx.x) * 256, words, by_words);
+  int64_t unit64;
+  int32_t word;
+  place(threadIdx.x, words, &unit64, &word);
+  if (unit64 >= s.units) return;
+  const auto unit = static_cast<int32_t>(unit64);
+  const int32_t first = unit * s.unit, last = min(a.rows - first, s.unit) + first;
+  const bool whole = word * kPer + kPer <= a.width;
+  uint32_t key = s.a[first].key;
+  if (key == none) return;  // as are all after it
+  bool open = first > 0 && s.a[first - 1].key == key;  // the run began in a unit before
+  float acc[kPer] = {};
+  constexpr int kBatch = 8;
+  for (int32_t i0 = first; i0 < last && key != none; i0 += kBatch) {
+    TokenRow item[kBatch];
+    Word4 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) item[i] = i0 + i < last ? s.a[i0 + i] : TokenRow{none, 0};
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      x[i] = Word4{0, 0, 0, 0};
+      if (item[i].key == none) continue;
+      const TI* from = static_cast<const TI*>(a.drows) + static_cast<int64_t>(item[i].row) * a.in_stride + word * kPer;
+      if (whole) {
+        x[i] = load_loose(from);
+      } else {
+        float v[kPer] = {};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (word * kPer + j < a.width) v[j] = Elem<TI>::load(from + j);
+        x[i] = Elem<TI>::pack(v);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i >= last || key == none) continue;
+      if (item[i].key != key) {
+        if (open) store_partial<kPer>(a, s, unit, 0, word, acc);
+        else finish_row<TI, TO>(a, key, word, acc);
+        open = false;
+        key = item[i].key;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) acc[j] = 0.0f;
+        if (key == none) continue;
+      }
+      float v[kPer];
+      Elem<TI>::unpack(x[i], v);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] += v[j];
+    }
+  }
+  if (key == none) return;
+  if (open) store_partial<kPer>(a, s, unit, 0, word, acc);
+  else if (last < a.rows && s.a[last].key == key) store_partial<kPer>(a, s, unit, 1, word, acc);
+  else finish_row<TI, TO>(a, key, word, acc);
+}
+
+// Runs that pass a unit's border: the thread of the unit in which the run begins
+// adds up its parts.
+template <typename TI, typename TO>
+__global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, EmbedSort s, int32_t words, FastDiv by_words) {
+  constexpr int kPer = Elem<TI>::kPer;
+  const auto none = static_cast<uint32_t>(a.vocab);
+  const FlatPlace place(static_cast<int64_t>(blockIdx.x) * 256, words, by_words);
+  int64_t unit64;
+  int32_t word;
+  place(threadIdx.x, words, &unit64, &word);
+  if (unit64 >= s.units) return;
+  const auto unit = static_cast<int32_t>(unit64);
+  const int32_t first = unit * s.unit, last = min(a.rows - first, s.unit) + first;
+  if (last >= a.rows) return;
+  const uint32_t key = s.a[last - 1].key;
+  if (key == none || s.a[last].key != key) return;
+  if (first > 0 && s.a[first].key == key && s.a[first - 1].key == key) return;  // it began before
+  int32_t low = last, high = a.rows;  // first place after the run
+  while (low < high) {
+    const int32_t mid = low + ((high - low) >> 1);
+    if (s.a[mid].key == key) low = mid + 1;
+    else high = mid;
+  }
+  const int32_t end = (low - 1) / s.unit;  // the run's last unit
+  float acc[kPer] = {};
+  const float* from = s.partial + (2 * static_cast<int64_t>(unit) + 1) * a.width + word * kPer;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (word * kPer + j < a.width) acc[j] = from[j];
+#pragma unroll 4
+  for (int32_t u = unit + 1; u <= end; ++u) {
+    from = s.partial + 2 * static_cast<int64_t>(u) * a.width + word * kPer;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (word * kPer + j < a.width) acc[j] += from[j];
+  }
+  finish_row<TI, TO>(a, key, word, acc);
+}
+
+template <typename TI, typename TO>
+hipError_t sums(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
+  const int32_t words = (a.width + Elem<TI>::kPer - 1) / Elem<TI>::kPer;
+  const auto by_words = FastDiv::make(words);
+  const auto unit_blocks = static_cast<int32_t>((static_cast<int64_t>(s.units) * words + 255) / 256);
+  // 64 KiB of the table a workgroup: its rows are searched for side by side
+  const int64_t row_bytes = static_cast<int64_t>(a.width) * static_cast<int64_t>(sizeof(TO));
+  const auto table_rows = static_cast<int32_t>(row_bytes >= 65536 ? 1 : row_bytes <= 256 ? 256 : 65536 / row_bytes);
+  const int64_t zero_blocks = a.accumulate ? 0 : (static_cast<int64_t>(a.vocab) + table_rows - 1) / table_rows;
+  const int64_t blocks = unit_blocks + zero_blocks;
+  if (blocks > 0)
+    embed_sums_kernel<TI, TO><<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, s, words, by_words, unit_blocks,
+                                                                                 table_rows);
+  if (unit_blocks > 0 && s.units > 1)
+    embed_join_kernel<TI, TO><<<unit_blocks, 256, 0, stream>>>(a, s, words, by_words);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t lookup(const EmbedArgs& a, hipStream_t stream) {
+  const int32_t words = (a.width + Elem<T>::kPer - 1) / Elem<T>::kPer;
+  const int64_t blocks = (static_cast<int64_t>(a.rows) * words + 256 * kLookupEach - 1) / (256 * kLookupEach);
+  embed_kernel<T><<<static_cast<uint32_t>(blocks + (a.scan ? 1 : 0)), 256, 0, stream>>>(a, words,
+                                                                                        FastDiv::make(words), blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+EmbedSort embed_sort(int64_t rows, int64_t vocab) {
+  EmbedSort s{};
+  int32_t bits = 1;
+  while ((int64_t{1} << bits) <= vocab) ++bits;  // keys 0..vocab
+  s.passes = (bits + 8) / 9;
+  s.bits = (bits + s.passes - 1) / s.passes;
+  s.blocks = 1;
+  if (rows > kSortBlock) {
+    const int64_t tiles = (rows + kSortTile - 1) / kSortTile;
+    s.turns = static_cast<int32_t>((tiles + kSortBlocks - 1) / kSortBlocks);
+    s.blocks = static_cast<int32_t>((tiles + s.turns - 1) / s.turns);
+  }
+  // long units have fewer borders; with few rows short ones give more threads
+  s.unit = rows < 65536 ? 32 : 64;
+  s.units = static_cast<int32_t>((rows + s.unit - 1) / s.unit);
+  return s;
+}
+
+hipError_t launch_embedding(const EmbedArgs& a, hipStream_t stream) {
+  if (a.dtype == THD_BF16) return lookup<Bf16>(a, stream);
+  return a.dtype == THD_FP16 ? lookup<Fp16>(a, stream) : lookup<float>(a, stream);
+}
+
+hipError_t launch_embedding_sort(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
+  if (a.rows <= kSortBlock) {
+    embed_sort_block_kernel<<<1, kSortThreads, 0, stream>>>(a, s);
+    return hipGetLastError();
+  }
+  const TokenRow* from = nullptr;
+  for (int32_t p = 0; p < s.passes; ++p) {
+    TokenRow* to = (s.passes - 1 - p) % 2 == 0 ? s.a : s.b;
+    embed_count_kernel<<<s.blocks, kSortThreads, 0, stream>>>(a, s, from, p * s.bits);
+    embed_place_kernel<<<s.blocks, kSortThreads, 0, stream>>>(a, s, from, to, p * s.bits);
+    from = to;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_embedding_sums(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
+  if (a.dtype == THD_FP32) return sums<float, float>(a, s, stream);
+  if (a.dtype == THD_BF16)
+    return a.out_dtype == THD_FP32 ? sums<Bf16, float>(a, s, stream) : sums<Bf16, Bf16>(a, s, stream);
+  return a.out_dtype == THD_FP32 ? sums<Fp16, float>(a, s, stream) : sums<Fp16, Fp16>(a, s, stream);
+}
+
+}  // namespace thdcp

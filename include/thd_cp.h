@@ -70,6 +70,10 @@ extern "C" {
 #define THD_ERR_LABEL         -18   /* a label or teacher column is not a column       */
 #define THD_ERR_PAIR          -19   /* a preference pair names no slot                 */
 
+/* Written on the device by the calls of thd_params.h: */
+#define THD_ERR_TOKEN         -20   /* a token id is not a row of the table            */
+#define THD_ERR_NORM          -21   /* the gradients' norm is not finite               */
+
 /* ---- directions ---------------------------------------------------------- */
 #define THD_ZIGZAG_TO_CONTIGUOUS 0
 #define THD_CONTIGUOUS_TO_ZIGZAG 1
