@@ -38,6 +38,9 @@ __device__ __forceinline__ float add_row16(float x) {
   return x;
 }
 
+// Rows that are not finite have no say in other rows' scale.
+__device__ __forceinline__ float finite_or_zero(float x) { return x < kAttnInf ? x : 0.0f; }
+
 // delta of a tile's rows, 16 lanes a row, and the largest norms for fp16.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t query_blocks) {
@@ -68,7 +71,7 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
       }
       dot = add_row16(dot);
       if (word == 0 && row < tile.valid) delta[row] = dot;
-      if constexpr (T::kNarrow) most = fmaxf(most, add_row16(square));
+      if constexpr (T::kNarrow) most = fmaxf(most, finite_or_zero(add_row16(square)));
     }
   } else if constexpr (T::kNarrow) {
     const int32_t b = blockIdx.x - query_blocks;
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
         square = fmaf(T::low(u), T::low(u), square);
         square = fmaf(T::high(u), T::high(u), square);
       }
-      most = fmaxf(most, add_row16(square));
+      most = fmaxf(most, finite_or_zero(add_row16(square)));
     }
   }
   if constexpr (T::kNarrow) {

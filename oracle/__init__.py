@@ -31,7 +31,10 @@ Pins (each function is checked against something other than itself in
 
 * losses (``loss_oracle.py``): every gradient against central differences of its
   loss, closed forms (uniform rows, a one-column vocabulary, a teacher equal to
-  the student, equal documents), masks that leave nothing.
+  the student, equal documents), masks that leave nothing;
+* attention, embedding and clipping (``train_oracle.py``): gradients against
+  central differences or as the transpose, the ranks' rows against the whole
+  stream's, closed forms.
 
 Parity unpinned: the values written at masked positions (the pages only say the
 positions are cleared; the oracle writes ``fill``).
@@ -61,4 +64,14 @@ from .thd_oracle import (  # noqa: F401
     roll_labels,
     roll_valid_at,
     pack_batch,
+)
+from .train_oracle import (  # noqa: F401
+    attention,
+    attention_backward,
+    clip_gradients,
+    embedding,
+    embedding_backward,
+    gradient_norm,
+    share_rows,
+    visible,
 )
