@@ -56,9 +56,9 @@ def embedding(ids, table, mask=None, scale=1.0, out=None, stream=None):
     """``scale * table[ids]`` in the table's dtype: (rows [*ids.shape, width], status).
     ``ids`` int64, ``mask`` uint8 of the same number of elements or None: rows with
     mask 0 are 0."""
-    w = _matrix(table, "table")
-    if table.dim() != 2:
+    if table is not None and table.dim() != 2:
         raise ValueError("table must be [vocab, width]")
+    w = _matrix(table, "table")
     vocab, width = w.shape
     on = w.get_device()
     if ids is None:
