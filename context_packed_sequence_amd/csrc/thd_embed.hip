@@ -341,9 +341,37 @@ template <int kPer>
 __device__ __forceinline__ void store_partial(const EmbedArgs& a, const EmbedSort& s, int32_t unit, int32_t slot,
                                               int32_t word, const float (&acc)[kPer]) {
   float* to = s.partial + (2 * static_cast<int64_t>(unit) + slot) * a.width + word * kPer;
+  if (word * kPer + kPer <= a.width) {
+#pragma unroll
+    for (int part = 0; part < kPer; part += 4)
+      store_loose(to + part, Word4{__builtin_bit_cast(uint32_t, acc[part]), __builtin_bit_cast(uint32_t, acc[part + 1]),
+                                   __builtin_bit_cast(uint32_t, acc[part + 2]),
+                                   __builtin_bit_cast(uint32_t, acc[part + 3])});
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
     if (word * kPer + j < a.width) to[j] = acc[j];
+}
+
+template <int kPer>
+__device__ __forceinline__ void load_partial(const EmbedArgs& a, const EmbedSort& s, int32_t unit, int32_t slot,
+                                             int32_t word, float (&x)[kPer]) {
+  const float* from = s.partial + (2 * static_cast<int64_t>(unit) + slot) * a.width + word * kPer;
+  if (word * kPer + kPer <= a.width) {
+#pragma unroll
+    for (int part = 0; part < kPer; part += 4) {
+      const Word4 w = load_loose(from + part);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t bits = w[j];
+        x[part + j] = __builtin_bit_cast(float, bits);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) x[j] = word * kPer + j < a.width ? from[j] : 0.0f;
 }
 
 template <typename TI, typename TO>
@@ -461,17 +489,17 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, EmbedSort 
     else high = mid;
   }
   const int32_t end = (low - 1) / s.unit;  // the run's last unit
-  float acc[kPer] = {};
-  const float* from = s.partial + (2 * static_cast<int64_t>(unit) + 1) * a.width + word * kPer;
+  float acc[kPer];
+  load_partial<kPer>(a, s, unit, 1, word, acc);
+  constexpr int kBatch = 8;  // parts in flight
+  for (int32_t u0 = unit + 1; u0 <= end; u0 += kBatch) {
+    float part[kBatch][kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (word * kPer + j < a.width) acc[j] = from[j];
-#pragma unroll 4
-  for (int32_t u = unit + 1; u <= end; ++u) {
-    from = s.partial + 2 * static_cast<int64_t>(u) * a.width + word * kPer;
+    for (int i = 0; i < kBatch; ++i) load_partial<kPer>(a, s, min(u0 + i, end), 0, word, part[i]);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (word * kPer + j < a.width) acc[j] += from[j];
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] += u0 + i <= end ? part[i][j] : 0.0f;
   }
   finish_row<TI, TO>(a, key, word, acc);
 }

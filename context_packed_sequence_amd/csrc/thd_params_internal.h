@@ -61,12 +61,15 @@ constexpr int32_t kListTensors = 96;          // tensors of one launch, passed b
 constexpr int32_t kNormBlocks = 2048;         // workgroups, and partial sums, of one launch
 constexpr int32_t kGradChunkBytes = 32768;    // of a tensor's elements in a workgroup's turn
 
+struct GradEntry {
+  const void* in;
+  void* out;
+  int32_t tail;                               // elements of the last chunk
+  int32_t types;                              // in, out << 8
+};
 struct GradList {
-  const void* in[kListTensors];
-  void* out[kListTensors];
-  int32_t tail[kListTensors];                 // elements of the last chunk
+  GradEntry entry[kListTensors];
   int32_t first[kListTensors + 1];            // chunks of the tensors before
-  int8_t in_type[kListTensors], out_type[kListTensors];
   int32_t tensors;
 };
 static_assert(sizeof(GradList) < 3584, "a launch takes 4 KiB of arguments");
@@ -80,7 +83,8 @@ struct ClipArgs {
   int32_t* status;           // or null
 };
 
-hipError_t launch_norm(const GradList& l, double* partial, int32_t blocks, hipStream_t stream);
+// last: the tensors whose chunks are scaled first, as far as caches keep them.
+hipError_t launch_norm(const GradList& l, double* partial, int32_t blocks, bool last, hipStream_t stream);
 hipError_t launch_norm_finish(const ClipArgs& c, hipStream_t stream);
 hipError_t launch_clip(const GradList& l, const ClipArgs& c, int32_t blocks, bool finish, hipStream_t stream);
 

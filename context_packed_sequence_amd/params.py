@@ -128,19 +128,20 @@ def embedding_backward(drows, ids, vocab, mask=None, scale=1.0, out=None, accumu
 
 def _tensors(tensors, name, device):
     """Host arrays (addresses, elements, types) of contiguous tensors on one device."""
-    types, at, elements = [], [], []
-    for i, x in enumerate(tensors):
-        kind = _DTYPES.get(x.dtype)
-        if kind is None:
-            raise ValueError(f"{name}[{i}] must be bfloat16, float16 or float32, got {x.dtype}")
-        if x.get_device() != device:
-            raise ValueError(f"{name}[{i}] is on {x.device}, which is not the current device")
-        if not x.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        types.append(kind)
-        at.append(x.data_ptr())
-        elements.append(x.numel())
-    return np.array(at, np.uint64), np.array(elements, np.int64), np.array(types, np.int32)
+    dtypes = [x.dtype for x in tensors]
+    # one look at all of them; the one that is wrong is found only where there is one
+    if not _DTYPES.keys() >= set(dtypes):
+        i = next(i for i, d in enumerate(dtypes) if d not in _DTYPES)
+        raise ValueError(f"{name}[{i}] must be bfloat16, float16 or float32, got {dtypes[i]}")
+    on = [x.get_device() for x in tensors]
+    if on.count(device) != len(on):
+        i = next(i for i, d in enumerate(on) if d != device)
+        raise ValueError(f"{name}[{i}] is on {tensors[i].device}, which is not the current device")
+    whole = [x.is_contiguous() for x in tensors]
+    if not all(whole):
+        raise ValueError(f"{name}[{whole.index(False)}] must be contiguous")
+    return (np.array([x.data_ptr() for x in tensors], np.uint64), np.array([x.numel() for x in tensors], np.int64),
+            np.array([_DTYPES[d] for d in dtypes], np.int32))
 
 
 def _gradients(grads):
@@ -203,7 +204,6 @@ def clip_gradients(grads, max_norm, scale=1.0, outs=None, norm=None, stream=None
                                       status.data_ptr(), room_at, nbytes, handle)
         if code < 0:
             raise _b.ThdError(code, "thd_clip_gradients")
-        for x in grads if outs is None else outs:
-            torch.autograd.graph.increment_version(x)
+        torch.autograd.graph.increment_version(grads if outs is None else outs)
         return result, status
     return _run(call, stream)
