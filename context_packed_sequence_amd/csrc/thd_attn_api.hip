@@ -38,7 +38,8 @@ int64_t most_tiles(int64_t rows, int64_t runs, int64_t per) { return rows / per 
 Layout layout(const thd_attention_shape& s, void* workspace, bool backward) {
   Layout l{};
   const int64_t rows = s.total_tokens / s.cp_size;
-  const int64_t nq = most_tiles(rows, (s.cp_size > 1 ? 2LL : 1LL) * s.n_slots, thdcp::kAttnRows);
+  const int64_t nq = most_tiles(rows, (s.cp_size > 1 ? 2LL : 1LL) * s.n_slots,
+                                thdcp::kAttnRows / thdcp::attn_tile_heads(s.heads / s.kv_heads));
   const int64_t nk = backward ? most_tiles(s.total_tokens, s.n_slots, thdcp::kAttnKeys) : 0;
   if ((nq + nk + 8) * s.heads > INT32_MAX) {
     l.bytes = -1;
@@ -137,6 +138,7 @@ AttnArgs arguments(const thd_attention_shape& s, const Layout& l) {
   a.heads = s.heads;
   a.kv_heads = s.kv_heads;
   a.group = s.heads / s.kv_heads;
+  a.tile_heads = thdcp::attn_tile_heads(a.group);
   a.dim = s.dim;
   a.dtype = s.dtype;
   a.causal = s.causal;

@@ -48,15 +48,15 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
   const int32_t l = threadIdx.x & 63, word = l & 15;
   float most = 0.0f;
   if (static_cast<int32_t>(blockIdx.x) < query_blocks) {
-    const int32_t index = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-    if (index >= a.plan.header[kAttnQueryTiles]) return;
-    const QueryTile tile = a.plan.query_tiles[index];
-    const RowsRead o(head_rows(a.out, tile.row, head), static_cast<int32_t>(2 * a.out.row), tile.valid, a.dim);
-    const RowsRead g(head_rows(a.dout, tile.row, head), static_cast<int32_t>(2 * a.dout.row), tile.valid, a.dim);
-    float* delta = a.plan.delta + static_cast<int64_t>(head) * a.rows + tile.row;
+    const int32_t parts = a.heads / a.tile_heads, first_head = blockIdx.x % parts * a.tile_heads;
+    const QueryTile tile = a.plan.query_tiles[blockIdx.x / parts];
+    if (tile.rows == 0) return;
+    const int32_t tile_rows = kAttnRows / a.tile_heads;  // 32 and up: 16 rows are of one head
 #pragma unroll
     for (int i = 0; i < kAttnRows / 16; ++i) {
-      const int32_t row = 16 * i + (threadIdx.x >> 4);
+      const int32_t head = first_head + 16 * i / tile_rows, row = 16 * i % tile_rows + (threadIdx.x >> 4);
+      const RowsRead o(head_rows(a.out, tile.row, head), static_cast<int32_t>(2 * a.out.row), tile.valid, a.dim);
+      const RowsRead g(head_rows(a.dout, tile.row, head), static_cast<int32_t>(2 * a.dout.row), tile.valid, a.dim);
       const U32x4 x = o.load(row, word, a.dim), y = g.load(row, word, a.dim);
       float dot = 0.0f, square = 0.0f;
 #pragma unroll
@@ -70,14 +70,15 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
         }
       }
       dot = add_row16(dot);
-      if (word == 0 && row < tile.valid) delta[row] = dot;
+      if (word == 0 && row < tile.valid)
+        a.plan.delta[static_cast<int64_t>(head) * a.rows + tile.row + row] = dot;
       if constexpr (T::kNarrow) most = fmaxf(most, finite_or_zero(add_row16(square)));
     }
   } else if constexpr (T::kNarrow) {
     const int32_t b = blockIdx.x - query_blocks;
     const int32_t index = b / a.kv_heads, head = b % a.kv_heads;
-    if (index >= a.plan.header[kAttnKeyTiles]) return;
     const KeyTile tile = a.plan.key_tiles[index];
+    if (tile.keys == 0) return;
     const RowsRead v(head_rows(a.v, static_cast<int64_t>(tile.doc) + tile.key, head),
                      static_cast<int32_t>(2 * a.v.row), tile.valid, a.dim);
 #pragma unroll
@@ -112,47 +113,63 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
 // register): p, and dz times `held`.  lse and delta are the registers' or the
 // lane's, by the caller's functions of the register; scores not seen have p 0.
 template <typename T, bool kCap, typename Lse, typename Delta, typename Visible>
-__device__ __forceinline__ void score_gradients(const AttnArgs& a, F32x16& s, F32x16& dp, float held, Lse lse,
+__device__ __forceinline__ void score_gradients(const AttnArgs& a, F32x16 s, F32x16 dp, float held, Lse lse,
                                                 Delta delta, Visible visible, U32x4 (&p16)[2], U32x4 (&dz16)[2]) {
   const float factor = (kCap ? a.cap : a.scale) * kAttnLog2e;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    float z = s[r], slope = held;
-    if constexpr (kCap) {
-      z = attn_tanh(z * (a.scale / a.cap));
-      slope = held * fmaf(-z, z, 1.0f);
-    }
-    const float p = visible(r) ? attn_exp2(fmaf(z, factor, -lse(r))) : 0.0f;
-    s[r] = T::kNarrow ? p * kProbabilityScale : p;
-    dp[r] = p * (dp[r] - delta(r)) * slope;
-  }
+  if constexpr (kCap) attn_tanh(s, a.scale / a.cap);
 #pragma unroll
   for (int r = 0; r < 16; r += 2) {
-    p16[r >> 3][(r & 7) >> 1] = T::pack(s[r], s[r + 1]);
-    dz16[r >> 3][(r & 7) >> 1] = T::pack(dp[r], dp[r + 1]);
+    if (kCap && r % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // few registers at a time
+    float p[2], dz[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float z = s[r + e], slope = kCap ? held * fmaf(-z, z, 1.0f) : held;
+      p[e] = visible(r + e) ? attn_exp2(fmaf(z, factor, -lse(r + e))) : 0.0f;
+      dz[e] = p[e] * (dp[r + e] - delta(r + e)) * slope;
+      if (T::kNarrow) p[e] *= kProbabilityScale;
+    }
+    p16[r >> 3][(r & 7) >> 1] = T::pack(p[0], p[1]);
+    dz16[r >> 3][(r & 7) >> 1] = T::pack(dz[0], dz[1]);
   }
 }
 
-// acc [dim][32] += (rows [row, row + 32) of the tile)^T b
+// A number for each register's row of a C fragment, from this lane's first row on.
+__device__ __forceinline__ F32x16 lds_rows(const float* at) {
+  F32x16 r;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float4 x = *reinterpret_cast<const float4*>(at + 8 * g);
+    r[4 * g] = x.x, r[4 * g + 1] = x.y, r[4 * g + 2] = x.z, r[4 * g + 3] = x.w;
+  }
+  return r;
+}
+
+// A's half for 16 rows, from the addresses of its first and second 8.
+__device__ __forceinline__ U32x4 transposed_pair(const char* first, const char* second, int32_t from) {
+  const U32x2 x = lds_read_transposed(first + from), y = lds_read_transposed(second + from);
+  return U32x4{x[0], x[1], y[0], y[1]};
+}
+
+// acc [dim][32] += (32 rows of LDS from `from` on)^T b.  `from` is a constant where the
+// calls are inlined and goes into the reads' offset fields: one array of all tiles, so
+// that a lane holds one address for each place in a tile and not one for each tile.
 template <typename T, int kDim>
-__device__ __forceinline__ void add_transposed(F32x16 (&acc)[kDim / 32], const char* tile,
+__device__ __forceinline__ void add_transposed(F32x16 (&acc)[kDim / 32], const char* lds, int32_t from,
                                                const int32_t (&at)[kDim / 32][2], const U32x4 (&b)[2]) {
 #pragma unroll
   for (int t = 0; t < kDim / 32; ++t)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const U32x2 x = lds_read_transposed(tile + at[t][0] + j * 16 * 2 * kDim);
-      const U32x2 y = lds_read_transposed(tile + at[t][1] + j * 16 * 2 * kDim);
-      acc[t] = T::mfma(U32x4{x[0], x[1], y[0], y[1]}, b[j], acc[t]);
+      acc[t] = T::mfma(transposed_pair(lds + at[t][0], lds + at[t][1], from + j * 16 * 2 * kDim), b[j], acc[t]);
     }
 }
 
 template <typename T, int kDim>
-__device__ __forceinline__ F32x16 product(const char* tile, const int32_t (&at)[kDim / 16],
+__device__ __forceinline__ F32x16 product(const char* lds, int32_t from, const int32_t (&at)[kDim / 16],
                                           const U32x4 (&b)[kDim / 16]) {
   F32x16 c = zero16();
 #pragma unroll
-  for (int i = 0; i < kDim / 16; ++i) c = T::mfma(lds_read(tile, at[i]), b[i], c);
+  for (int i = 0; i < kDim / 16; ++i) c = T::mfma(lds_read(lds + at[i], from), b[i], c);
   return c;
 }
 
@@ -161,15 +178,15 @@ __device__ __forceinline__ F32x16 product(const char* tile, const int32_t (&at)[
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
   constexpr int kTile = kAttnStep * 2 * kDim;
-  __shared__ __attribute__((aligned(16))) char s_keys0[kTile], s_values0[kTile], s_keys1[kTile], s_values1[kTile];
-  const AttnPlace place(blockIdx.x, a.kv_heads, a.group);
-  if (place.tile >= a.plan.header[kAttnQueryTiles]) return;
+  __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile];  // keys, values, and both again
+  const AttnPlace place(blockIdx.x, a.kv_heads, a.group / a.tile_heads);
+  if (place.tile >= a.plan.max_query_tiles) return;
   const QueryTile tile = a.plan.query_tiles[place.tile];
+  if (tile.rows == 0) return;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t l = threadIdx.x & 63, c = l & 31, h = l >> 5;
-  const int32_t own_rows = min(32, max(0, tile.rows - 32 * wave));
-  const int32_t own_valid = min(32, max(0, tile.valid - 32 * wave));
-  const int32_t pos = tile.pos + 32 * wave;
+  const WaveRows own(a, tile, place, wave);
+  const int32_t pos = tile.pos + own.first;
   const float held = T::kNarrow ? gradient_scale(a.plan) : 1.0f;
 
   F32x16 dq[kDim / 32];
@@ -178,10 +195,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
   if (tile.valid > 0) {
     U32x4 q[kDim / 16], g[kDim / 16];
     int32_t row_at[kDim / 16], column_at[kDim / 32][2];
-    const RowsRead queries(head_rows(a.q, tile.row + 32 * wave, place.head), static_cast<int32_t>(2 * a.q.row),
-                           own_valid, a.dim);
-    const RowsRead grads(head_rows(a.dout, tile.row + 32 * wave, place.head), static_cast<int32_t>(2 * a.dout.row),
-                         own_valid, a.dim);
+    const RowsRead queries(head_rows(a.q, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.q.row),
+                           own.valid, a.dim);
+    const RowsRead grads(head_rows(a.dout, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.dout.row),
+                         own.valid, a.dim);
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) {
       q[i] = queries.load(c, 2 * i + h, a.dim);
@@ -194,8 +211,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
       column_at[t][1] = transposed_at<kDim>(t, 1);
     }
     float lse = kAttnInf, delta = 0.0f;  // of a row that sees nothing: p 0
-    if (c < own_valid) {
-      const int64_t at = static_cast<int64_t>(place.head) * a.rows + tile.row + 32 * wave + c;
+    if (c < own.valid) {
+      const int64_t at = static_cast<int64_t>(own.head) * a.rows + tile.row + own.first + c;
       const float x = a.lse[at] * kAttnLog2e;
       lse = x == -kAttnInf ? kAttnInf : x;
       delta = a.plan.delta[at];
@@ -204,23 +221,23 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
     const int32_t end = last.low + static_cast<int32_t>(last.span);
     int32_t key = first.low & ~(kAttnStep - 1);
     const Seen seen(a, pos + c, tile.real);
-    const auto load = [&](char* keys, char* values, int32_t at) {
+    const auto load = [&](int32_t to, int32_t at) {
       const int32_t n = min(kAttnStep, tile.real - at);
-      load_tile<kDim>(keys, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+      load_tile<kDim>(s_tiles + to, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
                                      static_cast<int32_t>(2 * a.k.row), n, a.dim), a.dim);
-      load_tile<kDim>(values, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+      load_tile<kDim>(s_tiles + to + kTile, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
                                        static_cast<int32_t>(2 * a.v.row), n, a.dim), a.dim);
     };
-    const auto turn = [&](const char* keys, const char* values, char* next_keys, char* next_values) {
+    const auto turn = [&](int32_t keys, int32_t next) {
       lds_arrived();
       __syncthreads();
-      if (key + kAttnStep < end) load(next_keys, next_values, key + kAttnStep);
+      if (key + kAttnStep < end) load(next, key + kAttnStep);
 #pragma unroll
       for (int b = 0; b < kAttnStep / 32; ++b) {
-        const int32_t k0 = key + 32 * b, at = 32 * b * 2 * kDim;
-        if (own_valid <= 0 || !sees_any(a, pos, own_valid, k0, 32, tile.real)) continue;
-        F32x16 s = product<T, kDim>(keys + at, row_at, q);
-        F32x16 dp = product<T, kDim>(values + at, row_at, g);
+        const int32_t k0 = key + 32 * b, at = keys + 32 * b * 2 * kDim;
+        if (own.valid <= 0 || !sees_any(a, pos, own.valid, k0, 32, tile.real)) continue;
+        F32x16 s = product<T, kDim>(s_tiles, at, row_at, q);
+        F32x16 dp = product<T, kDim>(s_tiles, at + kTile, row_at, g);
         U32x4 p16[2], dz16[2];
         const bool all = sees_all(a, pos, 32, k0, 32, tile.real);
         const auto lane_lse = [&](int) { return lse; };
@@ -230,21 +247,20 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
         else
           score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta,
                                    [&](int r) { return seen(k0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
-        add_transposed<T, kDim>(dq, keys + at, column_at, dz16);
+        add_transposed<T, kDim>(dq, s_tiles, at, column_at, dz16);
       }
       key += kAttnStep;
     };
-    load(s_keys0, s_values0, key);
+    load(0, key);
     while (key < end) {
-      turn(s_keys0, s_values0, s_keys1, s_values1);
+      turn(0, 2 * kTile);
       if (key >= end) break;
-      turn(s_keys1, s_values1, s_keys0, s_values0);
+      turn(2 * kTile, 0);
     }
     __syncthreads();
   }
-  char* own = wave == 0 ? s_keys0 : wave == 1 ? s_values0 : wave == 2 ? s_keys1 : s_values1;
-  store_rows<T, kDim>(own, dq, a.scale / held, const_cast<char*>(head_rows(a.dq, tile.row + 32 * wave, place.head)),
-                      2 * a.dq.row, own_rows, own_valid, a.dim);
+  store_rows<T, kDim>(s_tiles + wave * kTile, dq, a.scale / held, const_cast<char*>(head_rows(a.dq, tile.row + own.first, own.head)),
+                      2 * a.dq.row, own.rows, own.valid, a.dim);
 }
 
 // The query rows that a key tile's gradients come from: for each head of the
@@ -279,21 +295,30 @@ struct QueryWalk {
     range(a, k);
     settle(a, k);
   }
-  __device__ __forceinline__ void next(const AttnArgs& a, const KeyTile& k) {
-    row += kAttnStep;
+  __device__ __forceinline__ void next(const AttnArgs& a, const KeyTile& k, int32_t step) {
+    row += step;
     settle(a, k);
   }
 };
 
 // Key and value gradients: 128 keys of one key head a workgroup, 32 a wave.
+//
+// A wave holds its keys' rows and both sums in registers.  With 128 elements a head
+// that leaves no room for its values' rows beside two waves on each SIMD, of which one
+// computes probabilities while the other multiplies; they are read from LDS instead,
+// and query rows come 32 at a time, so that two workgroups share a compute unit's LDS.
 template <typename T, int kDim, bool kCap>
-__global__ __launch_bounds__(256, kDim == 64 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
-  constexpr int kTile = kAttnStep * 2 * kDim;
-  __shared__ __attribute__((aligned(16))) char s_queries0[kTile], s_grads0[kTile], s_queries1[kTile], s_grads1[kTile];
-  __shared__ __attribute__((aligned(16))) float s_lse[2][kAttnStep], s_delta[2][kAttnStep];
+__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
+  constexpr bool kHold = kDim == 64;           // values in registers
+  constexpr int kStep = kHold ? kAttnStep : 32;
+  constexpr int kTile = kStep * 2 * kDim;
+  // query rows, rows of dout, both again, values
+  __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile + (kHold ? 0 : kAttnKeys * 2 * kDim)];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
   const AttnPlace place(blockIdx.x, a.kv_heads, 1);
-  if (place.tile >= a.plan.header[kAttnKeyTiles]) return;
+  if (place.tile >= a.plan.max_key_tiles) return;
   const KeyTile tile = a.plan.key_tiles[place.tile];
+  if (tile.keys == 0) return;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t l = threadIdx.x & 63, c = l & 31, h = l >> 5;
   const int32_t own_keys = min(32, max(0, tile.keys - 32 * wave));
@@ -306,90 +331,109 @@ __global__ __launch_bounds__(256, kDim == 64 ? 2 : 1) void attn_dkv_kernel(AttnA
 #pragma unroll
   for (int t = 0; t < kDim / 32; ++t) dk[t] = dv[t] = zero16();
   if (tile.valid > 0) {
-    U32x4 k[kDim / 16], v[kDim / 16];
-    int32_t row_at[kDim / 16], column_at[kDim / 32][2];
+    U32x4 k[kDim / 16], v[kHold ? kDim / 16 : 1];
+    const int32_t row_at = lds_word<kDim>(c, h);
+    const int32_t column_at[2] = {transposed_at<kDim>(0, 0), transposed_at<kDim>(0, 1)};
     const RowsRead keys(head_rows(a.k, stream, place.kv_head), static_cast<int32_t>(2 * a.k.row), own_valid, a.dim);
-    const RowsRead values(head_rows(a.v, stream, place.kv_head), static_cast<int32_t>(2 * a.v.row), own_valid, a.dim);
 #pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) {
-      k[i] = keys.load(c, 2 * i + h, a.dim);
-      v[i] = values.load(c, 2 * i + h, a.dim);
-      row_at[i] = lds_word<kDim>(c, 2 * i + h);
-    }
+    for (int i = 0; i < kDim / 16; ++i) k[i] = keys.load(c, 2 * i + h, a.dim);
+    if constexpr (kHold) {
+      const RowsRead values(head_rows(a.v, stream, place.kv_head), static_cast<int32_t>(2 * a.v.row), own_valid, a.dim);
 #pragma unroll
-    for (int t = 0; t < kDim / 32; ++t) {
-      column_at[t][0] = transposed_at<kDim>(t, 0);
-      column_at[t][1] = transposed_at<kDim>(t, 1);
+      for (int i = 0; i < kDim / 16; ++i) v[i] = values.load(c, 2 * i + h, a.dim);
+    } else {
+      const RowsRead values(head_rows(a.v, static_cast<int64_t>(tile.doc) + tile.key, place.kv_head),
+                            static_cast<int32_t>(2 * a.v.row), tile.valid, a.dim);
+      load_tile<kDim, kAttnKeys>(s_tiles + 4 * kTile, values, a.dim);
     }
     QueryWalk walk(a, tile, place.kv_head);
     // positions that see key key + c
     const Seen seen(a.causal ? key + c : a.window ? key + c - a.window + 1 : 0,
                     a.window ? (a.causal ? a.window : 2u * a.window - 1u) : 0x7fffffffu);
-    float next_lse = kAttnInf, next_delta = 0.0f;
-    const auto load = [&](char* queries, char* grads) {
-      const int32_t n = min(kAttnStep, walk.end - walk.row);
+    float next_lse = -kAttnInf, next_delta = 0.0f;
+    // what scores start from, or (with a cap) is taken from their power of two
+    const float lse_factor = kCap ? kAttnLog2e : -1.0f / a.scale;
+    const auto load = [&](int32_t to) {
+      const int32_t n = min(kStep, walk.end - walk.row);
       const int64_t row = static_cast<int64_t>(tile.first) + walk.chunk * tile.chunk + walk.row;
-      load_tile<kDim>(queries, RowsRead(head_rows(a.q, row, walk.head), static_cast<int32_t>(2 * a.q.row), n, a.dim),
-                      a.dim);
-      load_tile<kDim>(grads, RowsRead(head_rows(a.dout, row, walk.head), static_cast<int32_t>(2 * a.dout.row), n,
-                                      a.dim), a.dim);
-      next_lse = kAttnInf;  // rows past the range: p 0
+      load_tile<kDim, kStep>(s_tiles + to, RowsRead(head_rows(a.q, row, walk.head), static_cast<int32_t>(2 * a.q.row), n,
+                                               a.dim), a.dim);
+      load_tile<kDim, kStep>(s_tiles + to + kTile, RowsRead(head_rows(a.dout, row, walk.head), static_cast<int32_t>(2 * a.dout.row),
+                                             n, a.dim), a.dim);
+      next_lse = kCap ? kAttnInf : -kAttnInf;  // rows past the range: p 0
       next_delta = 0.0f;
       if (static_cast<int32_t>(threadIdx.x) < n) {
         const int64_t at = static_cast<int64_t>(walk.head) * a.rows + row + threadIdx.x;
-        const float x = a.lse[at] * kAttnLog2e;
-        next_lse = x == -kAttnInf ? kAttnInf : x;
-        next_delta = a.plan.delta[at];
+        const float x = a.lse[at];
+        if (x != -kAttnInf) next_lse = x * lse_factor;
+        next_delta = -a.plan.delta[at];
       }
     };
-    const auto turn = [&](const char* queries, const char* grads, int32_t mine, char* next_queries,
-                          char* next_grads) {
-      if (threadIdx.x < kAttnStep) {
+    const auto turn = [&](int32_t queries, int32_t mine, int32_t next) {
+      if (threadIdx.x < kStep) {
         s_lse[mine][threadIdx.x] = next_lse;
         s_delta[mine][threadIdx.x] = next_delta;
       }
       lds_arrived();
       __syncthreads();
-      const int32_t n = min(kAttnStep, walk.end - walk.row);
+      const int32_t n = min(kStep, walk.end - walk.row);
       const int32_t pos = walk.position(a, tile) + walk.row;
-      walk.next(a, tile);
-      if (!walk.done()) load(next_queries, next_grads);
+      walk.next(a, tile, kStep);
+      if (!walk.done()) load(next);
 #pragma unroll
-      for (int b = 0; b < kAttnStep / 32; ++b) {
-        const int32_t p0 = pos + 32 * b, at = 32 * b * 2 * kDim;
+      for (int b = 0; b < kStep / 32; ++b) {
+        const int32_t p0 = pos + 32 * b, at = queries + 32 * b * 2 * kDim;
         if (32 * b >= n || own_valid <= 0 || !sees_any(a, p0, min(32, n - 32 * b), key, own_valid, tile.real)) continue;
-        F32x16 s = product<T, kDim>(queries + at, row_at, k);
-        F32x16 dp = product<T, kDim>(grads + at, row_at, v);
-        float lse[16], delta[16];
+        // A lane's places in a tile differ in single bits from word to word: one address
+        // each for rows, columns and values, hidden from the compiler so that it does not
+        // keep all of them in registers.
+        int32_t row = row_at, first = column_at[0], second = column_at[1], value = row_at + 32 * wave * 2 * kDim;
+        asm volatile("" : "+v"(row), "+v"(first), "+v"(second), "+v"(value));
+        // the sums start at what is taken from them: -lse (as a score; with a cap, after it)
+        // and -delta
+        F32x16 s = kCap ? zero16() : lds_rows(&s_lse[mine][32 * b + 4 * h]);
+        F32x16 dp = lds_rows(&s_delta[mine][32 * b + 4 * h]);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 x = *reinterpret_cast<const float4*>(&s_lse[mine][32 * b + 8 * g + 4 * h]);
-          const float4 y = *reinterpret_cast<const float4*>(&s_delta[mine][32 * b + 8 * g + 4 * h]);
-          lse[4 * g] = x.x, lse[4 * g + 1] = x.y, lse[4 * g + 2] = x.z, lse[4 * g + 3] = x.w;
-          delta[4 * g] = y.x, delta[4 * g + 1] = y.y, delta[4 * g + 2] = y.z, delta[4 * g + 3] = y.w;
+        for (int i = 0; i < kDim / 16; ++i) {
+          const char* x = s_tiles + (row ^ (32 * i));
+          s = T::mfma(lds_read(x, at), k[i], s);
+          dp = T::mfma(lds_read(x, at + kTile),
+                       kHold ? v[kHold ? i : 0] : lds_read(s_tiles + (value ^ (32 * i)), 4 * kTile), dp);
         }
+        __builtin_amdgcn_sched_barrier(0);
         U32x4 p16[2], dz16[2];
-        const auto row_lse = [&](int r) { return lse[r]; };
-        const auto row_delta = [&](int r) { return delta[r]; };
+        const float* lse = &s_lse[mine][32 * b + 4 * h];
+        const auto row_lse = [&](int r) { return kCap ? lse[(r & 3) + 8 * (r >> 2)] : 0.0f; };
+        const auto no_delta = [](int) { return 0.0f; };
         // pads among the keys are other lanes' and are not stored
         if (sees_all(a, p0, 32, key, 32, INT32_MAX))
-          score_gradients<T, kCap>(a, s, dp, held, row_lse, row_delta, [](int) { return true; }, p16, dz16);
+          score_gradients<T, kCap>(a, s, dp, held, row_lse, no_delta, [](int) { return true; }, p16, dz16);
         else
-          score_gradients<T, kCap>(a, s, dp, held, row_lse, row_delta,
+          score_gradients<T, kCap>(a, s, dp, held, row_lse, no_delta,
                                    [&](int r) { return seen(p0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
-        add_transposed<T, kDim>(dv, grads + at, column_at, p16);
-        add_transposed<T, kDim>(dk, queries + at, column_at, dz16);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < kDim / 32; ++t) {
+          const char *x = s_tiles + (first ^ (64 * t)), *y = s_tiles + (second ^ (64 * t));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int32_t from = at + j * 16 * 2 * kDim;
+            dv[t] = T::mfma(transposed_pair(x, y, from + kTile), p16[j], dv[t]);
+            dk[t] = T::mfma(transposed_pair(x, y, from), dz16[j], dk[t]);
+          }
+        }
       }
     };
-    if (!walk.done()) load(s_queries0, s_grads0);
+    if (!walk.done()) load(0);
     while (!walk.done()) {
-      turn(s_queries0, s_grads0, 0, s_queries1, s_grads1);
+      turn(0, 0, 2 * kTile);
       if (walk.done()) break;
-      turn(s_queries1, s_grads1, 1, s_queries0, s_grads0);
+      turn(2 * kTile, 1, 0);
     }
     __syncthreads();
   }
-  char* own = wave == 0 ? s_queries0 : wave == 1 ? s_grads0 : wave == 2 ? s_queries1 : s_grads1;
+  // 32 rows of the results for each wave
+  char* own = s_tiles + wave * kTile;
   store_rows<T, kDim>(own, dk, a.scale / held, const_cast<char*>(head_rows(a.dk, stream, place.kv_head)),
                       2 * a.dk.row, own_keys, own_valid, a.dim);
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -402,7 +446,7 @@ __global__ __launch_bounds__(256, kDim == 64 ? 2 : 1) void attn_dkv_kernel(AttnA
 
 template <typename T>
 hipError_t delta(const AttnArgs& a, hipStream_t stream) {
-  const int32_t query_blocks = a.plan.max_query_tiles * a.heads;
+  const int32_t query_blocks = a.plan.max_query_tiles * (a.heads / a.tile_heads);
   const int32_t blocks = query_blocks + (T::kNarrow ? a.plan.max_key_tiles * a.kv_heads : 0);
   attn_delta_kernel<T><<<blocks, 256, 0, stream>>>(a, query_blocks);
   return hipGetLastError();
@@ -411,7 +455,7 @@ hipError_t delta(const AttnArgs& a, hipStream_t stream) {
 template <typename T, int kDim>
 hipError_t dq(const AttnArgs& a, hipStream_t stream) {
   const int32_t units = a.plan.max_query_tiles * a.kv_heads;
-  const dim3 grid((units + 7) / 8 * 8 * a.group);
+  const dim3 grid((units + 7) / 8 * 8 * (a.group / a.tile_heads));
   if (a.cap > 0.0f) attn_dq_kernel<T, kDim, true><<<grid, 256, 0, stream>>>(a);
   else attn_dq_kernel<T, kDim, false><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();

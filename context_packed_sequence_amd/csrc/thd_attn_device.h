@@ -82,9 +82,30 @@ __device__ __forceinline__ F32x16 zero16() {
 
 __device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// tanh(x) = 1 - 2 / (1 + e^(2x)), its ends included
-__device__ __forceinline__ float attn_tanh(float x) {
-  return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + attn_exp2(2.0f * kAttnLog2e * x));
+// s = tanh(s in), element by element.  Scores are mostly well below their cap, and for
+// |x| <= 0.75 a polynomial takes fewer cycles than the two quarter-rate instructions of
+// 1 - 2 / (1 + e^(2x)), and keeps its relative precision near 0 (minimax over the
+// interval, error 3.3e-8 before rounding; the other form is off by up to 2^-23
+// absolute).  Taken where no lane's score is larger.
+__device__ __forceinline__ void attn_tanh(F32x16& s, float in) {
+  float top = fmaxf(fabsf(s[0]), fabsf(s[1]));
+#pragma unroll
+  for (int r = 2; r < 16; r += 2) top = fmaxf(fmaxf(top, fabsf(s[r])), fabsf(s[r + 1]));
+  if (!__any(top * in > 0.75f)) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const float x = s[r] * in, u = x * x;
+      float p = fmaf(u, -0.00476947f, 0.01966489f);
+      p = fmaf(u, p, -0.05339025f);
+      p = fmaf(u, p, 0.13326521f);
+      p = fmaf(u, p, -0.33333068f);
+      s[r] = fmaf(x, u * p, x);
+    }
+    return;
+  }
+  const float in2 = 2.0f * kAttnLog2e * in;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + attn_exp2(s[r] * in2));
 }
 
 // Value of lane l ^ 32, combined.
@@ -157,15 +178,15 @@ __device__ __forceinline__ const char* head_rows(const AttnTensor& t, int64_t ro
   return static_cast<const char*>(t.data) + 2 * (row * t.row + static_cast<int64_t>(head) * t.head);
 }
 
-// Moves kAttnStep rows into an LDS tile, 16 bytes a lane and turn straight from
+// Moves kRows rows into an LDS tile, 16 bytes a lane and turn straight from
 // memory (no registers in between); the caller waits (lds_arrived) before the
 // barrier after which the tile is read.
-template <int kDim>
+template <int kDim, int kRows = kAttnStep>
 __device__ __forceinline__ void load_tile(char* tile, const RowsRead& r, int32_t dim) {
   constexpr int kWords = kDim / 8;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-  for (int j = 0; j < kAttnStep * kWords / 256; ++j) {
+  for (int j = 0; j < kRows * kWords / 256; ++j) {
     const int32_t s = j * 256 + threadIdx.x;
     const int32_t row = s / kWords;
     const int32_t w = (s % kWords) ^ lds_swizzle<kDim>(row);
@@ -217,17 +238,29 @@ __device__ __forceinline__ bool sees_any(const AttnArgs& a, int32_t p, int32_t n
   return !(a.window && !a.causal && k - (p + np - 1) >= a.window);
 }
 
-// Tile and head of workgroup b, which runs on XCD b mod 8: the heads of a group
-// read the same keys, and stay on one XCD one after the other; tiles of a key
-// head are dealt out so that, with 8 key heads, each XCD keeps to one of them.
+// Tile and heads of workgroup b, which runs on XCD b mod 8: the workgroups of a group
+// read the same keys, and stay on one XCD one after the other; tiles of a key head are
+// dealt out so that, with 8 key heads, each XCD keeps to one of them.  `parts`:
+// workgroups of a group.
 struct AttnPlace {
-  int32_t tile, kv_head, head;
-  __device__ __forceinline__ AttnPlace(int32_t b, int32_t kv_heads, int32_t group) {
+  int32_t tile, kv_head, part;
+  __device__ __forceinline__ AttnPlace(int32_t b, int32_t kv_heads, int32_t parts) {
     const int32_t j = b >> 3;
-    const int32_t unit = (j / group) * 8 + (b & 7);
+    const int32_t unit = (j / parts) * 8 + (b & 7);
     tile = unit / kv_heads;
     kv_head = unit % kv_heads;
-    head = kv_head * group + j % group;
+    part = j % parts;
+  }
+};
+
+// A wave's 32 query rows of a workgroup's tile.
+struct WaveRows {
+  int32_t head, first, rows, valid;  // first: within the tile
+  __device__ __forceinline__ WaveRows(const AttnArgs& a, const QueryTile& tile, const AttnPlace& place, int32_t wave) {
+    head = place.kv_head * a.group + place.part * a.tile_heads + wave % a.tile_heads;
+    first = 32 * (wave / a.tile_heads);
+    rows = min(32, max(0, tile.rows - first));
+    valid = min(32, max(0, tile.valid - first));
   }
 };
 

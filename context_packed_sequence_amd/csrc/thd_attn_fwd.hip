@@ -41,9 +41,12 @@ struct ForwardWave {
     }
   }
 
-  // Keys key0 .. key0 + 63; `partly`: the rows do not see all of them.
-  __device__ __forceinline__ void step(const AttnArgs& a, const char* keys, const char* values, int32_t key0,
-                                       bool partly, const Seen& seen) {
+  // Keys key0 .. key0 + 63, whose tile is at `keys` in LDS and their values' after it;
+  // `partly`: the rows do not see all of them.  `keys` is a constant where the calls are
+  // inlined and goes into the reads' offset fields.
+  __device__ __forceinline__ void step(const AttnArgs& a, const char* lds, int32_t keys, int32_t key0, bool partly,
+                                       const Seen& seen) {
+    const int32_t values = keys + kAttnStep * 2 * kDim;
     const int32_t h = (threadIdx.x & 63) >> 5;
     F32x16 s[2];
 #pragma unroll
@@ -51,17 +54,15 @@ struct ForwardWave {
       s[b] = zero16();
 #pragma unroll
       for (int i = 0; i < kDim / 16; ++i)
-        s[b] = T::mfma(lds_read(keys, key_at[i] + b * 32 * 2 * kDim), q[i], s[b]);
+        s[b] = T::mfma(lds_read(lds + key_at[i], keys + b * 32 * 2 * kDim), q[i], s[b]);
     }
     // scores in powers of two: z log2(e) = s factor
     float factor = a.scale * kAttnLog2e;
     if constexpr (kCap) {
       const float in = a.scale / a.cap;
       factor = a.cap * kAttnLog2e;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[b][r] = attn_tanh(s[b][r] * in);
+      attn_tanh(s[0], in);
+      attn_tanh(s[1], in);
     }
     if (partly) {
 #pragma unroll
@@ -103,8 +104,8 @@ struct ForwardWave {
     for (int t = 0; t < kDim / 32; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const U32x2 x = lds_read_transposed(values + value_at[t][0] + j * 16 * 2 * kDim);
-        const U32x2 y = lds_read_transposed(values + value_at[t][1] + j * 16 * 2 * kDim);
+        const U32x2 x = lds_read_transposed(lds + value_at[t][0] + (values + j * 16 * 2 * kDim));
+        const U32x2 y = lds_read_transposed(lds + value_at[t][1] + (values + j * 16 * 2 * kDim));
         o[t] = T::mfma(U32x4{x[0], x[1], y[0], y[1]}, p[j], o[t]);
       }
   }
@@ -113,20 +114,20 @@ struct ForwardWave {
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 2) void attn_forward_kernel(AttnArgs a) {
   constexpr int kTile = kAttnStep * 2 * kDim;  // bytes
-  __shared__ __attribute__((aligned(16))) char s_keys0[kTile], s_values0[kTile], s_keys1[kTile], s_values1[kTile];
-  const AttnPlace place(blockIdx.x, a.kv_heads, a.group);
-  if (place.tile >= a.plan.header[kAttnQueryTiles]) return;
+  __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile];  // keys, values, and both again
+  const AttnPlace place(blockIdx.x, a.kv_heads, a.group / a.tile_heads);
+  if (place.tile >= a.plan.max_query_tiles) return;
   const QueryTile tile = a.plan.query_tiles[place.tile];
+  if (tile.rows == 0) return;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t l = threadIdx.x & 63, c = l & 31;
-  const int32_t own_rows = min(32, max(0, tile.rows - 32 * wave));     // of this wave
-  const int32_t own_valid = min(32, max(0, tile.valid - 32 * wave));
-  const int32_t pos = tile.pos + 32 * wave;
+  const WaveRows own(a, tile, place, wave);
+  const int32_t pos = tile.pos + own.first;
 
   ForwardWave<T, kDim, kCap> w;
   if (tile.valid > 0) {
-    const RowsRead queries(head_rows(a.q, tile.row + 32 * wave, place.head), static_cast<int32_t>(2 * a.q.row),
-                           own_valid, a.dim);
+    const RowsRead queries(head_rows(a.q, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.q.row),
+                           own.valid, a.dim);
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) w.q[i] = queries.load(c, 2 * i + (l >> 5), a.dim);
 
@@ -134,43 +135,43 @@ __global__ __launch_bounds__(256, 2) void attn_forward_kernel(AttnArgs a) {
     const int32_t end = last.low + static_cast<int32_t>(last.span);
     int32_t key = first.low & ~(kAttnStep - 1);
     const Seen seen(a, pos + c, tile.real);
-    const auto load = [&](char* keys, char* values, int32_t at) {
+    const auto load = [&](int32_t to, int32_t at) {
       const int32_t n = min(kAttnStep, tile.real - at);
-      load_tile<kDim>(keys, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+      load_tile<kDim>(s_tiles + to, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
                                      static_cast<int32_t>(2 * a.k.row), n, a.dim), a.dim);
-      load_tile<kDim>(values, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
+      load_tile<kDim>(s_tiles + to + kTile, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
                                        static_cast<int32_t>(2 * a.v.row), n, a.dim), a.dim);
     };
-    const auto turn = [&](const char* keys, const char* values, char* next_keys, char* next_values) {
+    const auto turn = [&](int32_t keys, int32_t next) {
       lds_arrived();
       __syncthreads();  // the tile is there, and nobody reads the one before
-      if (key + kAttnStep < end) load(next_keys, next_values, key + kAttnStep);
-      if (own_valid > 0 && sees_any(a, pos, own_valid, key, kAttnStep, tile.real))
-        w.step(a, keys, values, key, !sees_all(a, pos, 32, key, kAttnStep, tile.real), seen);
+      if (key + kAttnStep < end) load(next, key + kAttnStep);
+      if (own.valid > 0 && sees_any(a, pos, own.valid, key, kAttnStep, tile.real))
+        w.step(a, s_tiles, keys, key, !sees_all(a, pos, 32, key, kAttnStep, tile.real), seen);
       key += kAttnStep;
     };
-    load(s_keys0, s_values0, key);
+    load(0, key);
     while (key < end) {
-      turn(s_keys0, s_values0, s_keys1, s_values1);
+      turn(0, 2 * kTile);
       if (key >= end) break;
-      turn(s_keys1, s_values1, s_keys0, s_values0);
+      turn(2 * kTile, 0);
     }
     __syncthreads();
   }
   const float sum = add_halves(w.sum);
   const float inverse = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
-  char* own = wave == 0 ? s_keys0 : wave == 1 ? s_values0 : wave == 2 ? s_keys1 : s_values1;
-  store_rows<T, kDim>(own, w.o, inverse, const_cast<char*>(head_rows(a.out, tile.row + 32 * wave, place.head)),
-                      2 * a.out.row, own_rows, own_valid, a.dim);
-  if (l < own_rows)
-    a.lse[static_cast<int64_t>(place.head) * a.rows + tile.row + 32 * wave + l] =
-        l < own_valid ? (w.top + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -kAttnInf;
+  store_rows<T, kDim>(s_tiles + wave * kTile, w.o, inverse,
+                      const_cast<char*>(head_rows(a.out, tile.row + own.first, own.head)), 2 * a.out.row, own.rows,
+                      own.valid, a.dim);
+  if (l < own.rows)
+    a.lse[static_cast<int64_t>(own.head) * a.rows + tile.row + own.first + l] =
+        l < own.valid ? (w.top + __builtin_amdgcn_logf(sum)) * kAttnLn2 : -kAttnInf;
 }
 
 template <typename T, int kDim>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const int32_t units = a.plan.max_query_tiles * a.kv_heads;
-  const dim3 grid((units + 7) / 8 * 8 * a.group);
+  const dim3 grid((units + 7) / 8 * 8 * (a.group / a.tile_heads));
   if (a.cap > 0.0f) attn_forward_kernel<T, kDim, true><<<grid, 256, 0, stream>>>(a);
   else attn_forward_kernel<T, kDim, false><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();

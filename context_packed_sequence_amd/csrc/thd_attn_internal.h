@@ -10,15 +10,20 @@
 
 namespace thdcp {
 
-constexpr int kAttnRows = 128;   // query rows of a workgroup: 32 in each of its 4 waves
+constexpr int kAttnRows = 128;   // query rows of a workgroup, over all its heads: 32 in each of its 4 waves
 constexpr int kAttnKeys = 128;   // keys of a workgroup that computes their gradients
 constexpr int kAttnStep = 64;    // keys (or query rows) that a workgroup moves through LDS at a time
+
+// Heads of a group whose queries a workgroup takes together, the same rows of each: its
+// waves then walk through the same keys to the same end, and a tile of few rows ends
+// nearer to the diagonal and to the document's end.
+constexpr int32_t attn_tile_heads(int32_t group) { return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
 
 // Query rows of one workgroup: a run of rows of one document's share.  Rows
 // [valid, rows) are pads.
 struct QueryTile {
   int32_t row;       // first row of the share
-  int32_t rows;      // 1..kAttnRows
+  int32_t rows;      // 1..kAttnRows / tile heads; 0: no tile
   int32_t valid;     // rows that hold tokens
   int32_t pos;       // position in the document of the first row
   int32_t doc;       // stream row of the document's first token
@@ -31,7 +36,7 @@ struct QueryTile {
 // the length of each of its two zigzag chunks (the whole document if cp is 1).
 struct KeyTile {
   int32_t key;       // position in the document of the first key
-  int32_t keys;      // 1..kAttnKeys
+  int32_t keys;      // 1..kAttnKeys; 0: no tile
   int32_t valid;
   int32_t doc;
   int32_t real;
@@ -41,15 +46,14 @@ struct KeyTile {
 };
 
 // Workspace, written by the plan kernel.
-enum AttnHeader : int { kAttnCode = 0, kAttnQueryTiles = 1, kAttnKeyTiles = 2, kAttnMaxGrad = 3, kAttnMaxValue = 4,
-                        kAttnHeaderWords = 16 };
+enum AttnHeader : int { kAttnMaxGrad = 0, kAttnMaxValue = 1, kAttnHeaderWords = 16 };
 
 struct AttnPlan {
   int32_t* header;         // [kAttnHeaderWords]
   int32_t* query_first;    // [slots + 1] tiles of the slots before
   int32_t* key_first;      // [slots + 1], null without key tiles
-  QueryTile* query_tiles;  // heaviest first
-  KeyTile* key_tiles;
+  QueryTile* query_tiles;  // [max_query_tiles], heaviest first, those without rows last
+  KeyTile* key_tiles;      // [max_key_tiles]
   float* delta;            // [heads][rows], backward only
   int32_t max_query_tiles;
   int32_t max_key_tiles;
@@ -69,6 +73,7 @@ struct AttnArgs {
   int32_t* status;         // or null
   int32_t n_slots, total, rows;
   int32_t heads, kv_heads, group, dim, dtype;
+  int32_t tile_heads;      // heads of a group in a workgroup
   int32_t causal, window;  // window 0: none
   int32_t cp, rank;
   float scale, cap;        // cap 0: none

@@ -39,17 +39,18 @@ struct Slot {
 };
 
 __device__ __forceinline__ int32_t query_tiles_of(const AttnArgs& a, const Slot& s) {
-  return (a.cp == 1 ? 1 : 2) * tiles_of(s.chunk, kAttnRows);
+  return (a.cp == 1 ? 1 : 2) * tiles_of(s.chunk, kAttnRows / a.tile_heads);
 }
 
 // Tile t of a slot's query tiles, and its weight: the keys it looks at.
 __device__ QueryTile query_tile(const AttnArgs& a, const Slot& s, int32_t t, int32_t* weight) {
   QueryTile q{};
-  const int32_t per = tiles_of(s.chunk, kAttnRows);
+  const int32_t tile_rows = kAttnRows / a.tile_heads;
+  const int32_t per = tiles_of(s.chunk, tile_rows);
   const int32_t second = t >= per ? 1 : 0;
-  const int32_t at = (t - second * per) * kAttnRows;
+  const int32_t at = (t - second * per) * tile_rows;
   q.row = s.first + second * s.chunk + at;
-  q.rows = min(kAttnRows, s.chunk - at);
+  q.rows = min(tile_rows, s.chunk - at);
   q.pos = at + (a.cp == 1 ? 0 : second ? (2 * a.cp - 1 - a.rank) * s.chunk : a.rank * s.chunk);
   q.valid = max(0, min(q.rows, s.real - q.pos));
   q.doc = s.start;
@@ -113,9 +114,11 @@ __device__ __forceinline__ int32_t slot_of(const int32_t* first, int32_t n_slots
   return low;
 }
 
-// Places n tiles by falling weight: make(t, &weight) describes tile t.
+// Places n tiles by falling weight: make(t, &weight) describes tile t.  Places up to
+// `most` hold no tile.
 template <typename Tile, typename Make>
-__device__ void place_tiles(int32_t n, Tile* out, int32_t* s_bucket, Make make) {
+__device__ void place_tiles(int32_t n, int32_t most, Tile* out, int32_t* s_bucket, Make make) {
+  for (int32_t t = n + threadIdx.x; t < most; t += kPlanThreads) out[t] = Tile{};
   for (int32_t b = threadIdx.x; b < kBuckets; b += kPlanThreads) s_bucket[b] = 0;
   __syncthreads();
   for (int32_t t = threadIdx.x; t < n; t += kPlanThreads) {
@@ -171,32 +174,27 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnArgs a) {
   const int32_t code = severity_to_code(s_severity);
   if (threadIdx.x == 0) {
     if (a.status) *a.status = code;
-    p.header[kAttnCode] = code;
     p.header[kAttnMaxGrad] = 0;
     p.header[kAttnMaxValue] = 0;
   }
-  if (code != THD_OK) {
-    if (threadIdx.x == 0) p.header[kAttnQueryTiles] = p.header[kAttnKeyTiles] = 0;
+  if (code != THD_OK) {  // no tiles: nothing is written
+    for (int32_t t = threadIdx.x; t < p.max_query_tiles; t += kPlanThreads) p.query_tiles[t] = QueryTile{};
+    for (int32_t t = threadIdx.x; t < p.max_key_tiles; t += kPlanThreads) p.key_tiles[t] = KeyTile{};
     return;
   }
   const int32_t nq = slot_prefix(a.n_slots, p.query_first, s_wave,
                                  [&](int32_t s) { return query_tiles_of(a, Slot(a, s)); });
-  place_tiles(nq, p.query_tiles, s_bucket, [&](int32_t t, int32_t* weight) {
+  place_tiles(nq, p.max_query_tiles, p.query_tiles, s_bucket, [&](int32_t t, int32_t* weight) {
     const int32_t s = slot_of(p.query_first, a.n_slots, t);
     return query_tile(a, Slot(a, s), t - p.query_first[s], weight);
   });
-  int32_t nk = 0;
   if (p.key_tiles) {
-    nk = slot_prefix(a.n_slots, p.key_first, s_wave,
+    const int32_t nk = slot_prefix(a.n_slots, p.key_first, s_wave,
                      [&](int32_t s) { return tiles_of(Slot(a, s).padded, kAttnKeys); });
-    place_tiles(nk, p.key_tiles, s_bucket, [&](int32_t t, int32_t* weight) {
+    place_tiles(nk, p.max_key_tiles, p.key_tiles, s_bucket, [&](int32_t t, int32_t* weight) {
       const int32_t s = slot_of(p.key_first, a.n_slots, t);
       return key_tile(a, Slot(a, s), t - p.key_first[s], weight);
     });
-  }
-  if (threadIdx.x == 0) {
-    p.header[kAttnQueryTiles] = nq;
-    p.header[kAttnKeyTiles] = nk;
   }
 }
 
