@@ -144,12 +144,6 @@ __device__ __forceinline__ F32x16 lds_rows(const float* at) {
   return r;
 }
 
-// A's half for 16 rows, from the addresses of its first and second 8.
-__device__ __forceinline__ U32x4 transposed_pair(const char* first, const char* second, int32_t from) {
-  const U32x2 x = lds_read_transposed(first + from), y = lds_read_transposed(second + from);
-  return U32x4{x[0], x[1], y[0], y[1]};
-}
-
 // acc [dim][32] += (32 rows of LDS from `from` on)^T b.  `from` is a constant where the
 // calls are inlined and goes into the reads' offset fields: one array of all tiles, so
 // that a lane holds one address for each place in a tile and not one for each tile.
@@ -221,25 +215,25 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
     const int32_t end = last.low + static_cast<int32_t>(last.span);
     int32_t key = first.low & ~(kAttnStep - 1);
     const Seen seen(a, pos + c, tile.real);
-    const auto load = [&](int32_t to, int32_t at) {
-      const int32_t n = min(kAttnStep, tile.real - at);
-      load_tile<kDim>(s_tiles + to, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
-                                     static_cast<int32_t>(2 * a.k.row), n, a.dim), a.dim);
-      load_tile<kDim>(s_tiles + to + kTile, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
-                                       static_cast<int32_t>(2 * a.v.row), n, a.dim), a.dim);
+    RowsWalk keys(a.k, static_cast<int64_t>(tile.doc) + key, place.kv_head, tile.real - key);
+    RowsWalk values(a.v, static_cast<int64_t>(tile.doc) + key, place.kv_head, tile.real - key);
+    const KeySteps steps(a, pos, 32, own.valid, tile.real);
+    const auto load = [&](int32_t to) {
+      keys.load<kDim, kAttnStep>(s_tiles + to, a.dim);
+      values.load<kDim, kAttnStep>(s_tiles + to + kTile, a.dim);
     };
-    const auto turn = [&](int32_t keys, int32_t next) {
+    const auto turn = [&](int32_t now, int32_t next) {
       lds_arrived();
       __syncthreads();
-      if (key + kAttnStep < end) load(next, key + kAttnStep);
+      if (key + kAttnStep < end) load(next);
 #pragma unroll
       for (int b = 0; b < kAttnStep / 32; ++b) {
-        const int32_t k0 = key + 32 * b, at = keys + 32 * b * 2 * kDim;
-        if (own.valid <= 0 || !sees_any(a, pos, own.valid, k0, 32, tile.real)) continue;
+        const int32_t k0 = key + 32 * b, at = now + 32 * b * 2 * kDim;
+        if (k0 < steps.any || k0 >= steps.any_end) continue;
         F32x16 s = product<T, kDim>(s_tiles, at, row_at, q);
         F32x16 dp = product<T, kDim>(s_tiles, at + kTile, row_at, g);
         U32x4 p16[2], dz16[2];
-        const bool all = sees_all(a, pos, 32, k0, 32, tile.real);
+        const bool all = k0 >= steps.all && k0 < steps.all_end;
         const auto lane_lse = [&](int) { return lse; };
         const auto lane_delta = [&](int) { return delta; };
         if (all)
@@ -251,7 +245,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
       }
       key += kAttnStep;
     };
-    load(0, key);
+    load(0);
     while (key < end) {
       turn(0, 2 * kTile);
       if (key >= end) break;

@@ -154,6 +154,12 @@ __device__ __forceinline__ U32x2 lds_read_transposed(const char* at) {
   return __builtin_bit_cast(U32x2, r);
 }
 
+// A's half for 16 rows, from the addresses of its first and second 8.
+__device__ __forceinline__ U32x4 transposed_pair(const char* first, const char* second, int32_t from) {
+  const U32x2 x = lds_read_transposed(first + from), y = lds_read_transposed(second + from);
+  return U32x4{x[0], x[1], y[0], y[1]};
+}
+
 // Rows [0, valid) of one head, from `base` on, behind a buffer resource of
 // exactly their size: a word past the last row, or past the head's elements, is
 // read as zeros.  The resource is built anew for each tile, so that offsets stay
@@ -220,6 +226,38 @@ struct Seen {
   __device__ __forceinline__ Seen(int32_t first, uint32_t n) : low(first), span(n) {}
   __device__ __forceinline__ bool operator()(int32_t key) const {
     return static_cast<uint32_t>(key) - static_cast<uint32_t>(low) < span;
+  }
+};
+
+// Rows that a loop walks through, `step` at a time, from one running address: what a
+// step costs beside the loads is a few scalar instructions.
+struct RowsWalk {
+  const char* at;
+  int32_t left;      // rows from `at` on that hold tokens
+  int32_t stride;    // bytes
+  __device__ __forceinline__ RowsWalk(const AttnTensor& t, int64_t row, int32_t head, int32_t rows)
+      : at(head_rows(t, row, head)), left(rows), stride(static_cast<int32_t>(2 * t.row)) {}
+  template <int kDim, int kStep>
+  __device__ __forceinline__ void load(char* tile, int32_t dim) {
+    load_tile<kDim, kStep>(tile, RowsRead(at, stride, min(left, kStep), dim), dim);
+    at += static_cast<int64_t>(stride) * kStep;
+    left -= kStep;
+  }
+};
+
+// The steps of 32 keys, numbered by their first key, that positions [p, p + np) see
+// something of, and of which they see everything.
+struct KeySteps {
+  int32_t any, any_end, all, all_end;
+  __device__ __forceinline__ KeySteps(const AttnArgs& a, int32_t p, int32_t np, int32_t valid, int32_t real) {
+    const int32_t last = p + np - 1;
+    any = a.window ? p - a.window - 30 : 0;   // k + 31 > p - window
+    all = a.window ? last - a.window + 1 : 0;
+    any_end = all_end = 0;
+    if (valid <= 0) return;
+    any_end = a.causal ? p + valid : a.window ? window_end(a, p + valid, real) : real;
+    any_end = min(any_end, real);
+    all_end = min(a.causal ? p + 1 : a.window ? window_end(a, p + 1, real) : real, real) - 31;
   }
 };
 

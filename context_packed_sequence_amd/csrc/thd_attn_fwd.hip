@@ -26,58 +26,43 @@ struct ForwardWave {
   F32x16 o[kDim / 32];       // [dim][query]
   float top = -kAttnInf;     // reference of the row's exponents, in powers of two
   float sum = 0.0f;          // of this lane's keys
-  int32_t key_at[kDim / 16]; // this lane's places in a tile
-  int32_t value_at[kDim / 32][2];
+  int32_t key_at, value_at[2];  // this lane's places in a tile
 
   __device__ __forceinline__ ForwardWave() {
     const int32_t l = threadIdx.x & 63;
+    key_at = lds_word<kDim>(l & 31, l >> 5);
+    value_at[0] = transposed_at<kDim>(0, 0);
+    value_at[1] = transposed_at<kDim>(0, 1);
 #pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) key_at[i] = lds_word<kDim>(l & 31, 2 * i + (l >> 5));
-#pragma unroll
-    for (int t = 0; t < kDim / 32; ++t) {
-      value_at[t][0] = transposed_at<kDim>(t, 0);
-      value_at[t][1] = transposed_at<kDim>(t, 1);
-      o[t] = zero16();
-    }
+    for (int t = 0; t < kDim / 32; ++t) o[t] = zero16();
   }
 
-  // Keys key0 .. key0 + 63, whose tile is at `keys` in LDS and their values' after it;
-  // `partly`: the rows do not see all of them.  `keys` is a constant where the calls are
-  // inlined and goes into the reads' offset fields.
-  __device__ __forceinline__ void step(const AttnArgs& a, const char* lds, int32_t keys, int32_t key0, bool partly,
-                                       const Seen& seen) {
-    const int32_t values = keys + kAttnStep * 2 * kDim;
+  // Keys key0 .. key0 + 31, whose rows are at `keys` in LDS and their values' at `values`;
+  // `partly`: the rows do not see all of them.  The places are constants where the calls
+  // are inlined and go into the reads' offset fields.
+  __device__ __forceinline__ void step(const AttnArgs& a, const char* lds, int32_t keys, int32_t values, int32_t key0,
+                                       bool partly, const Seen& seen) {
     const int32_t h = (threadIdx.x & 63) >> 5;
-    F32x16 s[2];
+    // places differ in single bits from word to word: one address each, hidden from the
+    // compiler so that it does not keep all of them in registers
+    int32_t row = key_at, first = value_at[0], second = value_at[1];
+    asm volatile("" : "+v"(row), "+v"(first), "+v"(second));
+    F32x16 s = zero16();
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      s[b] = zero16();
-#pragma unroll
-      for (int i = 0; i < kDim / 16; ++i)
-        s[b] = T::mfma(lds_read(lds + key_at[i], keys + b * 32 * 2 * kDim), q[i], s[b]);
-    }
+    for (int i = 0; i < kDim / 16; ++i) s = T::mfma(lds_read(lds + (row ^ (32 * i)), keys), q[i], s);
     // scores in powers of two: z log2(e) = s factor
     float factor = a.scale * kAttnLog2e;
     if constexpr (kCap) {
-      const float in = a.scale / a.cap;
       factor = a.cap * kAttnLog2e;
-      attn_tanh(s[0], in);
-      attn_tanh(s[1], in);
+      attn_tanh(s, a.scale / a.cap);
     }
     if (partly) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int32_t key = key0 + 4 * h + 32 * b + (r & 3) + 8 * (r >> 2);
-          s[b][r] = seen(key) ? s[b][r] : -kAttnInf;
-        }
+      for (int r = 0; r < 16; ++r) s[r] = seen(key0 + 4 * h + (r & 3) + 8 * (r >> 2)) ? s[r] : -kAttnInf;
     }
-    float m = s[0][0];
+    float m = fmaxf(s[0], s[1]);
 #pragma unroll
-    for (int r = 1; r < 16; ++r) m = fmaxf(m, s[0][r]);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) m = fmaxf(m, s[1][r]);
+    for (int r = 2; r < 16; r += 2) m = fmaxf(fmaxf(m, s[r]), s[r + 1]);
     m = max_halves(m) * factor;
     if (__any(m > top + kGrowth)) {
       const float to = fmaxf(top, m);
@@ -90,30 +75,27 @@ struct ForwardWave {
         for (int r = 0; r < 16; ++r) o[t][r] *= shrink;
     }
     const float base = top == -kAttnInf ? 0.0f : top;
-    U32x4 p[4];
+    U32x4 p[2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int r = 0; r < 16; r += 2) {
+      const float x = attn_exp2(fmaf(s[r], factor, -base));
+      const float y = attn_exp2(fmaf(s[r + 1], factor, -base));
+      sum += x + y;
+      p[r >> 3][(r & 7) >> 1] = T::pack(x, y);
+    }
 #pragma unroll
-      for (int r = 0; r < 16; r += 2) {
-        const float x = attn_exp2(fmaf(s[b][r], factor, -base));
-        const float y = attn_exp2(fmaf(s[b][r + 1], factor, -base));
-        sum += x + y;
-        p[2 * b + (r >> 3)][(r & 7) >> 1] = T::pack(x, y);
-      }
+    for (int t = 0; t < kDim / 32; ++t) {
+      const char *x = lds + (first ^ (64 * t)), *y = lds + (second ^ (64 * t));
 #pragma unroll
-    for (int t = 0; t < kDim / 32; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const U32x2 x = lds_read_transposed(lds + value_at[t][0] + (values + j * 16 * 2 * kDim));
-        const U32x2 y = lds_read_transposed(lds + value_at[t][1] + (values + j * 16 * 2 * kDim));
-        o[t] = T::mfma(U32x4{x[0], x[1], y[0], y[1]}, p[j], o[t]);
-      }
+      for (int j = 0; j < 2; ++j) o[t] = T::mfma(transposed_pair(x, y, values + j * 16 * 2 * kDim), p[j], o[t]);
+    }
   }
 };
 
 template <typename T, int kDim, bool kCap>
-__global__ __launch_bounds__(256, 2) void attn_forward_kernel(AttnArgs a) {
-  constexpr int kTile = kAttnStep * 2 * kDim;  // bytes
+__global__ __launch_bounds__(256, 3) void attn_forward_kernel(AttnArgs a) {
+  constexpr int kStep = kDim == 64 ? 64 : 32;
+  constexpr int kTile = kStep * 2 * kDim;  // bytes
   __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile];  // keys, values, and both again
   const AttnPlace place(blockIdx.x, a.kv_heads, a.group / a.tile_heads);
   if (place.tile >= a.plan.max_query_tiles) return;
@@ -133,24 +115,28 @@ __global__ __launch_bounds__(256, 2) void attn_forward_kernel(AttnArgs a) {
 
     const Seen first(a, tile.pos, tile.real), last(a, tile.pos + tile.valid - 1, tile.real);
     const int32_t end = last.low + static_cast<int32_t>(last.span);
-    int32_t key = first.low & ~(kAttnStep - 1);
+    int32_t key = first.low & ~(kStep - 1);
     const Seen seen(a, pos + c, tile.real);
-    const auto load = [&](int32_t to, int32_t at) {
-      const int32_t n = min(kAttnStep, tile.real - at);
-      load_tile<kDim>(s_tiles + to, RowsRead(head_rows(a.k, static_cast<int64_t>(tile.doc) + at, place.kv_head),
-                                     static_cast<int32_t>(2 * a.k.row), n, a.dim), a.dim);
-      load_tile<kDim>(s_tiles + to + kTile, RowsRead(head_rows(a.v, static_cast<int64_t>(tile.doc) + at, place.kv_head),
-                                       static_cast<int32_t>(2 * a.v.row), n, a.dim), a.dim);
+    RowsWalk keys(a.k, static_cast<int64_t>(tile.doc) + key, place.kv_head, tile.real - key);
+    RowsWalk values(a.v, static_cast<int64_t>(tile.doc) + key, place.kv_head, tile.real - key);
+    const KeySteps steps(a, pos, 32, own.valid, tile.real);
+    const auto load = [&](int32_t to) {
+      keys.load<kDim, kStep>(s_tiles + to, a.dim);
+      values.load<kDim, kStep>(s_tiles + to + kTile, a.dim);
     };
-    const auto turn = [&](int32_t keys, int32_t next) {
+    const auto turn = [&](int32_t now, int32_t next) {
       lds_arrived();
       __syncthreads();  // the tile is there, and nobody reads the one before
-      if (key + kAttnStep < end) load(next, key + kAttnStep);
-      if (own.valid > 0 && sees_any(a, pos, own.valid, key, kAttnStep, tile.real))
-        w.step(a, s_tiles, keys, key, !sees_all(a, pos, 32, key, kAttnStep, tile.real), seen);
-      key += kAttnStep;
+      if (key + kStep < end) load(next);
+#pragma unroll
+      for (int b = 0; b < kStep / 32; ++b) {
+        const int32_t at = now + 32 * b * 2 * kDim, k0 = key + 32 * b;
+        if (k0 >= steps.any && k0 < steps.any_end)
+          w.step(a, s_tiles, at, at + kTile, k0, k0 < steps.all || k0 >= steps.all_end, seen);
+      }
+      key += kStep;
     };
-    load(0, key);
+    load(0);
     while (key < end) {
       turn(0, 2 * kTile);
       if (key >= end) break;
