@@ -144,27 +144,37 @@ __device__ __forceinline__ F32x16 lds_rows(const float* at) {
   return r;
 }
 
-// acc [dim][32] += (32 rows of LDS from `from` on)^T b.  `from` is a constant where the
-// calls are inlined and goes into the reads' offset fields: one array of all tiles, so
-// that a lane holds one address for each place in a tile and not one for each tile.
+// acc [dim][32] += (the 32 rows f was read from)^T b
 template <typename T, int kDim>
-__device__ __forceinline__ void add_transposed(F32x16 (&acc)[kDim / 32], const char* lds, int32_t from,
-                                               const int32_t (&at)[kDim / 32][2], const U32x4 (&b)[2]) {
+__device__ __forceinline__ void add_columns(F32x16 (&acc)[kDim / 32], const U32x4 (&f)[kDim / 32][2],
+                                            const U32x4 (&b)[2]) {
 #pragma unroll
-  for (int t = 0; t < kDim / 32; ++t)
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      acc[t] = T::mfma(transposed_pair(lds + at[t][0], lds + at[t][1], from + j * 16 * 2 * kDim), b[j], acc[t]);
-    }
+    for (int t = 0; t < kDim / 32; ++t) acc[t] = T::mfma(f[t][j], b[j], acc[t]);
 }
 
+// s += x bx^T and dp += y by^T for 32 rows of two tiles, a lane's place in them `row`.
+// Reads go out four words at a time before the first is waited for.
 template <typename T, int kDim>
-__device__ __forceinline__ F32x16 product(const char* lds, int32_t from, const int32_t (&at)[kDim / 16],
-                                          const U32x4 (&b)[kDim / 16]) {
-  F32x16 c = zero16();
+__device__ __forceinline__ void row_products(const char* x, const char* y, int32_t row, const U32x4 (&bx)[kDim / 16],
+                                             const U32x4 (&by)[kDim / 16], F32x16& s, F32x16& dp) {
+  asm volatile("" : "+v"(row));  // words' places differ in single bits: not kept in registers
 #pragma unroll
-  for (int i = 0; i < kDim / 16; ++i) c = T::mfma(lds_read(lds + at[i], from), b[i], c);
-  return c;
+  for (int i0 = 0; i0 < kDim / 16; i0 += 4) {
+    U32x4 fx[4], fy[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fx[i] = lds_read(x + (row ^ (32 * (i0 + i))), 0);
+      fy[i] = lds_read(y + (row ^ (32 * (i0 + i))), 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = T::mfma(fx[i], bx[i0 + i], s);
+      dp = T::mfma(fy[i], by[i0 + i], dp);
+    }
+  }
 }
 
 // Query gradients: 128 query rows of one head a workgroup, as in the forward
@@ -188,7 +198,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
   for (int t = 0; t < kDim / 32; ++t) dq[t] = zero16();
   if (tile.valid > 0) {
     U32x4 q[kDim / 16], g[kDim / 16];
-    int32_t row_at[kDim / 16], column_at[kDim / 32][2];
+    const int32_t row_at = lds_word<kDim>(c, h);
+    const uint32_t column_at[2] = {lds_address(s_tiles) + transposed_at<kDim>(0, 0),
+                                   lds_address(s_tiles) + transposed_at<kDim>(0, 1)};
     const RowsRead queries(head_rows(a.q, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.q.row),
                            own.valid, a.dim);
     const RowsRead grads(head_rows(a.dout, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.dout.row),
@@ -197,12 +209,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
     for (int i = 0; i < kDim / 16; ++i) {
       q[i] = queries.load(c, 2 * i + h, a.dim);
       g[i] = grads.load(c, 2 * i + h, a.dim);
-      row_at[i] = lds_word<kDim>(c, 2 * i + h);
-    }
-#pragma unroll
-    for (int t = 0; t < kDim / 32; ++t) {
-      column_at[t][0] = transposed_at<kDim>(t, 0);
-      column_at[t][1] = transposed_at<kDim>(t, 1);
     }
     float lse = kAttnInf, delta = 0.0f;  // of a row that sees nothing: p 0
     if (c < own.valid) {
@@ -222,16 +228,16 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
       keys.load<kDim, kAttnStep>(s_tiles + to, a.dim);
       values.load<kDim, kAttnStep>(s_tiles + to + kTile, a.dim);
     };
-    const auto turn = [&](int32_t now, int32_t next) {
+    const auto turn = [&](auto now, int32_t next) {
       lds_arrived();
       __syncthreads();
       if (key + kAttnStep < end) load(next);
 #pragma unroll
       for (int b = 0; b < kAttnStep / 32; ++b) {
-        const int32_t k0 = key + 32 * b, at = now + 32 * b * 2 * kDim;
+        const int32_t k0 = key + 32 * b, skip = 32 * b * 2 * kDim;
         if (k0 < steps.any || k0 >= steps.any_end) continue;
-        F32x16 s = product<T, kDim>(s_tiles, at, row_at, q);
-        F32x16 dp = product<T, kDim>(s_tiles, at + kTile, row_at, g);
+        F32x16 s = zero16(), dp = zero16();
+        row_products<T, kDim>(s_tiles + now + skip, s_tiles + now + kTile + skip, row_at, q, g, s, dp);
         U32x4 p16[2], dz16[2];
         const bool all = k0 >= steps.all && k0 < steps.all_end;
         const auto lane_lse = [&](int) { return lse; };
@@ -241,15 +247,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
         else
           score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta,
                                    [&](int r) { return seen(k0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
-        add_transposed<T, kDim>(dq, s_tiles, at, column_at, dz16);
+        U32x4 f[kDim / 32][2];
+        read_columns<kDim, now>(column_at[0] + skip, column_at[1] + skip, f);
+        add_columns<T, kDim>(dq, f, dz16);
       }
       key += kAttnStep;
     };
     load(0);
     while (key < end) {
-      turn(0, 2 * kTile);
+      turn(Place<0>{}, 2 * kTile);
       if (key >= end) break;
-      turn(2 * kTile, 0);
+      turn(Place<2 * kTile>{}, 0);
     }
     __syncthreads();
   }
@@ -327,7 +335,8 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
   if (tile.valid > 0) {
     U32x4 k[kDim / 16], v[kHold ? kDim / 16 : 1];
     const int32_t row_at = lds_word<kDim>(c, h);
-    const int32_t column_at[2] = {transposed_at<kDim>(0, 0), transposed_at<kDim>(0, 1)};
+    const uint32_t column_at[2] = {lds_address(s_tiles) + transposed_at<kDim>(0, 0),
+                                   lds_address(s_tiles) + transposed_at<kDim>(0, 1)};
     const RowsRead keys(head_rows(a.k, stream, place.kv_head), static_cast<int32_t>(2 * a.k.row), own_valid, a.dim);
 #pragma unroll
     for (int i = 0; i < kDim / 16; ++i) k[i] = keys.load(c, 2 * i + h, a.dim);
@@ -363,7 +372,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
         next_delta = -a.plan.delta[at];
       }
     };
-    const auto turn = [&](int32_t queries, int32_t mine, int32_t next) {
+    const auto turn = [&](auto queries, int32_t mine, int32_t next) {
       if (threadIdx.x < kStep) {
         s_lse[mine][threadIdx.x] = next_lse;
         s_delta[mine][threadIdx.x] = next_delta;
@@ -376,23 +385,33 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
       if (!walk.done()) load(next);
 #pragma unroll
       for (int b = 0; b < kStep / 32; ++b) {
-        const int32_t p0 = pos + 32 * b, at = queries + 32 * b * 2 * kDim;
+        const int32_t p0 = pos + 32 * b, skip = 32 * b * 2 * kDim;
         if (32 * b >= n || own_valid <= 0 || !sees_any(a, p0, min(32, n - 32 * b), key, own_valid, tile.real)) continue;
-        // A lane's places in a tile differ in single bits from word to word: one address
-        // each for rows, columns and values, hidden from the compiler so that it does not
-        // keep all of them in registers.
-        int32_t row = row_at, first = column_at[0], second = column_at[1], value = row_at + 32 * wave * 2 * kDim;
-        asm volatile("" : "+v"(row), "+v"(first), "+v"(second), "+v"(value));
         // the sums start at what is taken from them: -lse (as a score; with a cap, after it)
         // and -delta
         F32x16 s = kCap ? zero16() : lds_rows(&s_lse[mine][32 * b + 4 * h]);
         F32x16 dp = lds_rows(&s_delta[mine][32 * b + 4 * h]);
+        const char* rows = s_tiles + queries + skip;
+        if constexpr (kHold) {
+          row_products<T, kDim>(rows, rows + kTile, row_at, k, v, s, dp);
+        } else {
+          int32_t row = row_at, value = row_at + 32 * wave * 2 * kDim;
+          asm volatile("" : "+v"(row), "+v"(value));
 #pragma unroll
-        for (int i = 0; i < kDim / 16; ++i) {
-          const char* x = s_tiles + (row ^ (32 * i));
-          s = T::mfma(lds_read(x, at), k[i], s);
-          dp = T::mfma(lds_read(x, at + kTile),
-                       kHold ? v[kHold ? i : 0] : lds_read(s_tiles + (value ^ (32 * i)), 4 * kTile), dp);
+          for (int i0 = 0; i0 < kDim / 16; i0 += 2) {
+            U32x4 fx[2], fy[2], fv[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              fx[i] = lds_read(rows + (row ^ (32 * (i0 + i))), 0);
+              fy[i] = lds_read(rows + (row ^ (32 * (i0 + i))), kTile);
+              fv[i] = lds_read(s_tiles + (value ^ (32 * (i0 + i))), 4 * kTile);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              s = T::mfma(fx[i], k[i0 + i], s);
+              dp = T::mfma(fy[i], fv[i], dp);
+            }
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
         U32x4 p16[2], dz16[2];
@@ -406,23 +425,18 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
           score_gradients<T, kCap>(a, s, dp, held, row_lse, no_delta,
                                    [&](int r) { return seen(p0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < kDim / 32; ++t) {
-          const char *x = s_tiles + (first ^ (64 * t)), *y = s_tiles + (second ^ (64 * t));
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int32_t from = at + j * 16 * 2 * kDim;
-            dv[t] = T::mfma(transposed_pair(x, y, from + kTile), p16[j], dv[t]);
-            dk[t] = T::mfma(transposed_pair(x, y, from), dz16[j], dk[t]);
-          }
-        }
+        U32x4 f[kDim / 32][2];
+        read_columns<kDim, queries + kTile>(column_at[0] + skip, column_at[1] + skip, f);
+        add_columns<T, kDim>(dv, f, p16);
+        read_columns<kDim, queries>(column_at[0] + skip, column_at[1] + skip, f);
+        add_columns<T, kDim>(dk, f, dz16);
       }
     };
     if (!walk.done()) load(0);
     while (!walk.done()) {
-      turn(0, 0, 2 * kTile);
+      turn(Place<0>{}, 0, 2 * kTile);
       if (walk.done()) break;
-      turn(2 * kTile, 1, 0);
+      turn(Place<2 * kTile>{}, 1, 0);
     }
     __syncthreads();
   }

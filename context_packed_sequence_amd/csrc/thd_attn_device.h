@@ -20,6 +20,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "thd_attn_internal.h"
 #include "thd_device.h"
 
@@ -137,9 +139,9 @@ __device__ __forceinline__ U32x4 lds_read(const char* tile, int32_t at) {
   return *reinterpret_cast<const U32x4*>(tile + at);
 }
 
-// A of a transposed tile: rows [row, row + 16) of the tile are the summed index
-// (in the order above), columns 32 t .. 32 t + 31 the 32 rows of A.  `at` is this
-// lane's transposed_at<kDim>(t, second).
+// Where a lane points to for a transposing read of rows 0..7 (second 0) or 8..15
+// (second 1) of a tile, which are the summed index (in the order above), and columns
+// 32 t .. 32 t + 31, the 32 rows of A.
 template <int kDim>
 __device__ __forceinline__ int32_t transposed_at(int32_t t, int32_t second) {
   const int32_t l = threadIdx.x & 63, i = l & 15;
@@ -147,17 +149,67 @@ __device__ __forceinline__ int32_t transposed_at(int32_t t, int32_t second) {
   const int32_t col = 32 * t + 16 * ((l >> 4) & 1) + 4 * (i & 3);
   return lds_word<kDim>(row, col >> 3) + 2 * (col & 7);
 }
-__device__ __forceinline__ U32x2 lds_read_transposed(const char* at) {
-  typedef __attribute__((address_space(3))) I16x4 LdsI16x4;
-  const I16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      reinterpret_cast<LdsI16x4*>(reinterpret_cast<uintptr_t>(at)));
-  return __builtin_bit_cast(U32x2, r);
+// A's fragments for 32 rows of a tile from kFrom on, all columns: [t][j] is columns
+// 32 t .. 32 t + 31 of rows 16 j .. 16 j + 15.  `first` and `second` are the lane's LDS
+// addresses transposed_at(0, 0) and (0, 1); other columns differ in single bits.  One
+// block of reads with its wait: the compiler would wait for every load from memory to
+// LDS before a transposing read, also for those of the tiles to come.
+template <int kDim, int kFrom>
+__device__ __forceinline__ void read_columns(uint32_t first, uint32_t second, U32x4 (&f)[kDim / 32][2]) {
+  U32x2 x[kDim / 32][2], y[kDim / 32][2];
+  if constexpr (kDim == 128) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %16 offset:%24\n"
+        "ds_read_b64_tr_b16 %1, %20 offset:%24\n"
+        "ds_read_b64_tr_b16 %2, %16 offset:%25\n"
+        "ds_read_b64_tr_b16 %3, %20 offset:%25\n"
+        "ds_read_b64_tr_b16 %4, %17 offset:%24\n"
+        "ds_read_b64_tr_b16 %5, %21 offset:%24\n"
+        "ds_read_b64_tr_b16 %6, %17 offset:%25\n"
+        "ds_read_b64_tr_b16 %7, %21 offset:%25\n"
+        "ds_read_b64_tr_b16 %8, %18 offset:%24\n"
+        "ds_read_b64_tr_b16 %9, %22 offset:%24\n"
+        "ds_read_b64_tr_b16 %10, %18 offset:%25\n"
+        "ds_read_b64_tr_b16 %11, %22 offset:%25\n"
+        "ds_read_b64_tr_b16 %12, %19 offset:%24\n"
+        "ds_read_b64_tr_b16 %13, %23 offset:%24\n"
+        "ds_read_b64_tr_b16 %14, %19 offset:%25\n"
+        "ds_read_b64_tr_b16 %15, %23 offset:%25\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(x[0][0]), "=&v"(y[0][0]), "=&v"(x[0][1]), "=&v"(y[0][1]), "=&v"(x[1][0]), "=&v"(y[1][0]),
+          "=&v"(x[1][1]), "=&v"(y[1][1]), "=&v"(x[2][0]), "=&v"(y[2][0]), "=&v"(x[2][1]), "=&v"(y[2][1]),
+          "=&v"(x[3][0]), "=&v"(y[3][0]), "=&v"(x[3][1]), "=&v"(y[3][1])
+        : "v"(first), "v"(first ^ 64), "v"(first ^ 128), "v"(first ^ 192), "v"(second), "v"(second ^ 64),
+          "v"(second ^ 128), "v"(second ^ 192), "i"(kFrom), "i"(kFrom + 16 * 2 * kDim)
+        : "memory");
+  } else {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%12\n"
+        "ds_read_b64_tr_b16 %1, %10 offset:%12\n"
+        "ds_read_b64_tr_b16 %2, %8 offset:%13\n"
+        "ds_read_b64_tr_b16 %3, %10 offset:%13\n"
+        "ds_read_b64_tr_b16 %4, %9 offset:%12\n"
+        "ds_read_b64_tr_b16 %5, %11 offset:%12\n"
+        "ds_read_b64_tr_b16 %6, %9 offset:%13\n"
+        "ds_read_b64_tr_b16 %7, %11 offset:%13\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(x[0][0]), "=&v"(y[0][0]), "=&v"(x[0][1]), "=&v"(y[0][1]), "=&v"(x[1][0]), "=&v"(y[1][0]),
+          "=&v"(x[1][1]), "=&v"(y[1][1])
+        : "v"(first), "v"(first ^ 64), "v"(second), "v"(second ^ 64), "i"(kFrom), "i"(kFrom + 16 * 2 * kDim)
+        : "memory");
+  }
+#pragma unroll
+  for (int t = 0; t < kDim / 32; ++t)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f[t][j] = U32x4{x[t][j][0], x[t][j][1], y[t][j][0], y[t][j][1]};
 }
 
-// A's half for 16 rows, from the addresses of its first and second 8.
-__device__ __forceinline__ U32x4 transposed_pair(const char* first, const char* second, int32_t from) {
-  const U32x2 x = lds_read_transposed(first + from), y = lds_read_transposed(second + from);
-  return U32x4{x[0], x[1], y[0], y[1]};
+// A place in LDS known when the code is compiled: it goes into reads' offset fields.
+template <int kAt>
+using Place = std::integral_constant<int, kAt>;
+
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
 }
 
 // Rows [0, valid) of one head, from `base` on, behind a buffer resource of

@@ -26,30 +26,38 @@ struct ForwardWave {
   F32x16 o[kDim / 32];       // [dim][query]
   float top = -kAttnInf;     // reference of the row's exponents, in powers of two
   float sum = 0.0f;          // of this lane's keys
-  int32_t key_at, value_at[2];  // this lane's places in a tile
+  int32_t key_at;            // this lane's place in a tile
+  uint32_t value_at[2];
 
-  __device__ __forceinline__ ForwardWave() {
+  __device__ __forceinline__ explicit ForwardWave(const char* lds) {
     const int32_t l = threadIdx.x & 63;
     key_at = lds_word<kDim>(l & 31, l >> 5);
-    value_at[0] = transposed_at<kDim>(0, 0);
-    value_at[1] = transposed_at<kDim>(0, 1);
+    value_at[0] = lds_address(lds) + transposed_at<kDim>(0, 0);
+    value_at[1] = lds_address(lds) + transposed_at<kDim>(0, 1);
 #pragma unroll
     for (int t = 0; t < kDim / 32; ++t) o[t] = zero16();
   }
 
-  // Keys key0 .. key0 + 31, whose rows are at `keys` in LDS and their values' at `values`;
-  // `partly`: the rows do not see all of them.  The places are constants where the calls
-  // are inlined and go into the reads' offset fields.
-  __device__ __forceinline__ void step(const AttnArgs& a, const char* lds, int32_t keys, int32_t values, int32_t key0,
-                                       bool partly, const Seen& seen) {
+  // Keys key0 .. key0 + 31, whose rows are at kKeys + skip in LDS and their values' at
+  // kValues + skip; `partly`: the rows do not see all of them.
+  template <int kKeys, int kValues>
+  __device__ __forceinline__ void step(const AttnArgs& a, const char* lds, int32_t skip, int32_t key0, bool partly,
+                                       const Seen& seen) {
     const int32_t h = (threadIdx.x & 63) >> 5;
-    // places differ in single bits from word to word: one address each, hidden from the
+    // places differ in single bits from word to word: one address, hidden from the
     // compiler so that it does not keep all of them in registers
-    int32_t row = key_at, first = value_at[0], second = value_at[1];
-    asm volatile("" : "+v"(row), "+v"(first), "+v"(second));
+    int32_t row = key_at;
+    asm volatile("" : "+v"(row));
     F32x16 s = zero16();
 #pragma unroll
-    for (int i = 0; i < kDim / 16; ++i) s = T::mfma(lds_read(lds + (row ^ (32 * i)), keys), q[i], s);
+    for (int i0 = 0; i0 < kDim / 16; i0 += 4) {
+      U32x4 k[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = lds_read(lds + skip + (row ^ (32 * (i0 + i))), kKeys);
+      __builtin_amdgcn_sched_barrier(0);  // all four on their way before the first is waited for
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = T::mfma(k[i], q[i0 + i], s);
+    }
     // scores in powers of two: z log2(e) = s factor
     float factor = a.scale * kAttnLog2e;
     if constexpr (kCap) {
@@ -83,12 +91,12 @@ struct ForwardWave {
       sum += x + y;
       p[r >> 3][(r & 7) >> 1] = T::pack(x, y);
     }
+    U32x4 v[kDim / 32][2];
+    read_columns<kDim, kValues>(value_at[0] + skip, value_at[1] + skip, v);
 #pragma unroll
-    for (int t = 0; t < kDim / 32; ++t) {
-      const char *x = lds + (first ^ (64 * t)), *y = lds + (second ^ (64 * t));
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) o[t] = T::mfma(transposed_pair(x, y, values + j * 16 * 2 * kDim), p[j], o[t]);
-    }
+      for (int t = 0; t < kDim / 32; ++t) o[t] = T::mfma(v[t][j], p[j], o[t]);
   }
 };
 
@@ -106,7 +114,7 @@ __global__ __launch_bounds__(256, 3) void attn_forward_kernel(AttnArgs a) {
   const WaveRows own(a, tile, place, wave);
   const int32_t pos = tile.pos + own.first;
 
-  ForwardWave<T, kDim, kCap> w;
+  ForwardWave<T, kDim, kCap> w(s_tiles);
   if (tile.valid > 0) {
     const RowsRead queries(head_rows(a.q, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.q.row),
                            own.valid, a.dim);
@@ -124,23 +132,24 @@ __global__ __launch_bounds__(256, 3) void attn_forward_kernel(AttnArgs a) {
       keys.load<kDim, kStep>(s_tiles + to, a.dim);
       values.load<kDim, kStep>(s_tiles + to + kTile, a.dim);
     };
-    const auto turn = [&](int32_t now, int32_t next) {
+    const auto turn = [&](auto now, int32_t next) {
       lds_arrived();
       __syncthreads();  // the tile is there, and nobody reads the one before
       if (key + kStep < end) load(next);
 #pragma unroll
       for (int b = 0; b < kStep / 32; ++b) {
-        const int32_t at = now + 32 * b * 2 * kDim, k0 = key + 32 * b;
+        const int32_t k0 = key + 32 * b;
         if (k0 >= steps.any && k0 < steps.any_end)
-          w.step(a, s_tiles, at, at + kTile, k0, k0 < steps.all || k0 >= steps.all_end, seen);
+          w.template step<now, now + kTile>(a, s_tiles, 32 * b * 2 * kDim, k0, k0 < steps.all || k0 >= steps.all_end,
+                                            seen);
       }
       key += kStep;
     };
     load(0);
     while (key < end) {
-      turn(0, 2 * kTile);
+      turn(Place<0>{}, 2 * kTile);
       if (key >= end) break;
-      turn(2 * kTile, 0);
+      turn(Place<2 * kTile>{}, 0);
     }
     __syncthreads();
   }
