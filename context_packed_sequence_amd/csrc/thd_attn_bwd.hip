@@ -265,43 +265,96 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
                       2 * a.dq.row, own.rows, own.valid, a.dim);
 }
 
-// The query rows that a key tile's gradients come from: for each head of the
-// group, of each of the document's chunks the rows that see the tile, 64 at a
-// time.
+// The query rows that a key tile's gradients come from: for each of the workgroup's
+// heads, of each of the document's chunks the rows that see the tile, kStep at a time,
+// from running addresses.
+template <int kStep>
 struct QueryWalk {
-  int32_t head, chunk, row, end;    // row, end: within the chunk
-  int32_t first_head, heads, chunks;
-  __device__ __forceinline__ void range(const AttnArgs& a, const KeyTile& k) {
-    const int32_t pos = position(a, k);
-    const int32_t valid = max(0, min(k.chunk, k.real - pos));
-    const int32_t low = a.causal ? k.key : a.window ? max(0, k.key - a.window + 1) : 0;
-    const int32_t high = a.window ? window_end(a, k.key + k.valid, k.real) : k.real;
-    row = max(0, low - pos);
-    end = max(0, min(valid, high - pos));
+  int32_t head, heads_end, chunk;
+  int32_t left = 0;                 // rows of the chunk that are still to come
+  int32_t pos = 0;                  // position of the next one
+  const char *q = nullptr, *grad = nullptr;
+  int64_t number = 0;               // of its lse and delta
+  __device__ __forceinline__ QueryWalk(const AttnArgs& a, const KeyTile& k, int32_t first_head, int32_t heads)
+      : head(first_head), heads_end(first_head + heads), chunk(-1) {
+    settle(a, k);
   }
-  __device__ __forceinline__ int32_t position(const AttnArgs& a, const KeyTile& k) const {
-    return a.cp == 1 ? 0 : chunk ? (2 * a.cp - 1 - a.rank) * k.chunk : a.rank * k.chunk;
-  }
-  __device__ __forceinline__ bool done() const { return head >= first_head + heads; }
+  __device__ __forceinline__ bool done() const { return head >= heads_end; }
+  // To the first row of the next chunk that has any.
   __device__ __forceinline__ void settle(const AttnArgs& a, const KeyTile& k) {
-    while (!done() && row >= end) {
-      if (++chunk == chunks) {
+    while (left <= 0) {
+      if (++chunk == (a.cp == 1 ? 1 : 2)) {
         chunk = 0;
-        if (++head >= first_head + heads) return;
+        ++head;
       }
-      range(a, k);
+      if (done()) return;
+      const int32_t start = a.cp == 1 ? 0 : chunk ? (2 * a.cp - 1 - a.rank) * k.chunk : a.rank * k.chunk;
+      const int32_t valid = min(k.chunk, k.real - start);
+      const int32_t low = a.causal ? k.key : a.window ? max(0, k.key - a.window + 1) : 0;
+      const int32_t high = a.window ? window_end(a, k.key + k.valid, k.real) : k.real;
+      const int32_t first = max(0, low - start);
+      left = min(valid, high - start) - first;
+      if (left <= 0) continue;
+      pos = start + first;
+      const int64_t row = static_cast<int64_t>(k.first) + chunk * k.chunk + first;
+      q = head_rows(a.q, row, head);
+      grad = head_rows(a.dout, row, head);
+      number = static_cast<int64_t>(head) * a.rows + row;
     }
   }
-  __device__ __forceinline__ QueryWalk(const AttnArgs& a, const KeyTile& k, int32_t kv_head)
-      : head(kv_head * a.group), chunk(0), first_head(kv_head * a.group), heads(a.group), chunks(a.cp == 1 ? 1 : 2) {
-    range(a, k);
-    settle(a, k);
-  }
-  __device__ __forceinline__ void next(const AttnArgs& a, const KeyTile& k, int32_t step) {
-    row += step;
-    settle(a, k);
+  __device__ __forceinline__ void next(const AttnArgs& a, const KeyTile& k) {
+    left -= kStep;
+    pos += kStep;
+    q += 2 * a.q.row * kStep;
+    grad += 2 * a.dout.row * kStep;
+    number += kStep;
+    if (left <= 0) settle(a, k);
   }
 };
+
+// The steps of 32 rows, numbered by their first position, that see something of keys
+// [k, k + valid), and that see everything of [k, k + 32).
+struct RowSteps {
+  int32_t any, any_end, all, all_end;
+  __device__ __forceinline__ RowSteps(const AttnArgs& a, int32_t k, int32_t valid) {
+    any = a.causal ? k - 31 : a.window ? k - a.window - 30 : INT32_MIN;
+    any_end = valid <= 0 ? INT32_MIN : a.window ? window_end(a, k + valid, INT32_MAX) : INT32_MAX;
+    all = a.causal ? k + 31 : a.window ? k + 32 - a.window : INT32_MIN;
+    all_end = a.window ? window_end(a, k + 1, INT32_MAX) - 31 : INT32_MAX;
+  }
+};
+
+// Number threadIdx.x of n, 0 past them.
+__device__ __forceinline__ float load_number(const float* from, int32_t n) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(from), 0, 4 * n, kBufferWord3);
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, 4 * threadIdx.x, 0, 0));
+}
+
+// A key row's sums of one part of a group's heads: [part][dk, dv][tokens][kv heads][dim].
+__device__ __forceinline__ float* partial_sums(const AttnArgs& a, int32_t part, int32_t which, int64_t row,
+                                               int32_t head) {
+  return a.plan.partial + (((2 * static_cast<int64_t>(part) + which) * a.total + row) * a.kv_heads + head) * a.dim;
+}
+
+// A wave's accumulators [kDim][32 rows] in 32 bits; rows from `valid` on are zero.
+template <int kDim>
+__device__ __forceinline__ void store_sums(const AttnArgs& a, int32_t part, int32_t which,
+                                           const F32x16 (&acc)[kDim / 32], float factor, int64_t row, int32_t head,
+                                           int32_t rows, int32_t valid) {
+  const int32_t c = threadIdx.x & 31, h = (threadIdx.x & 63) >> 5;
+  if (c >= rows) return;
+  float* to = partial_sums(a, part, which, row + c, head);
+#pragma unroll
+  for (int t = 0; t < kDim / 32; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int32_t d = 32 * t + 8 * g + 4 * h;
+      float4 x = {acc[t][4 * g] * factor, acc[t][4 * g + 1] * factor, acc[t][4 * g + 2] * factor,
+                  acc[t][4 * g + 3] * factor};
+      if (c >= valid) x = float4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (d < a.dim) *reinterpret_cast<float4*>(to + d) = x;
+    }
+}
 
 // Key and value gradients: 128 keys of one key head a workgroup, 32 a wave.
 //
@@ -309,6 +362,9 @@ struct QueryWalk {
 // that leaves no room for its values' rows beside two waves on each SIMD, of which one
 // computes probabilities while the other multiplies; they are read from LDS instead,
 // and query rows come 32 at a time, so that two workgroups share a compute unit's LDS.
+//
+// Where there are few key tiles, the heads of a group are dealt out over `parts`
+// workgroups, each of which leaves its sums in 32 bits for attn_join_kernel.
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
   constexpr bool kHold = kDim == 64;           // values in registers
@@ -317,7 +373,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
   // query rows, rows of dout, both again, values
   __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile + (kHold ? 0 : kAttnKeys * 2 * kDim)];
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
-  const AttnPlace place(blockIdx.x, a.kv_heads, 1);
+  const AttnPlace place(blockIdx.x, a.kv_heads, a.key_parts);
   if (place.tile >= a.plan.max_key_tiles) return;
   const KeyTile tile = a.plan.key_tiles[place.tile];
   if (tile.keys == 0) return;
@@ -349,44 +405,40 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
                             static_cast<int32_t>(2 * a.v.row), tile.valid, a.dim);
       load_tile<kDim, kAttnKeys>(s_tiles + 4 * kTile, values, a.dim);
     }
-    QueryWalk walk(a, tile, place.kv_head);
+    const int32_t part_heads = a.group / a.key_parts;
+    QueryWalk<kStep> walk(a, tile, place.kv_head * a.group + place.part * part_heads, part_heads);
+    const RowSteps steps(a, key, own_valid);
     // positions that see key key + c
     const Seen seen(a.causal ? key + c : a.window ? key + c - a.window + 1 : 0,
                     a.window ? (a.causal ? a.window : 2u * a.window - 1u) : 0x7fffffffu);
-    float next_lse = -kAttnInf, next_delta = 0.0f;
+    float next_lse = 0.0f, next_delta = 0.0f;
     // what scores start from, or (with a cap) is taken from their power of two
     const float lse_factor = kCap ? kAttnLog2e : -1.0f / a.scale;
     const auto load = [&](int32_t to) {
-      const int32_t n = min(kStep, walk.end - walk.row);
-      const int64_t row = static_cast<int64_t>(tile.first) + walk.chunk * tile.chunk + walk.row;
-      load_tile<kDim, kStep>(s_tiles + to, RowsRead(head_rows(a.q, row, walk.head), static_cast<int32_t>(2 * a.q.row), n,
-                                               a.dim), a.dim);
-      load_tile<kDim, kStep>(s_tiles + to + kTile, RowsRead(head_rows(a.dout, row, walk.head), static_cast<int32_t>(2 * a.dout.row),
-                                             n, a.dim), a.dim);
-      next_lse = kCap ? kAttnInf : -kAttnInf;  // rows past the range: p 0
-      next_delta = 0.0f;
-      if (static_cast<int32_t>(threadIdx.x) < n) {
-        const int64_t at = static_cast<int64_t>(walk.head) * a.rows + row + threadIdx.x;
-        const float x = a.lse[at];
-        if (x != -kAttnInf) next_lse = x * lse_factor;
-        next_delta = -a.plan.delta[at];
-      }
+      const int32_t n = min(kStep, walk.left);
+      // ahead of the tiles, which arrive after them; rows past the range are zero in all
+      // four, and add nothing
+      next_lse = load_number(a.lse + walk.number, n);
+      next_delta = load_number(a.plan.delta + walk.number, n);
+      load_tile<kDim, kStep>(s_tiles + to, RowsRead(walk.q, static_cast<int32_t>(2 * a.q.row), n, a.dim), a.dim);
+      load_tile<kDim, kStep>(s_tiles + to + kTile, RowsRead(walk.grad, static_cast<int32_t>(2 * a.dout.row), n, a.dim),
+                             a.dim);
     };
     const auto turn = [&](auto queries, int32_t mine, int32_t next) {
       if (threadIdx.x < kStep) {
-        s_lse[mine][threadIdx.x] = next_lse;
-        s_delta[mine][threadIdx.x] = next_delta;
+        // a row that sees nothing: p 0
+        s_lse[mine][threadIdx.x] = next_lse == -kAttnInf ? (kCap ? kAttnInf : -kAttnInf) : next_lse * lse_factor;
+        s_delta[mine][threadIdx.x] = -next_delta;
       }
       lds_arrived();
       __syncthreads();
-      const int32_t n = min(kStep, walk.end - walk.row);
-      const int32_t pos = walk.position(a, tile) + walk.row;
-      walk.next(a, tile, kStep);
+      const int32_t n = walk.left, pos = walk.pos;
+      walk.next(a, tile);
       if (!walk.done()) load(next);
 #pragma unroll
       for (int b = 0; b < kStep / 32; ++b) {
         const int32_t p0 = pos + 32 * b, skip = 32 * b * 2 * kDim;
-        if (32 * b >= n || own_valid <= 0 || !sees_any(a, p0, min(32, n - 32 * b), key, own_valid, tile.real)) continue;
+        if (32 * b >= n || p0 < steps.any || p0 >= steps.any_end) continue;
         // the sums start at what is taken from them: -lse (as a score; with a cap, after it)
         // and -delta
         F32x16 s = kCap ? zero16() : lds_rows(&s_lse[mine][32 * b + 4 * h]);
@@ -419,7 +471,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
         const auto row_lse = [&](int r) { return kCap ? lse[(r & 3) + 8 * (r >> 2)] : 0.0f; };
         const auto no_delta = [](int) { return 0.0f; };
         // pads among the keys are other lanes' and are not stored
-        if (sees_all(a, p0, 32, key, 32, INT32_MAX))
+        if (p0 >= steps.all && p0 < steps.all_end)
           score_gradients<T, kCap>(a, s, dp, held, row_lse, no_delta, [](int) { return true; }, p16, dz16);
         else
           score_gradients<T, kCap>(a, s, dp, held, row_lse, no_delta,
@@ -440,6 +492,12 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
     }
     __syncthreads();
   }
+  const float dv_factor = T::kNarrow ? 1.0f / kProbabilityScale : 1.0f;
+  if (a.key_parts > 1) {
+    store_sums<kDim>(a, place.part, 0, dk, a.scale / held, stream, place.kv_head, own_keys, own_valid);
+    store_sums<kDim>(a, place.part, 1, dv, dv_factor, stream, place.kv_head, own_keys, own_valid);
+    return;
+  }
   // 32 rows of the results for each wave
   char* own = s_tiles + wave * kTile;
   store_rows<T, kDim>(own, dk, a.scale / held, const_cast<char*>(head_rows(a.dk, stream, place.kv_head)),
@@ -447,9 +505,30 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  store_rows<T, kDim>(own, dv, T::kNarrow ? 1.0f / kProbabilityScale : 1.0f,
-                      const_cast<char*>(head_rows(a.dv, stream, place.kv_head)), 2 * a.dv.row, own_keys, own_valid,
-                      a.dim);
+  store_rows<T, kDim>(own, dv, dv_factor, const_cast<char*>(head_rows(a.dv, stream, place.kv_head)), 2 * a.dv.row,
+                      own_keys, own_valid, a.dim);
+}
+
+// Sums of the parts, in order, rounded once: 16 threads a row of a head, eight elements
+// a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  if (a.plan.header[kAttnCode] != THD_OK) return;
+  const int32_t word = threadIdx.x & 15, head = blockIdx.y;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (row >= a.total || 8 * word >= a.dim) return;
+  for (int which = 0; which < 2; ++which) {
+    float sum[8] = {};
+    for (int32_t part = 0; part < a.key_parts; ++part) {
+      const float4* from = reinterpret_cast<const float4*>(partial_sums(a, part, which, row, head) + 8 * word);
+      const float4 x = from[0], y = from[1];
+      sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+      sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+    }
+    const AttnTensor& t = which ? a.dv : a.dk;
+    *reinterpret_cast<U32x4*>(const_cast<char*>(head_rows(t, row, head)) + 16 * word) =
+        U32x4{T::pack(sum[0], sum[1]), T::pack(sum[2], sum[3]), T::pack(sum[4], sum[5]), T::pack(sum[6], sum[7])};
+  }
 }
 
 template <typename T>
@@ -472,9 +551,13 @@ hipError_t dq(const AttnArgs& a, hipStream_t stream) {
 template <typename T, int kDim>
 hipError_t dkv(const AttnArgs& a, hipStream_t stream) {
   const int32_t units = a.plan.max_key_tiles * a.kv_heads;
-  const dim3 grid((units + 7) / 8 * 8);
+  const dim3 grid((units + 7) / 8 * 8 * a.key_parts);
   if (a.cap > 0.0f) attn_dkv_kernel<T, kDim, true><<<grid, 256, 0, stream>>>(a);
   else attn_dkv_kernel<T, kDim, false><<<grid, 256, 0, stream>>>(a);
+  if (a.key_parts > 1) {
+    const dim3 rows(static_cast<uint32_t>((static_cast<int64_t>(a.total) + 15) / 16), a.kv_heads);
+    attn_join_kernel<T><<<rows, 256, 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -313,21 +313,6 @@ struct KeySteps {
   }
 };
 
-// Whether positions [p, p + np) see all, or any, of keys [k, k + nk).
-__device__ __forceinline__ bool sees_all(const AttnArgs& a, int32_t p, int32_t np, int32_t k, int32_t nk,
-                                         int32_t real) {
-  if (k + nk > real) return false;
-  if (a.causal && k + nk - 1 > p) return false;
-  if (a.window && p + np - 1 - k >= a.window) return false;
-  return !(a.window && !a.causal && k + nk - 1 - p >= a.window);
-}
-__device__ __forceinline__ bool sees_any(const AttnArgs& a, int32_t p, int32_t np, int32_t k, int32_t nk,
-                                         int32_t real) {
-  if (k >= real || (a.causal && k > p + np - 1)) return false;
-  if (a.window && p - (k + nk - 1) >= a.window) return false;
-  return !(a.window && !a.causal && k - (p + np - 1) >= a.window);
-}
-
 // Tile and heads of workgroup b, which runs on XCD b mod 8: the workgroups of a group
 // read the same keys, and stay on one XCD one after the other; tiles of a key head are
 // dealt out so that, with 8 key heads, each XCD keeps to one of them.  `parts`:

@@ -46,7 +46,7 @@ struct KeyTile {
 };
 
 // Workspace, written by the plan kernel.
-enum AttnHeader : int { kAttnMaxGrad = 0, kAttnMaxValue = 1, kAttnHeaderWords = 16 };
+enum AttnHeader : int { kAttnMaxGrad = 0, kAttnMaxValue = 1, kAttnCode = 2, kAttnHeaderWords = 16 };
 
 struct AttnPlan {
   int32_t* header;         // [kAttnHeaderWords]
@@ -55,6 +55,7 @@ struct AttnPlan {
   QueryTile* query_tiles;  // [max_query_tiles], heaviest first, those without rows last
   KeyTile* key_tiles;      // [max_key_tiles]
   float* delta;            // [heads][rows], backward only
+  float* partial;          // [key parts][2][tokens][kv heads][dim], with more than one part
   int32_t max_query_tiles;
   int32_t max_key_tiles;
 };
@@ -74,6 +75,7 @@ struct AttnArgs {
   int32_t n_slots, total, rows;
   int32_t heads, kv_heads, group, dim, dtype;
   int32_t tile_heads;      // heads of a group in a workgroup
+  int32_t key_parts;       // workgroups that a group's heads are dealt out over for the key gradients
   int32_t causal, window;  // window 0: none
   int32_t cp, rank;
   float scale, cap;        // cap 0: none

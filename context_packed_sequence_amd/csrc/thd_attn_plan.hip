@@ -174,6 +174,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnArgs a) {
   const int32_t code = severity_to_code(s_severity);
   if (threadIdx.x == 0) {
     if (a.status) *a.status = code;
+    p.header[kAttnCode] = code;
     p.header[kAttnMaxGrad] = 0;
     p.header[kAttnMaxValue] = 0;
   }

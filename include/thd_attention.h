@@ -74,7 +74,7 @@ typedef struct thd_attention_shape {
   int32_t cp_size, rank;
   int32_t n_slots;
   int64_t total_tokens;
-  double scale;        /* > 0, finite in 32 bits */
+  double scale;        /* > 0, finite in 32 bits, as its reciprocal */
   double cap;          /* 0: none; else > 0, finite in 32 bits */
   const int32_t* cu_seqlens_padded;
   const int32_t* cu_seqlens;
