@@ -115,16 +115,18 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
 template <typename T, bool kCap, typename Lse, typename Delta, typename Visible>
 __device__ __forceinline__ void score_gradients(const AttnArgs& a, F32x16 s, F32x16 dp, float held, Lse lse,
                                                 Delta delta, Visible visible, U32x4 (&p16)[2], U32x4 (&dz16)[2]) {
-  const float factor = (kCap ? a.cap : a.scale) * kAttnLog2e;
-  if constexpr (kCap) attn_tanh(s, a.scale / a.cap);
+  const float factor = kCap ? 1.0f : a.scale * kAttnLog2e;
+  // the slope of the cap, held - (root s)^2
+  const float root = kCap ? __builtin_sqrtf(held) / (a.cap * kAttnLog2e) : 0.0f;
+  if constexpr (kCap) attn_capped(a, s);
 #pragma unroll
   for (int r = 0; r < 16; r += 2) {
     if (kCap && r % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // few registers at a time
     float p[2], dz[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float z = s[r + e], slope = kCap ? held * fmaf(-z, z, 1.0f) : held;
-      p[e] = visible(r + e) ? attn_exp2(fmaf(z, factor, -lse(r + e))) : 0.0f;
+      const float z = s[r + e] * root, slope = kCap ? fmaf(-z, z, held) : held;
+      p[e] = visible(r + e) ? attn_exp2(fmaf(s[r + e], factor, -lse(r + e))) : 0.0f;
       dz[e] = p[e] * (dp[r + e] - delta(r + e)) * slope;
       if (T::kNarrow) p[e] *= kProbabilityScale;
     }

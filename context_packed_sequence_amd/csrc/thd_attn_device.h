@@ -84,30 +84,32 @@ __device__ __forceinline__ F32x16 zero16() {
 
 __device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// s = tanh(s in), element by element.  Scores are mostly well below their cap, and for
-// |x| <= 0.75 a polynomial takes fewer cycles than the two quarter-rate instructions of
-// 1 - 2 / (1 + e^(2x)), and keeps its relative precision near 0 (minimax over the
-// interval, error 3.3e-8 before rounding; the other form is off by up to 2^-23
-// absolute).  Taken where no lane's score is larger.
-__device__ __forceinline__ void attn_tanh(F32x16& s, float in) {
+// Capped scores in powers of two: s = cap log2(e) tanh(scale s / cap), element by
+// element.  Scores are mostly well below their cap, and up to half of it s times an even
+// polynomial, whose coefficients hold all the factors, takes six instructions an element
+// where 1 - 2 / (1 + e^(2x)) takes two of a quarter of their rate; it also keeps its
+// relative precision near 0, where the other form is off by up to 2^-23 of the cap.
+// Taken where no lane's score is larger.
+__device__ __forceinline__ void attn_capped(const AttnArgs& a, F32x16& s) {
   float top = fmaxf(fabsf(s[0]), fabsf(s[1]));
 #pragma unroll
   for (int r = 2; r < 16; r += 2) top = fmaxf(fmaxf(top, fabsf(s[r])), fabsf(s[r + 1]));
-  if (!__any(top * in > 0.75f)) {
+  if (!__any(top > a.curve_limit)) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const float x = s[r] * in, u = x * x;
-      float p = fmaf(u, -0.00476947f, 0.01966489f);
-      p = fmaf(u, p, -0.05339025f);
-      p = fmaf(u, p, 0.13326521f);
-      p = fmaf(u, p, -0.33333068f);
-      s[r] = fmaf(x, u * p, x);
+      const float u = s[r] * s[r];
+      float p = fmaf(u, a.curve[4], a.curve[3]);
+      p = fmaf(u, p, a.curve[2]);
+      p = fmaf(u, p, a.curve[1]);
+      p = fmaf(u, p, a.curve[0]);
+      s[r] *= p;
     }
     return;
   }
-  const float in2 = 2.0f * kAttnLog2e * in;
+  const float most = a.cap * kAttnLog2e, in = 2.0f * kAttnLog2e * (a.scale / a.cap);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) s[r] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + attn_exp2(s[r] * in2));
+  for (int r = 0; r < 16; ++r)
+    s[r] = fmaf(-2.0f * most, __builtin_amdgcn_rcpf(1.0f + attn_exp2(s[r] * in)), most);
 }
 
 // Value of lane l ^ 32, combined.

@@ -58,12 +58,9 @@ struct ForwardWave {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = T::mfma(k[i], q[i0 + i], s);
     }
-    // scores in powers of two: z log2(e) = s factor
-    float factor = a.scale * kAttnLog2e;
-    if constexpr (kCap) {
-      factor = a.cap * kAttnLog2e;
-      attn_tanh(s, a.scale / a.cap);
-    }
+    // scores in powers of two: s factor
+    const float factor = kCap ? 1.0f : a.scale * kAttnLog2e;
+    if constexpr (kCap) attn_capped(a, s);
     if (partly) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = seen(key0 + 4 * h + (r & 3) + 8 * (r >> 2)) ? s[r] : -kAttnInf;

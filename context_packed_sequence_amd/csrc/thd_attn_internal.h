@@ -78,6 +78,8 @@ struct AttnArgs {
   int32_t key_parts;       // workgroups that a group's heads are dealt out over for the key gradients
   int32_t causal, window;  // window 0: none
   int32_t cp, rank;
+  float curve[5];          // with a cap: coefficients of the capped scores' polynomial in s^2,
+  float curve_limit;       // for |s| up to this; -1: never
   float scale, cap;        // cap 0: none
   AttnPlan plan;
 };
