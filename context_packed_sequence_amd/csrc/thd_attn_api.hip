@@ -75,10 +75,9 @@ Layout layout(const thd_attention_shape& s, void* workspace, bool backward) {
     return p;
   };
   l.plan.header = reinterpret_cast<int32_t*>(take(thdcp::kAttnHeaderWords * 4));
-  l.plan.query_first = reinterpret_cast<int32_t*>(take((s.n_slots + 1LL) * 4));
+  l.plan.slot_first = reinterpret_cast<int32_t*>(take((s.n_slots + 1LL) * 4));
   l.plan.query_tiles = reinterpret_cast<thdcp::QueryTile*>(take(nq * static_cast<int64_t>(sizeof(thdcp::QueryTile))));
   if (backward) {
-    l.plan.key_first = reinterpret_cast<int32_t*>(take((s.n_slots + 1LL) * 4));
     l.plan.key_tiles = reinterpret_cast<thdcp::KeyTile*>(take(nk * static_cast<int64_t>(sizeof(thdcp::KeyTile))));
     l.plan.delta = reinterpret_cast<float*>(take(rows * s.heads * 4));
     l.key_parts = key_parts(s, nk);
@@ -260,9 +259,11 @@ int thd_attention_backward(const thd_attention_shape* shape, const thd_heads* q,
   a.status = status;
   if (thdcp::launch_attn_plan(a, as_stream(stream)) != hipSuccess) return THD_ERR_HIP;
   if (rows == 0) return THD_OK;
-  if (thdcp::launch_attn_delta(a, as_stream(stream)) != hipSuccess) return THD_ERR_HIP;
-  if (thdcp::launch_attn_dkv(a, as_stream(stream)) != hipSuccess) return THD_ERR_HIP;
-  return thdcp::launch_attn_dq(a, as_stream(stream)) == hipSuccess ? THD_OK : THD_ERR_HIP;
+  // fp16 gradients are scaled by the largest norms, which come with delta; bf16 takes
+  // delta in the query gradients' launch
+  if (s.dtype == THD_FP16 && thdcp::launch_attn_delta(a, as_stream(stream)) != hipSuccess) return THD_ERR_HIP;
+  if (thdcp::launch_attn_dq(a, as_stream(stream)) != hipSuccess) return THD_ERR_HIP;
+  return thdcp::launch_attn_dkv(a, as_stream(stream)) == hipSuccess ? THD_OK : THD_ERR_HIP;
 }
 
 }  // extern "C"

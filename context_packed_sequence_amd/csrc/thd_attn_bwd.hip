@@ -41,13 +41,26 @@ __device__ __forceinline__ float add_row16(float x) {
 // Rows that are not finite have no say in other rows' scale.
 __device__ __forceinline__ float finite_or_zero(float x) { return x < kAttnInf ? x : 0.0f; }
 
-// delta of a tile's rows, 16 lanes a row, and the largest norms for fp16.
+// sum + x . y of eight elements
+template <typename T>
+__device__ __forceinline__ float dot_words(const U32x4& x, const U32x4& y, float sum) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t u = x[k], v = y[k];
+    sum = fmaf(T::low(u), T::low(v), sum);
+    sum = fmaf(T::high(u), T::high(v), sum);
+  }
+  return sum;
+}
+
+// delta of a tile's rows, 16 lanes a row, and the largest norms, for fp16.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t query_blocks) {
   __shared__ float s_most[4];
   const int32_t l = threadIdx.x & 63, word = l & 15;
+  const bool query = static_cast<int32_t>(blockIdx.x) < query_blocks;
   float most = 0.0f;
-  if (static_cast<int32_t>(blockIdx.x) < query_blocks) {
+  if (query) {
     const int32_t parts = a.heads / a.tile_heads, first_head = blockIdx.x % parts * a.tile_heads;
     const QueryTile tile = a.plan.query_tiles[blockIdx.x / parts];
     if (tile.rows == 0) return;
@@ -58,23 +71,12 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
       const RowsRead o(head_rows(a.out, tile.row, head), static_cast<int32_t>(2 * a.out.row), tile.valid, a.dim);
       const RowsRead g(head_rows(a.dout, tile.row, head), static_cast<int32_t>(2 * a.dout.row), tile.valid, a.dim);
       const U32x4 x = o.load(row, word, a.dim), y = g.load(row, word, a.dim);
-      float dot = 0.0f, square = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t u = x[k], v = y[k];
-        dot = fmaf(T::low(u), T::low(v), dot);
-        dot = fmaf(T::high(u), T::high(v), dot);
-        if constexpr (T::kNarrow) {
-          square = fmaf(T::low(v), T::low(v), square);
-          square = fmaf(T::high(v), T::high(v), square);
-        }
-      }
-      dot = add_row16(dot);
+      const float dot = add_row16(dot_words<T>(x, y, 0.0f));
       if (word == 0 && row < tile.valid)
         a.plan.delta[static_cast<int64_t>(head) * a.rows + tile.row + row] = dot;
-      if constexpr (T::kNarrow) most = fmaxf(most, finite_or_zero(add_row16(square)));
+      most = fmaxf(most, finite_or_zero(add_row16(dot_words<T>(y, y, 0.0f))));
     }
-  } else if constexpr (T::kNarrow) {
+  } else {
     const int32_t b = blockIdx.x - query_blocks;
     const int32_t index = b / a.kv_heads, head = b % a.kv_heads;
     const KeyTile tile = a.plan.key_tiles[index];
@@ -84,28 +86,18 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
 #pragma unroll
     for (int i = 0; i < kAttnKeys / 16; ++i) {
       const U32x4 x = v.load(16 * i + (threadIdx.x >> 4), word, a.dim);
-      float square = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t u = x[k];
-        square = fmaf(T::low(u), T::low(u), square);
-        square = fmaf(T::high(u), T::high(u), square);
-      }
-      most = fmaxf(most, finite_or_zero(add_row16(square)));
+      most = fmaxf(most, finite_or_zero(add_row16(dot_words<T>(x, x, 0.0f))));
     }
   }
-  if constexpr (T::kNarrow) {
 #pragma unroll
-    for (int i = 16; i < 64; i <<= 1) most = fmaxf(most, __shfl_xor(most, i));
-    if (l == 0) s_most[threadIdx.x >> 6] = most;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      most = sqrtf(fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3])));
-      // not negative: floats order as their bits do, and a maximum has no order
-      const bool query = static_cast<int32_t>(blockIdx.x) < query_blocks;
-      if (most > 0.0f)
-        atomicMax(a.plan.header + (query ? kAttnMaxGrad : kAttnMaxValue), __builtin_bit_cast(int32_t, most));
-    }
+  for (int i = 16; i < 64; i <<= 1) most = fmaxf(most, __shfl_xor(most, i));
+  if (l == 0) s_most[threadIdx.x >> 6] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    most = sqrtf(fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3])));
+    // not negative: floats order as their bits do, and a maximum has no order
+    if (most > 0.0f)
+      atomicMax(a.plan.header + (query ? kAttnMaxGrad : kAttnMaxValue), __builtin_bit_cast(int32_t, most));
   }
 }
 
@@ -217,7 +209,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
       const int64_t at = static_cast<int64_t>(own.head) * a.rows + tile.row + own.first + c;
       const float x = a.lse[at] * kAttnLog2e;
       lse = x == -kAttnInf ? kAttnInf : x;
-      delta = a.plan.delta[at];
+      if constexpr (T::kNarrow) delta = a.plan.delta[at];
+    }
+    if constexpr (!T::kNarrow) {
+      // here, where the rows of dout are at hand, for the key gradients' launch too
+      const RowsRead outs(head_rows(a.out, tile.row + own.first, own.head), static_cast<int32_t>(2 * a.out.row),
+                          own.valid, a.dim);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kDim / 16; ++i) dot = dot_words<T>(outs.load(c, 2 * i + h, a.dim), g[i], dot);
+      delta = add_halves(dot);
+      if (l < own.valid) a.plan.delta[static_cast<int64_t>(own.head) * a.rows + tile.row + own.first + l] = delta;
     }
     const Seen first(a, tile.pos, tile.real), last(a, tile.pos + tile.valid - 1, tile.real);
     const int32_t end = last.low + static_cast<int32_t>(last.span);
@@ -533,14 +535,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   }
 }
 
-template <typename T>
-hipError_t delta(const AttnArgs& a, hipStream_t stream) {
-  const int32_t query_blocks = a.plan.max_query_tiles * (a.heads / a.tile_heads);
-  const int32_t blocks = query_blocks + (T::kNarrow ? a.plan.max_key_tiles * a.kv_heads : 0);
-  attn_delta_kernel<T><<<blocks, 256, 0, stream>>>(a, query_blocks);
-  return hipGetLastError();
-}
-
 template <typename T, int kDim>
 hipError_t dq(const AttnArgs& a, hipStream_t stream) {
   const int32_t units = a.plan.max_query_tiles * a.kv_heads;
@@ -566,7 +560,10 @@ hipError_t dkv(const AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {
-  return a.dtype == THD_BF16 ? delta<AttnBf16>(a, stream) : delta<AttnFp16>(a, stream);
+  const int32_t query_blocks = a.plan.max_query_tiles * (a.heads / a.tile_heads);
+  const int32_t blocks = query_blocks + a.plan.max_key_tiles * a.kv_heads;
+  attn_delta_kernel<AttnFp16><<<blocks, 256, 0, stream>>>(a, query_blocks);
+  return hipGetLastError();
 }
 
 hipError_t launch_attn_dq(const AttnArgs& a, hipStream_t stream) {

@@ -50,10 +50,9 @@ enum AttnHeader : int { kAttnMaxGrad = 0, kAttnMaxValue = 1, kAttnCode = 2, kAtt
 
 struct AttnPlan {
   int32_t* header;         // [kAttnHeaderWords]
-  int32_t* query_first;    // [slots + 1] tiles of the slots before
-  int32_t* key_first;      // [slots + 1], null without key tiles
+  int32_t* slot_first;     // [slots + 1] tiles of the slots before
   QueryTile* query_tiles;  // [max_query_tiles], heaviest first, those without rows last
-  KeyTile* key_tiles;      // [max_key_tiles]
+  KeyTile* key_tiles;      // [max_key_tiles], null in the forward pass
   float* delta;            // [heads][rows], backward only
   float* partial;          // [key parts][2][tokens][kv heads][dim], with more than one part
   int32_t max_query_tiles;

@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 256;
+constexpr int kSlotsInLds = 4096;
 
 __device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t per) { return (n + per - 1) / per; }
 
@@ -27,12 +28,18 @@ __device__ __forceinline__ int32_t bucket_of(int32_t weight) {
   return kBuckets - 2 - static_cast<int32_t>((bits >> 20) - 1016u);  // weights up to 2^31: 0..247
 }
 
+// The boundaries, and the tiles of all slots before each: in LDS where they fit.
+struct Bounds {
+  const int32_t *padded, *real;
+  int32_t* first;
+};
+
 struct Slot {
   int32_t start, padded, real, first, chunk;
-  __device__ __forceinline__ Slot(const AttnArgs& a, int32_t s) {
-    start = a.cu_padded[s];
-    padded = a.cu_padded[s + 1] - start;
-    real = a.cu_real ? a.cu_real[s + 1] - a.cu_real[s] : padded;
+  __device__ __forceinline__ Slot(const AttnArgs& a, const Bounds& b, int32_t s) {
+    start = b.padded[s];
+    padded = b.padded[s + 1] - start;
+    real = b.real[s + 1] - b.real[s];
     first = start / a.cp;
     chunk = a.cp == 1 ? padded : padded / (2 * a.cp);
   }
@@ -150,21 +157,32 @@ __device__ void place_tiles(int32_t n, int32_t most, Tile* out, int32_t* s_bucke
   __syncthreads();
 }
 
+template <bool kInLds>
 __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnArgs a) {
   __shared__ int32_t s_wave[kPlanThreads / 64 + 1];
   __shared__ int32_t s_bucket[kBuckets];
   __shared__ int32_t s_severity;
+  __shared__ int32_t s_bounds[kInLds ? 3 : 1][kInLds ? kSlotsInLds + 1 : 1];
   const AttnPlan& p = a.plan;
+  Bounds bounds{a.cu_padded, a.cu_real ? a.cu_real : a.cu_padded, p.slot_first};
+  if constexpr (kInLds) {
+    for (int32_t s = threadIdx.x; s <= a.n_slots; s += kPlanThreads) {
+      const int32_t padded = a.cu_padded[s], real = bounds.real[s];
+      s_bounds[0][s] = padded;
+      s_bounds[1][s] = real;
+    }
+    bounds = Bounds{s_bounds[0], s_bounds[1], s_bounds[2]};
+  }
   if (threadIdx.x == 0) s_severity = 0;
   __syncthreads();
   int32_t severity = 0;
   if (threadIdx.x == 0) {
-    if (a.cu_padded[0] != 0 || (a.cu_real && a.cu_real[0] != 0)) severity = kSevStart;
-    else if (a.cu_padded[a.n_slots] != a.total) severity = kSevTotal;
+    if (bounds.padded[0] != 0 || bounds.real[0] != 0) severity = kSevStart;
+    else if (bounds.padded[a.n_slots] != a.total) severity = kSevTotal;
   }
   for (int32_t s = threadIdx.x; s < a.n_slots; s += kPlanThreads) {
-    const int64_t padded = static_cast<int64_t>(a.cu_padded[s + 1]) - a.cu_padded[s];
-    const int64_t real = a.cu_real ? static_cast<int64_t>(a.cu_real[s + 1]) - a.cu_real[s] : padded;
+    const int64_t padded = static_cast<int64_t>(bounds.padded[s + 1]) - bounds.padded[s];
+    const int64_t real = static_cast<int64_t>(bounds.real[s + 1]) - bounds.real[s];
     if (padded < 0 || real < 0) severity = max(severity, kSevMonotone);
     else if (a.cp > 1 && padded % (2 * a.cp) != 0) severity = max(severity, kSevDivisible);
     else if (real > padded) severity = max(severity, kSevRealGtPadded);
@@ -183,18 +201,18 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnArgs a) {
     for (int32_t t = threadIdx.x; t < p.max_key_tiles; t += kPlanThreads) p.key_tiles[t] = KeyTile{};
     return;
   }
-  const int32_t nq = slot_prefix(a.n_slots, p.query_first, s_wave,
-                                 [&](int32_t s) { return query_tiles_of(a, Slot(a, s)); });
+  const int32_t nq = slot_prefix(a.n_slots, bounds.first, s_wave,
+                                 [&](int32_t s) { return query_tiles_of(a, Slot(a, bounds, s)); });
   place_tiles(nq, p.max_query_tiles, p.query_tiles, s_bucket, [&](int32_t t, int32_t* weight) {
-    const int32_t s = slot_of(p.query_first, a.n_slots, t);
-    return query_tile(a, Slot(a, s), t - p.query_first[s], weight);
+    const int32_t s = slot_of(bounds.first, a.n_slots, t);
+    return query_tile(a, Slot(a, bounds, s), t - bounds.first[s], weight);
   });
   if (p.key_tiles) {
-    const int32_t nk = slot_prefix(a.n_slots, p.key_first, s_wave,
-                     [&](int32_t s) { return tiles_of(Slot(a, s).padded, kAttnKeys); });
+    const int32_t nk = slot_prefix(a.n_slots, bounds.first, s_wave,
+                                   [&](int32_t s) { return tiles_of(Slot(a, bounds, s).padded, kAttnKeys); });
     place_tiles(nk, p.max_key_tiles, p.key_tiles, s_bucket, [&](int32_t t, int32_t* weight) {
-      const int32_t s = slot_of(p.key_first, a.n_slots, t);
-      return key_tile(a, Slot(a, s), t - p.key_first[s], weight);
+      const int32_t s = slot_of(bounds.first, a.n_slots, t);
+      return key_tile(a, Slot(a, bounds, s), t - bounds.first[s], weight);
     });
   }
 }
@@ -202,7 +220,8 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnArgs a) {
 }  // namespace
 
 hipError_t launch_attn_plan(const AttnArgs& a, hipStream_t stream) {
-  attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  if (a.n_slots <= kSlotsInLds) attn_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
+  else attn_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
