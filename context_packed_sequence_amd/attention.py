@@ -26,35 +26,42 @@ from .losses import _address, _need_gpu, _run, _workspace
 
 _DTYPES = {torch.bfloat16: _b.THD_BF16, torch.float16: _b.THD_FP16}
 _I32, _F32 = torch.int32, torch.float32
+_byref = ctypes.byref
 
 
 def _heads(x, name, rows=None, heads=None, like=None):
     """The tensor as the library takes it, after the checks it cannot make."""
     if x is None:
         raise ValueError(f"{name} is required")
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be bfloat16 or float16, got {x.dtype}")
-    if x.dim() != 3:
+    dtype, sizes = x.dtype, x.shape
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {dtype}")
+    if len(sizes) != 3:
         raise ValueError(f"{name} must be [rows, heads, dim]")
+    n, m, dim = sizes
     if like is not None:
-        if x.dtype != like.dtype:
-            raise ValueError(f"{name} must be {like.dtype}, got {x.dtype}")
+        if dtype != like.dtype:
+            raise ValueError(f"{name} must be {like.dtype}, got {dtype}")
         if x.get_device() != like.get_device():
             raise ValueError(f"{name} must be on {like.device}, got {x.device}")
-        if x.shape[2] != like.shape[2]:
-            raise ValueError(f"{name} must have heads of {like.shape[2]} elements, got {x.shape[2]}")
-    if (rows is not None and x.shape[0] != rows) or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name} must be [{rows}, {x.shape[1] if heads is None else heads}, {x.shape[2]}], "
-                         f"got {list(x.shape)}")
-    if x.numel() and x.stride(2) != 1 and x.shape[2] != 1:
+        if dim != like.shape[2]:
+            raise ValueError(f"{name} must have heads of {like.shape[2]} elements, got {dim}")
+    if (rows is not None and n != rows) or (heads is not None and m != heads):
+        raise ValueError(f"{name} must be [{rows}, {m if heads is None else heads}, {dim}], got {list(sizes)}")
+    rows_apart, heads_apart, step = x.stride()
+    some = n and m and dim
+    if some and step != 1 and dim != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    rows_apart = x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
-    heads_apart = x.stride(1) if x.shape[1] > 1 else x.shape[2]
-    if rows_apart % 8 or heads_apart % 8 or x.data_ptr() % 16:
+    if n <= 1:
+        rows_apart = m * dim
+    if m <= 1:
+        heads_apart = dim
+    at = x.data_ptr()
+    if rows_apart % 8 or heads_apart % 8 or at % 16:
         raise ValueError(f"{name}: rows and heads must start at multiples of 16 bytes")
-    if x.shape[0] > 1 and rows_apart < x.shape[2]:
+    if n > 1 and rows_apart < dim:
         raise ValueError(f"{name}: rows must not overlap")
-    return _b.thd_heads(x.data_ptr() if x.numel() else None, rows_apart, heads_apart)
+    return _b.thd_heads(at if some else None, rows_apart, heads_apart)
 
 
 def _shape(q, k, v, cu_seqlens_padded, cu_seqlens, causal, window, scale, cap, cp_size, rank):
@@ -63,7 +70,7 @@ def _shape(q, k, v, cu_seqlens_padded, cu_seqlens, causal, window, scale, cap, c
     k_at = _heads(k, "k", like=q)
     tokens, kv_heads, dim = k.shape
     v_at = _heads(v, "v", tokens, kv_heads, like=q)
-    rows, heads = q.shape[:2]
+    rows, heads, _ = q.shape
     if dim % 8 or not 8 <= dim <= _b.THD_MAX_HEAD_DIM:
         raise ValueError(f"heads must have a multiple of 8 elements, 8 to {_b.THD_MAX_HEAD_DIM}, got {dim}")
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
@@ -99,20 +106,22 @@ def packed_attention(q, k, v, cu_seqlens_padded, cu_seqlens=None, causal=True, w
     ``scale`` is 1 / sqrt(dim) unless given.  Pads, by ``cu_seqlens`` (real
     boundaries), take no part; their rows of ``out`` are 0, their lse -inf."""
     shape, q_at, k_at, v_at = _shape(q, k, v, cu_seqlens_padded, cu_seqlens, causal, window, scale, cap, cp_size, rank)
-    if out is not None:
-        _heads(out, "out", q.shape[0], q.shape[1], like=q)
+    rows, heads, dim = q.shape
+    out_at = None if out is None else _heads(out, "out", rows, heads, like=q)
     lib = _b.library()
 
     def call(handle):
         dev = q.device
-        result = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=_F32, device=dev)
+        result, result_at = out, out_at
+        if out is None:
+            result = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
+            result_at = _b.thd_heads(result.data_ptr(), heads * dim, dim)
+        lse = torch.empty((heads, rows), dtype=_F32, device=dev)
         status = torch.empty(1, dtype=_I32, device=dev)
-        nbytes = lib.thd_attention_workspace_bytes(ctypes.byref(shape), 0)
+        nbytes = lib.thd_attention_workspace_bytes(_byref(shape), 0)
         room, room_at = _workspace(nbytes, dev)
-        code = lib.thd_attention(ctypes.byref(shape), ctypes.byref(q_at), ctypes.byref(k_at), ctypes.byref(v_at),
-                                 ctypes.byref(_heads(result, "out")), lse.data_ptr(), status.data_ptr(), room_at,
-                                 nbytes, handle)
+        code = lib.thd_attention(_byref(shape), _byref(q_at), _byref(k_at), _byref(v_at), _byref(result_at),
+                                 lse.data_ptr(), status.data_ptr(), room_at, nbytes, handle)
         if code < 0:
             raise _b.ThdError(code, "thd_attention")
         if out is not None:
@@ -129,7 +138,7 @@ def packed_attention_backward(dout, q, k, v, out, lse, cu_seqlens_padded, cu_seq
     ranks.  ``grads`` may give the three tensors to write, e.g. views of one
     projection's gradient."""
     shape, q_at, k_at, v_at = _shape(q, k, v, cu_seqlens_padded, cu_seqlens, causal, window, scale, cap, cp_size, rank)
-    rows, heads = q.shape[:2]
+    rows, heads, _ = q.shape
     out_at = _heads(out, "out", rows, heads, like=q)
     dout_at = _heads(dout, "dout", rows, heads, like=q)
     if lse is not None and tuple(lse.shape) != (heads, rows):
@@ -138,25 +147,26 @@ def packed_attention_backward(dout, q, k, v, out, lse, cu_seqlens_padded, cu_seq
     if grads is not None:
         if len(grads) != 3:
             raise ValueError("grads must be three tensors, for q, k and v")
-        for name, g, x in zip(("dq", "dk", "dv"), grads, (q, k, v)):
-            _heads(g, name, x.shape[0], x.shape[1], like=q)
+        to = [_heads(g, name, x.shape[0], x.shape[1], like=q)
+              for name, g, x in zip(("dq", "dk", "dv"), grads, (q, k, v))]
     lib = _b.library()
 
     def call(handle):
         dev = q.device
-        dq, dk, dv = grads if grads is not None else [torch.empty(x.shape, dtype=x.dtype, device=dev)
-                                                      for x in (q, k, v)]
+        results, at = grads, None if grads is None else to
+        if grads is None:
+            results = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v)]
+            at = [_b.thd_heads(g.data_ptr(), g.shape[1] * g.shape[2], g.shape[2]) for g in results]
         status = torch.empty(1, dtype=_I32, device=dev)
-        nbytes = lib.thd_attention_workspace_bytes(ctypes.byref(shape), 1)
+        nbytes = lib.thd_attention_workspace_bytes(_byref(shape), 1)
         room, room_at = _workspace(nbytes, dev)
-        at = [ctypes.byref(x) for x in (q_at, k_at, v_at, out_at)]
-        to = [ctypes.byref(_heads(x, "gradient")) for x in (dq, dk, dv)]
-        code = lib.thd_attention_backward(ctypes.byref(shape), *at, lse_at, ctypes.byref(dout_at), *to,
+        code = lib.thd_attention_backward(_byref(shape), _byref(q_at), _byref(k_at), _byref(v_at), _byref(out_at),
+                                          lse_at, _byref(dout_at), _byref(at[0]), _byref(at[1]), _byref(at[2]),
                                           status.data_ptr(), room_at, nbytes, handle)
         if code < 0:
             raise _b.ThdError(code, "thd_attention_backward")
         if grads is not None:
             for g in grads:
                 torch.autograd.graph.increment_version(g)
-        return dq, dk, dv, status
+        return (*results, status)
     return _run(call, stream)

@@ -154,17 +154,18 @@ template <typename T, int kDim>
 __device__ __forceinline__ void row_products(const char* x, const char* y, int32_t row, const U32x4 (&bx)[kDim / 16],
                                              const U32x4 (&by)[kDim / 16], F32x16& s, F32x16& dp) {
   asm volatile("" : "+v"(row));  // words' places differ in single bits: not kept in registers
+  constexpr int kRead = kDim % 64 == 0 ? 4 : 3;
 #pragma unroll
-  for (int i0 = 0; i0 < kDim / 16; i0 += 4) {
-    U32x4 fx[4], fy[4];
+  for (int i0 = 0; i0 < kDim / 16; i0 += kRead) {
+    U32x4 fx[kRead], fy[kRead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kRead; ++i) {
       fx[i] = lds_read(x + (row ^ (32 * (i0 + i))), 0);
       fy[i] = lds_read(y + (row ^ (32 * (i0 + i))), 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kRead; ++i) {
       s = T::mfma(fx[i], bx[i0 + i], s);
       dp = T::mfma(fy[i], by[i0 + i], dp);
     }
@@ -175,7 +176,7 @@ __device__ __forceinline__ void row_products(const char* x, const char* y, int32
 // pass.
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
-  constexpr int kTile = kAttnStep * 2 * kDim;
+  constexpr int kTile = kAttnStep * kRowBytes<kDim>;
   __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile];  // keys, values, and both again
   const AttnPlace place(blockIdx.x, a.kv_heads, a.group / a.tile_heads);
   if (place.tile >= a.plan.max_query_tiles) return;
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
       if (key + kAttnStep < end) load(next);
 #pragma unroll
       for (int b = 0; b < kAttnStep / 32; ++b) {
-        const int32_t k0 = key + 32 * b, skip = 32 * b * 2 * kDim;
+        const int32_t k0 = key + 32 * b, skip = 32 * b * kRowBytes<kDim>;
         if (k0 < steps.any || k0 >= steps.any_end) continue;
         F32x16 s = zero16(), dp = zero16();
         row_products<T, kDim>(s_tiles + now + skip, s_tiles + now + kTile + skip, row_at, q, g, s, dp);
@@ -371,11 +372,11 @@ __device__ __forceinline__ void store_sums(const AttnArgs& a, int32_t part, int3
 // workgroups, each of which leaves its sums in 32 bits for attn_join_kernel.
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
-  constexpr bool kHold = kDim == 64;           // values in registers
+  constexpr bool kHold = kDim <= 96;           // values in registers
   constexpr int kStep = kHold ? kAttnStep : 32;
-  constexpr int kTile = kStep * 2 * kDim;
+  constexpr int kTile = kStep * kRowBytes<kDim>;
   // query rows, rows of dout, both again, values
-  __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile + (kHold ? 0 : kAttnKeys * 2 * kDim)];
+  __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile + (kHold ? 0 : kAttnKeys * kRowBytes<kDim>)];
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
   const AttnPlace place(blockIdx.x, a.kv_heads, a.key_parts);
   if (place.tile >= a.plan.max_key_tiles) return;
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
       if (!walk.done()) load(next);
 #pragma unroll
       for (int b = 0; b < kStep / 32; ++b) {
-        const int32_t p0 = pos + 32 * b, skip = 32 * b * 2 * kDim;
+        const int32_t p0 = pos + 32 * b, skip = 32 * b * kRowBytes<kDim>;
         if (32 * b >= n || p0 < steps.any || p0 >= steps.any_end) continue;
         // the sums start at what is taken from them: -lse (as a score; with a cap, after it)
         // and -delta
@@ -451,7 +452,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
         if constexpr (kHold) {
           row_products<T, kDim>(rows, rows + kTile, row_at, k, v, s, dp);
         } else {
-          int32_t row = row_at, value = row_at + 32 * wave * 2 * kDim;
+          int32_t row = row_at, value = row_at + 32 * wave * kRowBytes<kDim>;
           asm volatile("" : "+v"(row), "+v"(value));
 #pragma unroll
           for (int i0 = 0; i0 < kDim / 16; i0 += 2) {
@@ -557,6 +558,15 @@ hipError_t dkv(const AttnArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <typename T>
+hipError_t dq(const AttnArgs& a, hipStream_t stream) {
+  return a.dim <= 64 ? dq<T, 64>(a, stream) : a.dim <= 96 ? dq<T, 96>(a, stream) : dq<T, 128>(a, stream);
+}
+template <typename T>
+hipError_t dkv(const AttnArgs& a, hipStream_t stream) {
+  return a.dim <= 64 ? dkv<T, 64>(a, stream) : a.dim <= 96 ? dkv<T, 96>(a, stream) : dkv<T, 128>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {
@@ -567,13 +577,11 @@ hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_attn_dq(const AttnArgs& a, hipStream_t stream) {
-  if (a.dtype == THD_BF16) return a.dim <= 64 ? dq<AttnBf16, 64>(a, stream) : dq<AttnBf16, 128>(a, stream);
-  return a.dim <= 64 ? dq<AttnFp16, 64>(a, stream) : dq<AttnFp16, 128>(a, stream);
+  return a.dtype == THD_BF16 ? dq<AttnBf16>(a, stream) : dq<AttnFp16>(a, stream);
 }
 
 hipError_t launch_attn_dkv(const AttnArgs& a, hipStream_t stream) {
-  if (a.dtype == THD_BF16) return a.dim <= 64 ? dkv<AttnBf16, 64>(a, stream) : dkv<AttnBf16, 128>(a, stream);
-  return a.dim <= 64 ? dkv<AttnFp16, 64>(a, stream) : dkv<AttnFp16, 128>(a, stream);
+  return a.dtype == THD_BF16 ? dkv<AttnBf16>(a, stream) : dkv<AttnFp16>(a, stream);
 }
 
 }  // namespace thdcp

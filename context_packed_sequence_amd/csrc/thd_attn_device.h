@@ -12,7 +12,7 @@
 // ds_read_b64_tr_b16 gives just that: of 4 rows of 16 elements that 16 lanes
 // point to, lane i gets column i.
 //
-// LDS tiles are rows of kDim 16-bit elements in 16-byte words, word w of row r at
+// LDS tiles are rows of 64 or 128 16-bit elements in 16-byte words, word w of row r at
 // place w ^ f(r).  f gives any 16 rows different places (reads of one word of 32
 // rows, as A needs) and any 4 rows different quarters of the banks (transposing
 // reads: 64 bytes of each of 4 rows), so neither read has bank conflicts.
@@ -125,16 +125,21 @@ __device__ __forceinline__ float add_halves(float x) {
   return __builtin_bit_cast(float, static_cast<uint32_t>(r[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(r[1]));
 }
 
+// Heads of up to 64, 96 or 128 elements (kDim) have kernels of their own; a row in LDS
+// has room for 64 or 128.
+template <int kDim>
+constexpr int kRowBytes = kDim <= 64 ? 128 : 256;
+
 template <int kDim>
 __device__ __forceinline__ int32_t lds_swizzle(int32_t row) {
-  if constexpr (kDim == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  if constexpr (kRowBytes<kDim> == 256) return ((row & 3) << 2) | ((row >> 2) & 3);
   else return ((row & 2) << 1) | ((row >> 2) & 3);  // two rows share a line of banks
 }
 
 // Byte address in a tile of word w of a row.
 template <int kDim>
 __device__ __forceinline__ int32_t lds_word(int32_t row, int32_t w) {
-  return row * (2 * kDim) + ((w ^ lds_swizzle<kDim>(row)) << 4);
+  return row * kRowBytes<kDim> + ((w ^ lds_swizzle<kDim>(row)) << 4);
 }
 
 __device__ __forceinline__ U32x4 lds_read(const char* tile, int32_t at) {
@@ -182,7 +187,27 @@ __device__ __forceinline__ void read_columns(uint32_t first, uint32_t second, U3
           "=&v"(x[1][1]), "=&v"(y[1][1]), "=&v"(x[2][0]), "=&v"(y[2][0]), "=&v"(x[2][1]), "=&v"(y[2][1]),
           "=&v"(x[3][0]), "=&v"(y[3][0]), "=&v"(x[3][1]), "=&v"(y[3][1])
         : "v"(first), "v"(first ^ 64), "v"(first ^ 128), "v"(first ^ 192), "v"(second), "v"(second ^ 64),
-          "v"(second ^ 128), "v"(second ^ 192), "i"(kFrom), "i"(kFrom + 16 * 2 * kDim)
+          "v"(second ^ 128), "v"(second ^ 192), "i"(kFrom), "i"(kFrom + 16 * kRowBytes<kDim>)
+        : "memory");
+  } else if constexpr (kDim == 96) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %12 offset:%18\n"
+        "ds_read_b64_tr_b16 %1, %15 offset:%18\n"
+        "ds_read_b64_tr_b16 %2, %12 offset:%19\n"
+        "ds_read_b64_tr_b16 %3, %15 offset:%19\n"
+        "ds_read_b64_tr_b16 %4, %13 offset:%18\n"
+        "ds_read_b64_tr_b16 %5, %16 offset:%18\n"
+        "ds_read_b64_tr_b16 %6, %13 offset:%19\n"
+        "ds_read_b64_tr_b16 %7, %16 offset:%19\n"
+        "ds_read_b64_tr_b16 %8, %14 offset:%18\n"
+        "ds_read_b64_tr_b16 %9, %17 offset:%18\n"
+        "ds_read_b64_tr_b16 %10, %14 offset:%19\n"
+        "ds_read_b64_tr_b16 %11, %17 offset:%19\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(x[0][0]), "=&v"(y[0][0]), "=&v"(x[0][1]), "=&v"(y[0][1]), "=&v"(x[1][0]), "=&v"(y[1][0]),
+          "=&v"(x[1][1]), "=&v"(y[1][1]), "=&v"(x[2][0]), "=&v"(y[2][0]), "=&v"(x[2][1]), "=&v"(y[2][1])
+        : "v"(first), "v"(first ^ 64), "v"(first ^ 128), "v"(second), "v"(second ^ 64), "v"(second ^ 128), "i"(kFrom),
+          "i"(kFrom + 16 * kRowBytes<kDim>)
         : "memory");
   } else {
     asm volatile(
@@ -197,7 +222,7 @@ __device__ __forceinline__ void read_columns(uint32_t first, uint32_t second, U3
         "s_waitcnt lgkmcnt(0)\n"
         : "=&v"(x[0][0]), "=&v"(y[0][0]), "=&v"(x[0][1]), "=&v"(y[0][1]), "=&v"(x[1][0]), "=&v"(y[1][0]),
           "=&v"(x[1][1]), "=&v"(y[1][1])
-        : "v"(first), "v"(first ^ 64), "v"(second), "v"(second ^ 64), "i"(kFrom), "i"(kFrom + 16 * 2 * kDim)
+        : "v"(first), "v"(first ^ 64), "v"(second), "v"(second ^ 64), "i"(kFrom), "i"(kFrom + 16 * kRowBytes<kDim>)
         : "memory");
   }
 #pragma unroll
@@ -243,7 +268,7 @@ __device__ __forceinline__ const char* head_rows(const AttnTensor& t, int64_t ro
 // barrier after which the tile is read.
 template <int kDim, int kRows = kAttnStep>
 __device__ __forceinline__ void load_tile(char* tile, const RowsRead& r, int32_t dim) {
-  constexpr int kWords = kDim / 8;
+  constexpr int kWords = kRowBytes<kDim> / 16;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
   for (int j = 0; j < kRows * kWords / 256; ++j) {
@@ -364,7 +389,7 @@ __device__ __forceinline__ void store_rows(char* lds, const F32x16 (&acc)[kDim /
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  constexpr int kWords = kDim / 8;
+  constexpr int kWords = kRowBytes<kDim> / 16;
 #pragma unroll
   for (int j = 0; j < kWords / 2; ++j) {
     const int32_t s = j * 64 + l;

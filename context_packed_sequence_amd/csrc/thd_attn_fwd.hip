@@ -49,14 +49,15 @@ struct ForwardWave {
     int32_t row = key_at;
     asm volatile("" : "+v"(row));
     F32x16 s = zero16();
+    constexpr int kRead = kDim % 64 == 0 ? 4 : 3;
 #pragma unroll
-    for (int i0 = 0; i0 < kDim / 16; i0 += 4) {
-      U32x4 k[4];
+    for (int i0 = 0; i0 < kDim / 16; i0 += kRead) {
+      U32x4 k[kRead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = lds_read(lds + skip + (row ^ (32 * (i0 + i))), kKeys);
-      __builtin_amdgcn_sched_barrier(0);  // all four on their way before the first is waited for
+      for (int i = 0; i < kRead; ++i) k[i] = lds_read(lds + skip + (row ^ (32 * (i0 + i))), kKeys);
+      __builtin_amdgcn_sched_barrier(0);  // all on their way before the first is waited for
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s = T::mfma(k[i], q[i0 + i], s);
+      for (int i = 0; i < kRead; ++i) s = T::mfma(k[i], q[i0 + i], s);
     }
     // scores in powers of two: s factor
     const float factor = kCap ? 1.0f : a.scale * kAttnLog2e;
@@ -100,7 +101,7 @@ struct ForwardWave {
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 3) void attn_forward_kernel(AttnArgs a) {
   constexpr int kStep = kDim == 64 ? 64 : 32;
-  constexpr int kTile = kStep * 2 * kDim;  // bytes
+  constexpr int kTile = kStep * kRowBytes<kDim>;  // bytes
   __shared__ __attribute__((aligned(16))) char s_tiles[4 * kTile];  // keys, values, and both again
   const AttnPlace place(blockIdx.x, a.kv_heads, a.group / a.tile_heads);
   if (place.tile >= a.plan.max_query_tiles) return;
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(256, 3) void attn_forward_kernel(AttnArgs a) {
       for (int b = 0; b < kStep / 32; ++b) {
         const int32_t k0 = key + 32 * b;
         if (k0 >= steps.any && k0 < steps.any_end)
-          w.template step<now, now + kTile>(a, s_tiles, 32 * b * 2 * kDim, k0, k0 < steps.all || k0 >= steps.all_end,
+          w.template step<now, now + kTile>(a, s_tiles, 32 * b * kRowBytes<kDim>, k0, k0 < steps.all || k0 >= steps.all_end,
                                             seen);
       }
       key += kStep;
@@ -169,12 +170,15 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <typename T>
+hipError_t launch(const AttnArgs& a, hipStream_t stream) {
+  return a.dim <= 64 ? launch<T, 64>(a, stream) : a.dim <= 96 ? launch<T, 96>(a, stream) : launch<T, 128>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream) {
-  if (a.dtype == THD_BF16)
-    return a.dim <= 64 ? launch<AttnBf16, 64>(a, stream) : launch<AttnBf16, 128>(a, stream);
-  return a.dim <= 64 ? launch<AttnFp16, 64>(a, stream) : launch<AttnFp16, 128>(a, stream);
+  return a.dtype == THD_BF16 ? launch<AttnBf16>(a, stream) : launch<AttnFp16>(a, stream);
 }
 
 }  // namespace thdcp
