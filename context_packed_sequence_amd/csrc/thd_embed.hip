@@ -12,7 +12,8 @@
 // thousands of rows).  A token whose rows lie within one unit is stored at once;
 // where its run passes a unit's border the sums go to a workspace, and the thread
 // of the unit in which the run begins adds them up, in order, in the last launch.
-// The launch that sums also writes the rows of tokens that do not occur.
+// The rows of tokens that do not occur are cleared beside the sort of a small batch, or
+// beside the sums of a large one.
 #include "thd_loss_device.h"
 #include "thd_params_internal.h"
 
@@ -57,23 +58,28 @@ struct FlatPlace {
 constexpr int kLookupEach = 4;  // words of a thread
 
 template <typename T>
-__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int32_t words, FastDiv by_words, int64_t row_blocks) {
+__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int32_t words, FastDiv by_words) {
   constexpr int kPer = Elem<T>::kPer;
-  if (static_cast<int64_t>(blockIdx.x) == row_blocks) {  // the workgroup that looks through all ids
+  if (a.scan && blockIdx.x == 0) {  // the workgroup that looks through all ids, the first to start
     __shared__ int s_bad;
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
     bool bad = false;
-    for (int32_t t = threadIdx.x; t < a.rows; t += 256) {
-      const int64_t id = a.ids[t];
-      if (id < 0 || id >= a.vocab) bad |= !a.mask || a.mask[t] != 0;
+    constexpr int kAhead = 8;
+    for (int64_t t0 = threadIdx.x; t0 < a.rows; t0 += kAhead * 256) {
+      int64_t id[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) id[i] = t0 + i * 256 < a.rows ? a.ids[t0 + i * 256] : 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (t0 + i * 256 < a.rows && (id[i] < 0 || id[i] >= a.vocab)) bad |= !a.mask || a.mask[t0 + i * 256] != 0;
     }
     if (bad) s_bad = 1;
     __syncthreads();
     if (threadIdx.x == 0) *a.status = s_bad ? THD_ERR_TOKEN : THD_OK;
     return;
   }
-  const FlatPlace place(static_cast<int64_t>(blockIdx.x) * (256 * kLookupEach), words, by_words);
+  const FlatPlace place((static_cast<int64_t>(blockIdx.x) - a.scan) * (256 * kLookupEach), words, by_words);
   int64_t row[kLookupEach], id[kLookupEach];
   int32_t word[kLookupEach];
   bool live[kLookupEach];
@@ -120,6 +126,37 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int32_t words, 
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
         if (word[i] * kPer + j < a.width) to[j] = Elem<T>::round(v[j]);
+    }
+  }
+}
+
+// ---- rows without a token ---------------------------------------------------
+
+// The gradient's table for those who clear it: bytes are of a row, words its 16-byte
+// ones.
+struct ZeroRows {
+  char* to;
+  int64_t stride;
+  int32_t bytes, words;
+  FastDiv by_words;
+  int32_t first, end;  // rows of the table
+  int32_t each;        // of them to a workgroup
+  __device__ __forceinline__ int32_t row(int32_t block) const { return first + block * each; }
+};
+
+// Clears those of rows r0 .. r0 + n - 1 whose flag is not set.  Plain stores: parts of
+// a line at rows' ends meet in the caches (400 MB of rows of 1001 floats 74 us; stores
+// that pass the caches 97, and no faster for aligned rows).
+template <int kThreads>
+__device__ __forceinline__ void clear_rows(const ZeroRows& z, int32_t r0, int32_t n, const uint8_t* s_taken) {
+  for (int32_t i = threadIdx.x; i < n * z.words; i += kThreads) {
+    const int32_t r = z.by_words(i), at = 16 * (i - r * z.words);
+    if (s_taken[r]) continue;
+    char* to = z.to + (static_cast<int64_t>(r0) + r) * z.stride + at;
+    if (at + 16 <= z.bytes) {
+      store_loose(to, Word4{0, 0, 0, 0});
+    } else {
+      for (int32_t b = at; b < z.bytes; b += 2, to += 2) *reinterpret_cast<uint16_t*>(to) = 0;
     }
   }
 }
@@ -178,14 +215,29 @@ __device__ __forceinline__ void rank_digits(const uint32_t (&digit)[kEach], cons
   __syncthreads();
 }
 
-// Up to kSortBlock rows: one workgroup, all passes in LDS.
-__global__ __launch_bounds__(kSortThreads) void embed_sort_block_kernel(EmbedArgs a, EmbedSort s) {
+// Up to kSortBlock rows: one workgroup, all passes in LDS.  The others clear the rows
+// of tokens that do not occur meanwhile, having looked through the ids themselves: a
+// table far larger than the batch takes longer to clear than the batch to sort.
+__global__ __launch_bounds__(kSortThreads) void embed_sort_block_kernel(EmbedArgs a, EmbedSort s, ZeroRows z) {
   constexpr int kEach = kSortBlock / kSortThreads;
   __shared__ int32_t s_count[kSortWaves][kSortBins];
   __shared__ int32_t s_total[kSortBins];
   __shared__ int32_t s_wave[kSortWaves + 1];
   __shared__ int s_bad;
   __shared__ TokenRow s_item[kSortBlock];
+  if (blockIdx.x > 0) {
+    auto* s_taken = reinterpret_cast<uint8_t*>(s_item);
+    const int32_t r0 = z.row(static_cast<int32_t>(blockIdx.x) - 1), n = min(z.each, z.end - r0);
+    for (int32_t r = threadIdx.x; r < n; r += kSortThreads) s_taken[r] = 0;
+    __syncthreads();
+    for (int32_t t = threadIdx.x; t < a.rows; t += kSortThreads) {
+      const uint64_t r = static_cast<uint64_t>(a.ids[t]) - static_cast<uint64_t>(r0);
+      if (r < static_cast<uint64_t>(n) && (!a.mask || a.mask[t] != 0)) s_taken[r] = 1;
+    }
+    __syncthreads();
+    clear_rows<kSortThreads>(z, r0, n, s_taken);
+    return;
+  }
   const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (threadIdx.x == 0) s_bad = 0;
   TokenRow item[kEach];
@@ -376,15 +428,12 @@ __device__ __forceinline__ void load_partial(const EmbedArgs& a, const EmbedSort
 
 template <typename TI, typename TO>
 __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort s, int32_t words, FastDiv by_words,
-                                                         int32_t unit_blocks, int32_t table_rows) {
+                                                         int32_t unit_blocks, ZeroRows z) {
   constexpr int kPer = Elem<TI>::kPer;
   const auto none = static_cast<uint32_t>(a.vocab);
   if (static_cast<int32_t>(blockIdx.x) >= unit_blocks) {
-    // rows of the table without a token: table_rows of them a workgroup
-    constexpr int kOut = Elem<TO>::kPer;
-    __shared__ bool s_absent[256];
-    const int32_t r0 = (static_cast<int32_t>(blockIdx.x) - unit_blocks) * table_rows;
-    const int32_t n = min(table_rows, a.vocab - r0);
+    __shared__ uint8_t s_taken[256];
+    const int32_t r0 = z.row(static_cast<int32_t>(blockIdx.x) - unit_blocks), n = min(z.each, z.end - r0);
     if (static_cast<int32_t>(threadIdx.x) < n) {
       const auto v = static_cast<uint32_t>(r0 + threadIdx.x);
       int32_t low = 0, high = a.rows;  // first place whose key is not below v
@@ -393,19 +442,10 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort 
         if (s.a[mid].key < v) low = mid + 1;
         else high = mid;
       }
-      s_absent[threadIdx.x] = low == a.rows || s.a[low].key != v;
+      s_taken[threadIdx.x] = low < a.rows && s.a[low].key == v;
     }
     __syncthreads();
-    const int32_t out_words = (a.width + kOut - 1) / kOut;
-    for (int32_t r = 0; r < n; ++r) {
-      if (!s_absent[r]) continue;
-      TO* to = static_cast<TO*>(a.dtable) + static_cast<int64_t>(r0 + r) * a.out_stride;
-      for (int32_t w = threadIdx.x; w < out_words; w += 256) {
-        if (w * kOut + kOut <= a.width) store_loose(to + w * kOut, Word4{0, 0, 0, 0});
-        else
-          for (int j = w * kOut; j < a.width; ++j) to[j] = Elem<TO>::round(0.0f);
-      }
-    }
+    clear_rows<256>(z, r0, n, s_taken);
     return;
   }
   const FlatPlace place(static_cast<int64_t>(blockIdx.x) * 256, words, by_words);
@@ -504,19 +544,38 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, EmbedSort 
   finish_row<TI, TO>(a, key, word, acc);
 }
 
+// Rows [first, end) of the table, `bytes` of it and at most so many rows to a workgroup.
+ZeroRows zero_rows(const EmbedArgs& a, int32_t first, int32_t end, int64_t bytes, int32_t most_rows) {
+  const int64_t size = a.out_dtype == THD_FP32 ? 4 : 2, row = a.width * size;
+  ZeroRows z{};
+  z.to = static_cast<char*>(a.dtable);
+  z.stride = a.out_stride * size;
+  z.bytes = static_cast<int32_t>(row);
+  z.words = static_cast<int32_t>((row + 15) / 16);
+  z.by_words = FastDiv::make(z.words);
+  z.first = first;
+  z.end = end;
+  z.each = static_cast<int32_t>(row >= bytes ? 1 : bytes / row < most_rows ? bytes / row : most_rows);
+  return z;
+}
+int64_t zero_blocks(const EmbedArgs& a, const ZeroRows& z) {
+  return a.accumulate ? 0 : (static_cast<int64_t>(z.end) - z.first + z.each - 1) / z.each;
+}
+// Rows of the table that are cleared beside the sort; the others are, beside the sums.
+// Of a small batch, whose sort and sums are both short next to a large table.
+int32_t cleared_early(const EmbedArgs& a) {
+  return a.rows > 0 && a.rows <= kSortBlock ? static_cast<int32_t>(static_cast<int64_t>(a.vocab) * 5 / 8) : 0;
+}
+
 template <typename TI, typename TO>
 hipError_t sums(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
   const int32_t words = (a.width + Elem<TI>::kPer - 1) / Elem<TI>::kPer;
   const auto by_words = FastDiv::make(words);
   const auto unit_blocks = static_cast<int32_t>((static_cast<int64_t>(s.units) * words + 255) / 256);
-  // 64 KiB of the table a workgroup: its rows are searched for side by side
-  const int64_t row_bytes = static_cast<int64_t>(a.width) * static_cast<int64_t>(sizeof(TO));
-  const auto table_rows = static_cast<int32_t>(row_bytes >= 65536 ? 1 : row_bytes <= 256 ? 256 : 65536 / row_bytes);
-  const int64_t zero_blocks = a.accumulate ? 0 : (static_cast<int64_t>(a.vocab) + table_rows - 1) / table_rows;
-  const int64_t blocks = unit_blocks + zero_blocks;
+  const ZeroRows z = zero_rows(a, cleared_early(a), a.vocab, 65536, 256);  // rows are searched for side by side
+  const int64_t blocks = unit_blocks + zero_blocks(a, z);
   if (blocks > 0)
-    embed_sums_kernel<TI, TO><<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, s, words, by_words, unit_blocks,
-                                                                                 table_rows);
+    embed_sums_kernel<TI, TO><<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, s, words, by_words, unit_blocks, z);
   if (unit_blocks > 0 && s.units > 1)
     embed_join_kernel<TI, TO><<<unit_blocks, 256, 0, stream>>>(a, s, words, by_words);
   return hipGetLastError();
@@ -526,8 +585,7 @@ template <typename T>
 hipError_t lookup(const EmbedArgs& a, hipStream_t stream) {
   const int32_t words = (a.width + Elem<T>::kPer - 1) / Elem<T>::kPer;
   const int64_t blocks = (static_cast<int64_t>(a.rows) * words + 256 * kLookupEach - 1) / (256 * kLookupEach);
-  embed_kernel<T><<<static_cast<uint32_t>(blocks + (a.scan ? 1 : 0)), 256, 0, stream>>>(a, words,
-                                                                                        FastDiv::make(words), blocks);
+  embed_kernel<T><<<static_cast<uint32_t>(blocks + a.scan), 256, 0, stream>>>(a, words, FastDiv::make(words));
   return hipGetLastError();
 }
 
@@ -546,7 +604,7 @@ EmbedSort embed_sort(int64_t rows, int64_t vocab) {
     s.blocks = static_cast<int32_t>((tiles + s.turns - 1) / s.turns);
   }
   // long units have fewer borders; with few rows short ones give more threads
-  s.unit = rows < 65536 ? 32 : 64;
+  s.unit = rows <= kSortBlock ? 16 : rows < 65536 ? 32 : 64;
   s.units = static_cast<int32_t>((rows + s.unit - 1) / s.unit);
   return s;
 }
@@ -558,7 +616,8 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t stream) {
 
 hipError_t launch_embedding_sort(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
   if (a.rows <= kSortBlock) {
-    embed_sort_block_kernel<<<1, kSortThreads, 0, stream>>>(a, s);
+    const ZeroRows z = zero_rows(a, 0, cleared_early(a), 262144, 4096);
+    embed_sort_block_kernel<<<static_cast<uint32_t>(1 + zero_blocks(a, z)), kSortThreads, 0, stream>>>(a, s, z);
     return hipGetLastError();
   }
   const TokenRow* from = nullptr;

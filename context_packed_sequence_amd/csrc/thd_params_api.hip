@@ -211,7 +211,10 @@ int thd_embedding(const int64_t* ids, const uint8_t* mask, int64_t rows, const v
   a.dtype = dtype;
   a.scale = static_cast<float>(scale);
   a.status = status;
-  a.scan = status && rows > 0 && rows <= 8192;
+  // one workgroup looks through the ids beside the copy of the rows, which takes longer
+  // than that if rows are long, or there are few; else a launch clears the status first
+  const int64_t row_bytes = width * (dtype == THD_FP32 ? 4 : 2);
+  a.scan = status && rows > 0 && (rows <= 8192 || row_bytes >= 4096);
   if (status && !a.scan && thdcp::launch_status_init(status, as_stream(stream)) != hipSuccess) return THD_ERR_HIP;
   if (rows == 0) return THD_OK;
   return launched(thdcp::launch_embedding(a, as_stream(stream)));
