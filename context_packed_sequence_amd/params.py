@@ -15,11 +15,16 @@ it is done.
 
 from __future__ import annotations
 
+import operator
+
 import numpy as np
 import torch
 
 from . import binding as _b
 from .losses import _DTYPES, _F32, _I32, _I64, _U8, _address, _need_gpu, _run, _workspace
+
+_Tensor = torch.Tensor
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _matrix(x, name, width=None):
@@ -128,20 +133,22 @@ def embedding_backward(drows, ids, vocab, mask=None, scale=1.0, out=None, accumu
 
 def _tensors(tensors, name, device):
     """Host arrays (addresses, elements, types) of contiguous tensors on one device."""
-    dtypes = [x.dtype for x in tensors]
+    dtypes = list(map(_dtype_of, tensors))
     # one look at all of them; the one that is wrong is found only where there is one
     if not _DTYPES.keys() >= set(dtypes):
         i = next(i for i, d in enumerate(dtypes) if d not in _DTYPES)
         raise ValueError(f"{name}[{i}] must be bfloat16, float16 or float32, got {dtypes[i]}")
-    on = [x.get_device() for x in tensors]
+    on = list(map(_Tensor.get_device, tensors))
     if on.count(device) != len(on):
         i = next(i for i, d in enumerate(on) if d != device)
         raise ValueError(f"{name}[{i}] is on {tensors[i].device}, which is not the current device")
-    whole = [x.is_contiguous() for x in tensors]
+    whole = list(map(_Tensor.is_contiguous, tensors))
     if not all(whole):
         raise ValueError(f"{name}[{whole.index(False)}] must be contiguous")
-    return (np.array([x.data_ptr() for x in tensors], np.uint64), np.array([x.numel() for x in tensors], np.int64),
-            np.array([_DTYPES[d] for d in dtypes], np.int32))
+    n = len(dtypes)
+    return (np.fromiter(map(_Tensor.data_ptr, tensors), np.uint64, n),
+            np.fromiter(map(_Tensor.numel, tensors), np.int64, n),
+            np.fromiter(map(_DTYPES.__getitem__, dtypes), np.int32, n))
 
 
 def _gradients(grads):
