@@ -63,7 +63,12 @@ Layout layout(const thd_attention_shape& s, void* workspace, bool backward) {
   const int64_t nq = most_tiles(rows, (s.cp_size > 1 ? 2LL : 1LL) * s.n_slots,
                                 thdcp::kAttnRows / thdcp::attn_tile_heads(s.heads / s.kv_heads));
   const int64_t nk = backward ? most_tiles(s.total_tokens, s.n_slots, thdcp::kAttnKeys) : 0;
-  if ((nq + nk + 8) * s.heads > INT32_MAX) {
+  const int32_t group = s.heads / s.kv_heads;
+  l.key_parts = backward ? key_parts(s, nk) : 1;
+  // workgroups of 256 threads, which a launch counts in 32 bits
+  const int64_t query_blocks = (nq * s.kv_heads + 8) * (group / thdcp::attn_tile_heads(group));
+  const int64_t key_blocks = (nk * s.kv_heads + 8) * l.key_parts;
+  if (query_blocks + key_blocks > static_cast<int64_t>(UINT32_MAX / 256)) {
     l.bytes = -1;
     return l;
   }
@@ -80,7 +85,6 @@ Layout layout(const thd_attention_shape& s, void* workspace, bool backward) {
   if (backward) {
     l.plan.key_tiles = reinterpret_cast<thdcp::KeyTile*>(take(nk * static_cast<int64_t>(sizeof(thdcp::KeyTile))));
     l.plan.delta = reinterpret_cast<float*>(take(rows * s.heads * 4));
-    l.key_parts = key_parts(s, nk);
     if (l.key_parts > 1)
       l.plan.partial = reinterpret_cast<float*>(take(8 * l.key_parts * s.total_tokens * s.kv_heads * s.dim));
   }

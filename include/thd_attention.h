@@ -98,8 +98,10 @@ int thd_attention(const thd_attention_shape* shape, const thd_heads* q, const th
 /*
  * thd_attention_backward -- gradients of sum(dout * out) with respect to q, k and
  * v, with out and lse as thd_attention wrote them.  The gradients may be views of
- * one buffer whose rows interleave, as long as no two share an element.  Four
- * launches.
+ * one buffer whose rows interleave, as long as no two share an element.  Three
+ * launches, one more for THD_FP16, and one more where a group of heads is dealt out
+ * over workgroups (long documents, few key heads), with sums of its parts in the
+ * workspace.
  */
 int thd_attention_backward(const thd_attention_shape* shape, const thd_heads* q, const thd_heads* k,
                            const thd_heads* v, const thd_heads* out, const float* lse, const thd_heads* dout,

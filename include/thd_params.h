@@ -37,7 +37,7 @@ extern "C" {
  * elements apart (>= width); out: [rows][width] of the same dtype, rows `out_stride`
  * apart.  scale is finite in 32 bits.  An id that is no row of the table makes its
  * row NaN and the status word THD_ERR_TOKEN; without one it is THD_OK.  One launch,
- * and one before it for the status word above 8192 rows.
+ * and one before it for the status word above 8192 rows of less than 4096 bytes.
  */
 int thd_embedding(const int64_t* ids, const uint8_t* mask, int64_t rows, const void* table, int32_t dtype,
                   int64_t vocab, int64_t width, int64_t table_stride, double scale, void* out, int64_t out_stride,
@@ -46,15 +46,15 @@ int thd_embedding(const int64_t* ids, const uint8_t* mask, int64_t rows, const v
 /*
  * thd_embedding_workspace_bytes -- workspace of thd_embedding_backward, 16-byte
  * aligned: 16 bytes a row, partial sums of runs of one token that pass the borders of
- * 32 or 64 sorted rows (4 / 32 or 4 / 64 bytes times 2 for each element of drows), and
- * up to 0.5 MiB.  -1 for sizes the call refuses.  Host-only arithmetic.
+ * units of 16 to 128 sorted rows (8 bytes for each element of a row and unit), and up
+ * to 0.5 MiB.  -1 for sizes the call refuses.  Host-only arithmetic.
  */
 int64_t thd_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t width);
 
 /*
  * thd_embedding_backward -- dtable[v] = scale sum of drows[t] over the rows t with
- * ids[t] = v and mask not 0, in 32 bits in the rows' order within 32 or 64 of them,
- * those sums in order, rounded once.
+ * ids[t] = v and mask not 0, in 32 bits in the rows' order within units of 16 to 128
+ * sorted rows (the more rows, the longer), those sums in order, rounded once.
  *
  * drows: [rows][width] of dtype, rows `row_stride` elements apart; dtable:
  * [vocab][width] of out_dtype, which is dtype or THD_FP32, rows `table_stride` apart.
@@ -78,7 +78,8 @@ int64_t thd_gradients_workspace_bytes(int32_t n_tensors);
 
 /*
  * thd_gradient_norm -- *norm = |scale| sqrt(sum of the squares of all elements of all
- * tensors), summed in 64 bits.
+ * tensors): squares of 16 bytes of elements summed in 32 bits (in 64 where 32 cannot
+ * hold them), those sums in 64.
  *
  * grads, elements, dtypes: host arrays of n_tensors entries (0 to THD_MAX_TENSORS):
  * device address, number of elements (0 and up) and element type of each contiguous
@@ -102,7 +103,7 @@ int thd_gradient_norm(const void* const* grads, const int64_t* elements, const i
  * THD_FP32.  An output may be its own gradient of the same type (scaled in place; with
  * f = 1 it is left alone); any other overlap is THD_ERR_ALIAS.  max_norm > 0 (infinite:
  * f = scale), scale finite in 32 bits.  Two launches for each 96 tensors, one with
- * norm_in.
+ * norm_in, and one between for more than 64 MiB.
  */
 int thd_clip_gradients(const void* const* grads, void* const* outs, const int64_t* elements, const int32_t* dtypes,
                        const int32_t* out_dtypes, int32_t n_tensors, double max_norm, double scale,

@@ -237,6 +237,25 @@ def test_same_bits_every_time(torch, thd, dtype):
             assert torch.equal(x, y)
 
 
+# few slots and many of a plan's tables; 4096 boundaries fit its shared memory
+@pytest.mark.parametrize("slots", [4095, 4096, 4097, 9000])
+def test_many_slots(torch, thd, slots):
+    say("attention slots", slots)
+    lens = np.zeros(slots, dtype=np.int64)
+    lens[[0, 7, slots // 2, slots - 2]] = [40, 129, 70, 1]
+    real = lens.copy()
+    real[7] = 120
+    _check(thd, Batch(torch, list(lens), list(real), heads=2, kv_heads=1), "slots")
+
+
+# a group's heads in 1, 2, 3 and 8 parts
+@pytest.mark.parametrize("heads,kv_heads,lens", [(128, 32, [300]), (96, 32, [300]), (8, 1, [300]), (8, 2, [20] * 12)])
+def test_parts_of_a_group(torch, thd, heads, kv_heads, lens):
+    say("attention parts", heads, kv_heads, lens)
+    for cap in (0.0, 4.0):
+        _check(thd, Batch(torch, lens, [n - 3 for n in lens], heads=heads, kv_heads=kv_heads, dim=32, cap=cap), "parts")
+
+
 BAD = [([1, 4, 8], None, -10), ([0, 6, 4, 8], None, -11), ([0, 4, 7], None, -12), ([0, 4, 8], [0, 5, 8], -14),
        ([0, 4, 8], [0, 4, 3], -11), ([0, 4, 8], [1, 4, 8], -10)]
 

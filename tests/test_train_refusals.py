@@ -27,7 +27,8 @@ SHAPE = dict(dtype=thd.THD_BF16, heads=4, kv_heads=2, dim=64, causal=1, window=0
 BAD_SHAPES = [dict(dtype=thd.THD_FP32), dict(dtype=-1), dict(heads=3), dict(heads=0), dict(kv_heads=0), dict(dim=0),
               dict(dim=12), dict(dim=136), dict(causal=2), dict(window=-1), dict(cp_size=0), dict(rank=1),
               dict(rank=-1), dict(cp_size=thd.THD_MAX_CP + 1), dict(n_slots=-1), dict(total_tokens=-1),
-              dict(total_tokens=2 ** 31), dict(total_tokens=65, cp_size=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=1e-39),
+              dict(total_tokens=2 ** 31), dict(total_tokens=65, cp_size=2), dict(scale=0.0), dict(scale=-1.0),
+              dict(scale=1e-39), dict(total_tokens=2 ** 31 - 1, heads=16, kv_heads=16, dim=8),
               dict(scale=float("inf")), dict(scale=float("nan")), dict(cap=-1.0), dict(cap=float("inf")),
               dict(cap=float("nan")), dict(cap=1e-60), dict(scale=1e-30, cap=1e30), dict(scale=1e30, cap=1e-30)]
 
