@@ -10,7 +10,18 @@
 // would change the results.  Both hold a wave's own 32 rows (queries and dout, or
 // keys and values) in registers as B operands, so that p and dz come out of the
 // products as operands of the next ones, and move the other side's rows
-// through LDS, 64 at a time.
+// through LDS.  p and dz are rounded to the tensors' type as factors of those
+// products; with delta from the rounded out that makes dq and dk differ from the
+// formulas by about 1.6 roundings of their own elements (root mean square, bf16 2.8e-3
+// of the values; rounding the exact gradients alone 1.7e-3).
+//
+// bf16 takes delta in the query gradients' kernel, which runs first and leaves it for
+// the key gradients: a launch and a reading of dout less (16384 tokens of short
+// documents, 32 heads of 128: 54 us of 446).
+//
+// Bound as the forward pass is; one document of 8192 tokens, causal, 32 heads of 128
+// over 8: dq 713 us (1157 TFLOP/s, matrix units busy 61 %), dk and dv 996 (1104, 53 %)
+// and 70 to add up their parts; with a cap 888 and 1202.
 //
 // fp16: p times 2^10 and dz times a power of two for which no dz passes the
 // type's range (from the largest norms of a dout row and of a v row) keep small
@@ -172,8 +183,8 @@ __device__ __forceinline__ void row_products(const char* x, const char* y, int32
   }
 }
 
-// Query gradients: 128 query rows of one head a workgroup, as in the forward
-// pass.
+// Query gradients: 128 query rows a workgroup, as in the forward pass; 64 keys at a
+// time, of which two workgroups' tiles fill a compute unit's LDS.
 template <typename T, int kDim, bool kCap>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
   constexpr int kTile = kAttnStep * kRowBytes<kDim>;
@@ -515,7 +526,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnArgs a) {
 }
 
 // Sums of the parts, in order, rounded once: 16 threads a row of a head, eight elements
-// a thread.
+// a thread.  Memory: 8192 tokens, 8 key heads of 128, four parts 70 us (4.3 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (a.plan.header[kAttnCode] != THD_OK) return;

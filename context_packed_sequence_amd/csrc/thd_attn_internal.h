@@ -16,7 +16,8 @@ constexpr int kAttnStep = 64;    // keys (or query rows) that a workgroup moves 
 
 // Heads of a group whose queries a workgroup takes together, the same rows of each: its
 // waves then walk through the same keys to the same end, and a tile of few rows ends
-// nearer to the diagonal and to the document's end.
+// nearer to the diagonal and to the document's end (16384 tokens of short documents, 32
+// heads over 8: forward 157 -> 123 us, dq 212 -> 173).
 constexpr int32_t attn_tile_heads(int32_t group) { return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
 
 // Query rows of one workgroup: a run of rows of one document's share.  Rows

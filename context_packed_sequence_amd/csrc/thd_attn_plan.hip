@@ -7,8 +7,9 @@
 // most keys to look at first: the last workgroups to run are then the lightest.
 // A tile's weight is held to 8 steps per power of two, and tiles of equal weight
 // go where an LDS counter says, so their order may differ from run to run; a
-// tile's result does not depend on its place.  5-6 us for a few hundred slots or
-// a thousand tiles.
+// tile's result does not depend on its place.  Latency, of loads and barriers: 4 us
+// for one document of 8192 tokens, 8 for 16384 tokens of short documents, 9 for 32768
+// (with the boundaries in memory 12 and more).
 #include "thd_attn_device.h"
 
 namespace thdcp {
