@@ -178,12 +178,10 @@ AttnArgs arguments(const thd_attention_shape& s, const Layout& l) {
   a.cap = static_cast<float>(s.cap);
   a.plan = l.plan;
   a.curve_limit = -1.0f;
-  const double in = s.scale / s.cap;
-  if (s.cap > 0.0 && in >= 0x1p-12 && in <= 0x1p12 && s.scale >= 0x1p-24 && s.scale <= 0x1p24) {
-    // tanh(x) / x on [-1/2, 1/2], minimax in x^2: off by 1.5e-8 before rounding
-    constexpr double kTanh[5] = {1.0, -0.33333144, 0.13325879, -0.05304552, 0.01724153};
+  const double in = s.cap > 0.0 ? s.scale / s.cap : 0.0;
+  if (in >= 0x1p-12 && in <= 0x1p12 && s.scale >= 0x1p-24 && s.scale <= 0x1p24) {
     double c = s.scale * 1.4426950408889634;
-    for (int i = 0; i < 5; ++i, c *= in * in) a.curve[i] = static_cast<float>(c * kTanh[i]);
+    for (int i = 0; i < 5; ++i, c *= in * in) a.curve[i] = static_cast<float>(c * thdcp::kAttnTanh[i]);
     a.curve_limit = static_cast<float>(0.5 / in);
   }
   return a;

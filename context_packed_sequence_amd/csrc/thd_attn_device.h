@@ -86,10 +86,10 @@ __device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_ex
 
 // Capped scores in powers of two: s = cap log2(e) tanh(scale s / cap), element by
 // element.  Scores are mostly well below their cap, and up to half of it s times an even
-// polynomial, whose coefficients hold all the factors, takes six instructions an element
-// where 1 - 2 / (1 + e^(2x)) takes two of a quarter of their rate; it also keeps its
-// relative precision near 0, where the other form is off by up to 2^-23 of the cap.
-// Taken where no lane's score is larger.
+// polynomial, whose coefficients hold all the factors, takes six instructions an element;
+// it also keeps its relative precision near 0, where 1 - 2 / (1 + e^(2x)) is off by up to
+// 2^-23 of the cap.  Where a lane's score is larger, or the factors' powers do not fit 32
+// bits, each element takes one of the two by its size.
 __device__ __forceinline__ void attn_capped(const AttnArgs& a, F32x16& s) {
   float top = fmaxf(fabsf(s[0]), fabsf(s[1]));
 #pragma unroll
@@ -106,10 +106,18 @@ __device__ __forceinline__ void attn_capped(const AttnArgs& a, F32x16& s) {
     }
     return;
   }
-  const float most = a.cap * kAttnLog2e, in = 2.0f * kAttnLog2e * (a.scale / a.cap);
+  const float most = a.cap * kAttnLog2e, in = a.scale / a.cap, slope = a.scale * kAttnLog2e;
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
-    s[r] = fmaf(-2.0f * most, __builtin_amdgcn_rcpf(1.0f + attn_exp2(s[r] * in)), most);
+  for (int r = 0; r < 16; ++r) {
+    if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // few registers at a time
+    const float x = s[r] * in, u = x * x;
+    float p = fmaf(u, kAttnTanh[4], kAttnTanh[3]);
+    p = fmaf(u, p, kAttnTanh[2]);
+    p = fmaf(u, p, kAttnTanh[1]);
+    p = fmaf(u, p, 1.0f);
+    const float large = fmaf(-2.0f * most, __builtin_amdgcn_rcpf(1.0f + attn_exp2(x * (2.0f * kAttnLog2e))), most);
+    s[r] = fabsf(x) <= 0.5f ? s[r] * slope * p : large;
+  }
 }
 
 // Value of lane l ^ 32, combined.

@@ -20,6 +20,9 @@ constexpr int kAttnStep = 64;    // keys (or query rows) that a workgroup moves 
 // heads over 8: forward 157 -> 123 us, dq 212 -> 173).
 constexpr int32_t attn_tile_heads(int32_t group) { return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
 
+// tanh(x) / x on [-1/2, 1/2] as a polynomial in x^2, minimax: off by 1.5e-8 before rounding.
+constexpr float kAttnTanh[5] = {1.0f, -0.33333144f, 0.13325879f, -0.05304552f, 0.01724153f};
+
 // Query rows of one workgroup: a run of rows of one document's share.  Rows
 // [valid, rows) are pads.
 struct QueryTile {

@@ -153,6 +153,35 @@ def test_masks(torch, thd, causal, window, cap):
     _check(thd, b, "masks")
 
 
+@pytest.mark.parametrize("dim", [32, 80, 96, 128])
+@pytest.mark.parametrize("how", [dict(window=40), dict(window=129, cap=1.5), dict(causal=False, cap=0.7),
+                                 dict(causal=False, window=70)])
+def test_masks_of_head_sizes(torch, thd, dim, how):
+    say("attention masks of head sizes", dim, how)
+    _check(thd, Batch(torch, [170, 33], [161, 33], heads=4, kv_heads=2, dim=dim, **how), "masks")
+    _check(thd, Batch(torch, [260, 40], [251, 36], heads=2, kv_heads=2, dim=dim, dtype="fp16", cp=2, rank=1, **how),
+           "masks")
+
+
+# caps far above and far below the scores, and among them
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 8.0, 3e3, 1e6, 1e30])
+@pytest.mark.parametrize("spread", [1.0, 8.0])
+def test_caps(torch, thd, cap, spread):
+    say("attention cap", cap, spread)
+    _check(thd, Batch(torch, [140], heads=2, dim=64, cap=cap, spread=spread), "cap")
+
+
+@pytest.mark.parametrize("cap", [3e3, 1e6, 1e30])
+def test_far_cap_changes_nothing(torch, thd, cap):
+    # z - cap tanh(z / cap) is below |z|^3 / (3 cap^2): with |z| up to 8, 2e-5 for a cap of 3000
+    say("attention far cap", cap)
+    b = Batch(torch, [140], heads=2, dim=64)
+    want, bound = b.expected(grad=False)["lse"]
+    b.how["cap"] = cap
+    assert np.abs(want).max() < 8
+    _within(b.forward(thd)[1], want, bound + 8 ** 3 / (3 * cap ** 2), "lse")
+
+
 @pytest.mark.parametrize("cp", [2, 4, 8])
 @pytest.mark.parametrize("how", [dict(), dict(causal=False), dict(window=50, cap=5.0)])
 def test_zigzag_shares(torch, thd, cp, how):
