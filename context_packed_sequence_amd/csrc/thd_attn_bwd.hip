@@ -11,9 +11,10 @@
 // keys and values) in registers as B operands, so that p and dz come out of the
 // products as operands of the next ones, and move the other side's rows
 // through LDS.  p and dz are rounded to the tensors' type as factors of those
-// products; with delta from the rounded out that makes dq and dk differ from the
-// formulas by about 1.6 roundings of their own elements (root mean square, bf16 2.8e-3
-// of the values; rounding the exact gradients alone 1.7e-3).
+// products; with delta from the rounded out (of rows with more keys than a block) that
+// makes dq and dk differ from the formulas by about 1.6 roundings of their own elements
+// (root mean square, bf16 2.7e-3 of the values; rounding the exact gradients alone
+// 1.7e-3).
 //
 // bf16 takes delta in the query gradients' kernel, which runs first and leaves it for
 // the key gradients: a launch and a reading of dout less (16384 tokens of short
@@ -110,6 +111,19 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnArgs a, int32_t que
     if (most > 0.0f)
       atomicMax(a.plan.header + (query ? kAttnMaxGrad : kAttnMaxValue), __builtin_bit_cast(int32_t, most));
   }
+}
+
+// Sum of p dp over a block of scores (keys are registers), for both halves of a wave.
+template <bool kCap, typename Visible>
+__device__ __forceinline__ float block_delta(const AttnArgs& a, F32x16 s, const F32x16& dp, float lse,
+                                             Visible visible) {
+  const float factor = kCap ? 1.0f : a.scale * kAttnLog2e;
+  if constexpr (kCap) attn_capped(a, s);
+  float sum = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    if (visible(r)) sum = fmaf(attn_exp2(fmaf(s[r], factor, -lse)), dp[r], sum);
+  return add_halves(sum);
 }
 
 // What both kernels make of a block of scores and dp (32 x 32, one row a
@@ -240,6 +254,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
     RowsWalk keys(a.k, static_cast<int64_t>(tile.doc) + key, place.kv_head, tile.real - key);
     RowsWalk values(a.v, static_cast<int64_t>(tile.doc) + key, place.kv_head, tile.real - key);
     const KeySteps steps(a, pos, 32, own.valid, tile.real);
+    // Rows of which all keys stand in one block take delta from it, not from the rounded
+    // out: with few keys dp - delta is a small difference of large numbers.
+    const int32_t only = (max(steps.any, 0) + 31) & ~31;
+    const bool alone = only + 32 >= steps.any_end;
     const auto load = [&](int32_t to) {
       keys.load<kDim, kAttnStep>(s_tiles + to, a.dim);
       values.load<kDim, kAttnStep>(s_tiles + to + kTile, a.dim);
@@ -256,13 +274,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
         row_products<T, kDim>(s_tiles + now + skip, s_tiles + now + kTile + skip, row_at, q, g, s, dp);
         U32x4 p16[2], dz16[2];
         const bool all = k0 >= steps.all && k0 < steps.all_end;
+        const auto sees = [&](int r) { return seen(k0 + 4 * h + (r & 3) + 8 * (r >> 2)); };
+        if (alone) {
+          delta = block_delta<kCap>(a, s, dp, lse, sees);
+          if (l < own.valid) a.plan.delta[static_cast<int64_t>(own.head) * a.rows + tile.row + own.first + l] = delta;
+        }
         const auto lane_lse = [&](int) { return lse; };
         const auto lane_delta = [&](int) { return delta; };
         if (all)
           score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta, [](int) { return true; }, p16, dz16);
         else
-          score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta,
-                                   [&](int r) { return seen(k0 + 4 * h + (r & 3) + 8 * (r >> 2)); }, p16, dz16);
+          score_gradients<T, kCap>(a, s, dp, held, lane_lse, lane_delta, sees, p16, dz16);
         U32x4 f[kDim / 32][2];
         read_columns<kDim, now>(column_at[0] + skip, column_at[1] + skip, f);
         add_columns<T, kDim>(dq, f, dz16);
@@ -277,8 +299,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
     }
     __syncthreads();
   }
-  store_rows<T, kDim>(s_tiles + wave * kTile, dq, a.scale / held, const_cast<char*>(head_rows(a.dq, tile.row + own.first, own.head)),
-                      2 * a.dq.row, own.rows, own.valid, a.dim);
+  store_rows<T, kDim>(s_tiles + wave * kTile, dq, a.scale / held,
+                      const_cast<char*>(head_rows(a.dq, tile.row + own.first, own.head)), 2 * a.dq.row, own.rows,
+                      own.valid, a.dim);
 }
 
 // The query rows that a key tile's gradients come from: for each of the workgroup's

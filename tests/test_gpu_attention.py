@@ -182,6 +182,28 @@ def test_far_cap_changes_nothing(torch, thd, cap):
     _within(b.forward(thd)[1], want, bound + 8 ** 3 / (3 * cap ** 2), "lse")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+def test_documents_of_one_token(torch, thd, dtype, cap):
+    # dz = p dp (1 - p) with p = exp(z - lse) off by r_p from 1, where the formula's is 0; a
+    # delta from the rounded out would be off by w |dout| |v|, hundreds of times as much
+    say("attention documents of one token", dtype, cap)
+    b = Batch(torch, [1] * 40, heads=3, kv_heads=3, dim=128, dtype=dtype, cap=cap)
+    out, lse, _ = b.forward(thd)
+    dq, dk, _, _ = b.backward(thd, out, lse)
+    q, k, v, d = (np.abs(_host(x)) for x in (b.q, b.k, b.v, b.dout))
+    scale, u = 128 ** -0.5, 2.0 ** -24
+    e_z = (128 + 4) * u * scale * (q * k).sum(-1, keepdims=True) + 8 * u * cap
+    e_z = e_z + 4 * u * np.abs(_host(lse)).T[:, :, None]
+    bound = 1.02 * (2 * e_z + 17 * u) * scale * (d * v).sum(-1, keepdims=True)
+    # fp16: dz is held to 2^-38 of 2 max |dout| max |v|, and dq's and dk's smallest step is 2^-24
+    top = 2 * np.linalg.norm(d, axis=-1).max() * np.linalg.norm(v, axis=-1).max()
+    bound += 2.0 ** -38 * top if dtype == "fp16" else 0.0
+    tiny = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -126
+    _within(dq, np.zeros(dq.shape), bound * k + tiny, "dq")
+    _within(dk, np.zeros(dk.shape), bound * q + tiny, "dk")
+
+
 @pytest.mark.parametrize("cp", [2, 4, 8])
 @pytest.mark.parametrize("how", [dict(), dict(causal=False), dict(window=50, cap=5.0)])
 def test_zigzag_shares(torch, thd, cp, how):
