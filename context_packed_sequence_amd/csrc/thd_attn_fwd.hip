@@ -11,9 +11,15 @@
 // most half a step of each, while their sum is held in 32 bits), are the second
 // product's operand as they lie (O^T += V^T P^T, V read transposed).
 //
-// The output is rescaled only when some row's maximum grew by more than 2^8 since
-// the reference it is relative to: probabilities up to 256 lose nothing in 32-bit
-// sums, nor rounded to 16 bits.
+// Probabilities are held relative to a reference of their row, and the output is
+// rescaled only when some row's maximum grew by more than 2^8 beyond it: numbers up to
+// 256 lose nothing in 32-bit sums, nor rounded to bf16.  fp16 has few exponents below 1:
+// there the reference stands 2^9 below the maximum it was taken from, and may be
+// outgrown by 2^6 more, which stays below the type's end.  Probabilities down to 2^-23 of
+// that maximum keep all their bits, those down to 2^-34 some (without the 2^9, 2^-14 and
+// 2^-25: a key 16 e-folds above all others and of value 0 put its row off by 6 %).
+// 8192 tokens, 32 heads of 128 over 8, causal, fp16: 566 us against 563 without, 575 with
+// 2^13 and 2^2.
 //
 // Bound by the matrix units and the vector units together, which hardly overlap: one
 // document of 8192 tokens, causal, 32 heads over 8, takes 524 us with heads of 128 (1050
@@ -26,7 +32,12 @@ namespace thdcp {
 
 namespace {
 
-constexpr float kGrowth = 8.0f;  // in powers of two
+// In powers of two: how far above a row's reference the maximum stands when it is taken,
+// and how much further it may grow.
+template <typename T>
+constexpr float kLift = T::kNarrow ? 9.0f : 0.0f;
+template <typename T>
+constexpr float kGrowth = T::kNarrow ? 6.0f : 8.0f;
 
 template <typename T, int kDim, bool kCap>
 struct ForwardWave {
@@ -78,8 +89,8 @@ struct ForwardWave {
 #pragma unroll
     for (int r = 2; r < 16; r += 2) m = fmaxf(fmaxf(m, s[r]), s[r + 1]);
     m = max_halves(m) * factor;
-    if (__any(m > top + kGrowth)) {
-      const float to = fmaxf(top, m);
+    if (__any(m > top + (kLift<T> + kGrowth<T>))) {
+      const float to = fmaxf(top, m - kLift<T>);
       const float shrink = to == -kAttnInf ? 1.0f : attn_exp2(top - to);
       top = to;
       sum *= shrink;

@@ -1,0 +1,63 @@
+"""Attention where fp16 has few exponents to spare: rows with one key far above the
+others, and long documents, against closed forms and the oracle (64 bits)."""
+
+import math
+
+import numpy as np
+import pytest
+
+from gpu_util import dev_i32, say
+from test_gpu_attention import Batch, _host, _within, thd, torch  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+# half the smallest step of a probability, of the row's largest: fp16's 2^-25 over the 2^9 it is held with
+FLOOR = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -34}
+TINY = {"bf16": 2.0 ** -133, "fp16": 2.0 ** -25}
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [10, 12, 14, 15, 16, 17, 18, 20])
+@pytest.mark.parametrize("n", [40, 4000, 20000])
+@pytest.mark.parametrize("place", ["first", "last"])
+def test_one_strong_key(torch, thd, n, gap, dtype, place):
+    # z is `gap` for one key of value 0, and 0 for n - 1 keys of value 1:
+    # out = (n - 1) / (n - 1 + e^gap)
+    say("attention one strong key", n, gap, dtype, place)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    q = torch.zeros((n, 1, 64), device="cuda", dtype=dt)
+    k, v = torch.zeros_like(q), torch.ones_like(q)
+    at = 0 if place == "first" else n - 1
+    q[:, :, 0], k[at, :, 0], v[at] = 8.0, float(gap), 0.0
+    out, lse, status = thd.packed_attention(q, k, v, dev_i32([0, n]), causal=False)
+    assert int(status) == 0
+    total = n - 1 + math.exp(gap)
+    want, true_lse = (n - 1) / total, math.log(total)
+    # roundings as counted in attention_bounds.py; p of the largest key is at most 1
+    e_z = (64 + 4) * U * gap + 4 * U * gap
+    r_p = 2 * e_z + (n + 16) * U
+    bound = (HALF[dtype] + r_p + n * U) * want + (n - 1) * FLOOR[dtype] + HALF[dtype] * want + TINY[dtype]
+    _within(out, np.full(out.shape, want), np.full(out.shape, bound), "out")
+    _within(lse, np.full(lse.shape, true_lse), np.full(lse.shape, e_z + (n + 16) * U + 4 * U * true_lse), "lse")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("tokens,heads,dim,spread", [(4099, 2, 64, 1.0), (2500, 1, 128, 3.0)])
+def test_long_document(torch, thd, tokens, heads, dim, spread, dtype):
+    # hundreds of steps of the running softmax, and of both walks of the gradients
+    say("attention of a long document", tokens, heads, dim, spread, dtype)
+    b = Batch(torch, [tokens + 13], [tokens], heads=heads, kv_heads=1, dim=dim, dtype=dtype, spread=spread)
+    out, lse, status = b.forward(thd)
+    dq, dk, dv, status2 = b.backward(thd, out, lse)
+    assert int(status) == 0 and int(status2) == 0
+    want = b.expected()
+    for name, x in zip(("lse", "dq", "dk", "dv"), (lse, dq, dk, dv)):
+        _within(x, *want[name], f"long {name}")
+    # fp16: attention_bounds allows each probability 2^-25 of the row's largest; 2^-34 is what is lost
+    value, bound = want["out"]
+    if dtype == "fp16":
+        seen = np.cumsum(np.abs(np.nan_to_num(_host(b.v))), 0).repeat(heads, 1)
+        bound = bound - np.where(b.live[:, None, None], (2.0 ** -25 - FLOOR[dtype]) * seen, 0.0)
+    _within(out, value, bound, "long out")
