@@ -24,7 +24,7 @@
 // over 8: dq 713 us (1157 TFLOP/s, matrix units busy 61 %), dk and dv 996 (1104, 53 %)
 // and 70 to add up their parts; with a cap 888 and 1202.
 //
-// fp16: p times 2^10 and dz times a power of two for which no dz passes the
+// fp16: p times 2^14 and dz times a power of two for which no dz passes the
 // type's range (from the largest norms of a dout row and of a v row) keep small
 // factors out of the subnormals; the sums are scaled back.
 #include "thd_attn_device.h"
@@ -33,7 +33,9 @@ namespace thdcp {
 
 namespace {
 
-constexpr float kProbabilityScale = 1024.0f;  // of fp16 probabilities
+// Of fp16 probabilities, which are 1 at most but for the roundings of their scores: the
+// type ends below 2^16.  Those from 2^-28 on keep all their bits.
+constexpr float kProbabilityScale = 16384.0f;
 
 // Power of two by which fp16 score gradients are held: |dz| <= 2 |dout| |v|.
 __device__ __forceinline__ float gradient_scale(const AttnPlan& p) {

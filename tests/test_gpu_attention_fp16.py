@@ -61,3 +61,25 @@ def test_long_document(torch, thd, tokens, heads, dim, spread, dtype):
         seen = np.cumsum(np.abs(np.nan_to_num(_host(b.v))), 0).repeat(heads, 1)
         bound = bound - np.where(b.live[:, None, None], (2.0 ** -25 - FLOOR[dtype]) * seen, 0.0)
     _within(out, value, bound, "long out")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [12, 16, 18, 20])
+def test_gradient_of_weak_values(torch, thd, gap, dtype):
+    # the same keys, dout 1 in every row: dv of a weak key is n / (n - 1 + e^gap)
+    n = 20000
+    say("attention gradient of weak values", n, gap, dtype)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    q = torch.zeros((n, 1, 64), device="cuda", dtype=dt)
+    k, v = torch.zeros_like(q), torch.ones_like(q)
+    q[:, :, 0], k[0, :, 0], v[0] = 8.0, float(gap), 0.0
+    cu = dev_i32([0, n])
+    out, lse, _ = thd.packed_attention(q, k, v, cu, causal=False)
+    *_, dv, status = thd.packed_attention_backward(torch.ones_like(q), q, k, v, out, lse, cu, causal=False)
+    assert int(status) == 0
+    want = n / (n - 1 + math.exp(gap))
+    r_p = 2 * ((64 + 4) * U * gap + 4 * U * gap) + (n + 16) * U
+    # p is held times 2^14: half of fp16's smallest step is 2^-39 of it
+    floor = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -39}[dtype]
+    bound = (HALF[dtype] + r_p + n * U) * want + n * floor + HALF[dtype] * want + TINY[dtype]
+    _within(dv[1:], np.full((n - 1, 1, 64), want), np.full((n - 1, 1, 64), bound), "dv")
