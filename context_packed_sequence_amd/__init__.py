@@ -42,6 +42,7 @@ from .binding import (  # noqa: F401
     THD_ERR_SHAPE,
     THD_ERR_TOKEN,
     THD_BF16,
+    THD_CAP_LOG2,
     THD_FP16,
     THD_FP32,
     THD_IDENTITY,
@@ -53,6 +54,7 @@ from .binding import (  # noqa: F401
     THD_MAX_VOCAB,
     THD_MAX_WIDTH,
     THD_PACK_MAX_SEQ,
+    THD_SCALE_LOG2,
     THD_MAX_CP,
     THD_MAX_SHIFT,
     THD_OK,

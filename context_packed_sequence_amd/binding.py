@@ -67,6 +67,8 @@ THD_MAX_VOCAB = 268435456
 THD_MAX_TOPK = 256
 THD_MAX_PAIRS = 65536
 THD_MAX_HEAD_DIM = 128
+THD_SCALE_LOG2 = 100
+THD_CAP_LOG2 = 64
 THD_MAX_WIDTH = 1048576
 THD_MAX_TENSORS = 65536
 

@@ -19,10 +19,13 @@ bool shape_ok(const thd_attention_shape* s) {
   if (s->cp_size < 1 || s->cp_size > THD_MAX_CP || s->rank < 0 || s->rank >= s->cp_size) return false;
   if (s->n_slots < 0 || s->n_slots == INT32_MAX || s->total_tokens < 0 || s->total_tokens > INT32_MAX) return false;
   if (s->total_tokens % s->cp_size != 0) return false;
+  // In 32 bits lse / scale has to be finite, products may end at 2^-126, which times scale
+  // has to be nothing, and the gradients take up to 2^30 / cap and log2(e) cap.
   const auto scale = static_cast<float>(s->scale), cap = static_cast<float>(s->cap);
-  if (!(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f) || !std::isfinite(1.0f / scale)) return false;
-  if (!(s->cap >= 0.0) || (s->cap > 0.0 && !(cap > 0.0f)) || !std::isfinite(cap * 1.4426950408889634f)) return false;
-  return !(cap > 0.0f) || (std::isfinite(scale / cap) && scale / cap > 0.0f);
+  if (!(scale >= std::ldexp(1.0f, -THD_SCALE_LOG2)) || !(scale <= std::ldexp(1.0f, THD_SCALE_LOG2))) return false;
+  if (s->cap == 0.0) return true;
+  if (!(cap >= std::ldexp(1.0f, -THD_CAP_LOG2)) || !std::isfinite(cap * 1.4426950408889634f)) return false;
+  return std::isfinite(scale / cap) && scale / cap > 0.0f;
 }
 
 int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }

@@ -57,6 +57,8 @@ extern "C" {
 #endif
 
 #define THD_MAX_HEAD_DIM 128
+#define THD_SCALE_LOG2   100   /* scales are 2^-100 to 2^100 */
+#define THD_CAP_LOG2     64    /* caps are 2^-64 and up */
 
 /* One tensor: device address, elements from row to row and from head to head. */
 typedef struct thd_heads {
@@ -74,8 +76,9 @@ typedef struct thd_attention_shape {
   int32_t cp_size, rank;
   int32_t n_slots;
   int64_t total_tokens;
-  double scale;        /* > 0, finite in 32 bits, as its reciprocal */
-  double cap;          /* 0: none; else > 0, finite in 32 bits */
+  double scale;        /* 2^-THD_SCALE_LOG2 to 2^THD_SCALE_LOG2 */
+  double cap;          /* 0: none; else from 2^-THD_CAP_LOG2 on; 1.45 cap and scale / cap finite in
+                          32 bits, scale / cap not 0 there */
   const int32_t* cu_seqlens_padded;
   const int32_t* cu_seqlens;
 } thd_attention_shape;
