@@ -49,6 +49,7 @@ from .binding import (  # noqa: F401
     THD_MAX_BATCH,
     THD_MAX_HEAD_DIM,
     THD_MAX_PAIRS,
+    THD_MAX_STREAM,
     THD_MAX_TENSORS,
     THD_MAX_TOPK,
     THD_MAX_VOCAB,

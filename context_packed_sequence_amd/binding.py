@@ -67,6 +67,7 @@ THD_MAX_VOCAB = 268435456
 THD_MAX_TOPK = 256
 THD_MAX_PAIRS = 65536
 THD_MAX_HEAD_DIM = 128
+THD_MAX_STREAM = 2147418112
 THD_SCALE_LOG2 = 100
 THD_CAP_LOG2 = 64
 THD_MAX_WIDTH = 1048576

@@ -17,7 +17,9 @@ bool shape_ok(const thd_attention_shape* s) {
   if (s->dim < 8 || s->dim > THD_MAX_HEAD_DIM || s->dim % 8 != 0) return false;
   if ((s->causal != 0 && s->causal != 1) || s->window < 0) return false;
   if (s->cp_size < 1 || s->cp_size > THD_MAX_CP || s->rank < 0 || s->rank >= s->cp_size) return false;
-  if (s->n_slots < 0 || s->n_slots == INT32_MAX || s->total_tokens < 0 || s->total_tokens > INT32_MAX) return false;
+  // positions run a tile past the last token, and a window before the first, in 32 bits
+  if (s->n_slots < 0 || s->n_slots == INT32_MAX) return false;
+  if (s->total_tokens < 0 || s->total_tokens > THD_MAX_STREAM) return false;
   if (s->total_tokens % s->cp_size != 0) return false;
   // In 32 bits lse / scale has to be finite, products may end at 2^-126, which times scale
   // has to be nothing, and the gradients take up to 2^30 / cap and log2(e) cap.

@@ -57,6 +57,7 @@ extern "C" {
 #endif
 
 #define THD_MAX_HEAD_DIM 128
+#define THD_MAX_STREAM   2147418112 /* tokens: 2^31 - 2^16 */
 #define THD_SCALE_LOG2   100   /* scales are 2^-100 to 2^100 */
 #define THD_CAP_LOG2     64    /* caps are 2^-64 and up */
 
@@ -75,7 +76,7 @@ typedef struct thd_attention_shape {
   int32_t window;      /* 0: none */
   int32_t cp_size, rank;
   int32_t n_slots;
-  int64_t total_tokens;
+  int64_t total_tokens; /* up to THD_MAX_STREAM */
   double scale;        /* 2^-THD_SCALE_LOG2 to 2^THD_SCALE_LOG2 */
   double cap;          /* 0: none; else from 2^-THD_CAP_LOG2 on; 1.45 cap and scale / cap finite in
                           32 bits, scale / cap not 0 there */

@@ -24,3 +24,14 @@ def test_scales_without_room(lib, bad):
 def test_scales_with_room(lib, good):
     for backward in (0, 1):
         assert lib.thd_attention_workspace_bytes(ctypes.byref(_shape(**good)), backward) > 0
+
+
+def test_longest_stream(lib):
+    # a key position passes the last token by up to a tile, and a row's window starts before the
+    # first: both have to fit 32 bits
+    how = dict(heads=1, kv_heads=1, dim=8, cp_size=2, window=64)
+    shape = lambda n: ctypes.byref(_shape(total_tokens=n, **how))  # noqa: E731
+    assert lib.thd_attention_workspace_bytes(shape(thd.THD_MAX_STREAM), 0) > 0
+    for n in (thd.THD_MAX_STREAM + 2, 2 ** 31 - 64, 2 ** 31 - 4):
+        assert lib.thd_attention_workspace_bytes(shape(n), 0) == -1
+        assert _attention(lib, _shape(total_tokens=n, **how)) == thd.THD_ERR_ARG
