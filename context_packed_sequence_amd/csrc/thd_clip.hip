@@ -195,11 +195,25 @@ __global__ __launch_bounds__(kClipThreads) void norm_finish_kernel(ClipArgs c) {
   finish_norm(c, norm_of(c, s_wave));
 }
 
+// What gradients are multiplied by, rounded once from 64 bits: below 2^-126, where 32 bits
+// have no room for a factor of 24 bits, a number from 1/2 to 1 and a power of two, else the
+// factor itself and 2^0.
+struct Factor {
+  float f;
+  int32_t power = 0;
+  __device__ __forceinline__ explicit Factor(double x) {
+    if (x != 0.0 && fabs(x) < 0x1p-126) x = frexp(x, &power);
+    f = static_cast<float>(x);
+  }
+  __device__ __forceinline__ float operator()(float x) const { return ldexpf(x * f, power); }
+  __device__ __forceinline__ bool one() const { return f == 1.0f && power == 0; }
+};
+
 // A chunk scaled.  Words lie as the tensors do: stores at any place within 16 bytes run
 // as fast as words cut by the output (1 GiB of bf16, outputs 2 bytes past a word: 400
 // us against 419).
 template <typename TI, typename TO>
-__device__ __forceinline__ void scale_chunk(const TI* p, TO* to, int32_t n, float f, bool zero) {
+__device__ __forceinline__ void scale_chunk(const TI* p, TO* to, int32_t n, Factor f, bool zero) {
   constexpr int kPer = Elem<TI>::kPer, kOut = Elem<TO>::kPer, kWords = kGradChunkBytes / 16 / kClipThreads;
   const int32_t words = n / kPer;
   Word4 x[kWords];
@@ -209,7 +223,7 @@ __device__ __forceinline__ void scale_chunk(const TI* p, TO* to, int32_t n, floa
     if (w < words) x[i] = load_stream(p + w * kPer);
   }
   const int32_t edge = words * kPer + threadIdx.x;
-  if (edge < n) to[edge] = Elem<TO>::round(zero ? 0.0f : Elem<TI>::load(p + edge) * f);
+  if (edge < n) to[edge] = Elem<TO>::round(zero ? 0.0f : f(Elem<TI>::load(p + edge)));
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
     const int32_t w = i * kClipThreads + threadIdx.x;
@@ -220,14 +234,14 @@ __device__ __forceinline__ void scale_chunk(const TI* p, TO* to, int32_t n, floa
     for (int part = 0; part < kPer; part += kOut) {
       float y[kOut];
 #pragma unroll
-      for (int j = 0; j < kOut; ++j) y[j] = zero ? 0.0f : v[part + j] * f;
+      for (int j = 0; j < kOut; ++j) y[j] = zero ? 0.0f : f(v[part + j]);
       store_stream(to + w * kPer + part, Elem<TO>::pack(y));
     }
   }
 }
 
 template <typename TI>
-__device__ __forceinline__ void scale_tensor(const Chunk& k, float f, bool zero) {
+__device__ __forceinline__ void scale_tensor(const Chunk& k, Factor f, bool zero) {
   const TI* from = reinterpret_cast<const TI*>(k.in);
   if (k.out_type == THD_FP32) scale_chunk(from, reinterpret_cast<float*>(k.out), k.n, f, zero);
   else scale_chunk(from, reinterpret_cast<TI*>(k.out), k.n, f, zero);
@@ -238,9 +252,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(GradList l, ClipArgs
   const float norm = norm_of(c, s_wave);
   if (finish && blockIdx.x == 0) finish_norm(c, norm);
   const bool zero = !(fabsf(norm) < __builtin_huge_valf());
-  // the factor in 64 bits, rounded once
   const double shrink = c.max_norm / (static_cast<double>(norm) + 1e-6);
-  const auto f = static_cast<float>(c.scale * (shrink < 1.0 ? shrink : 1.0));
+  const Factor f(c.scale * (shrink < 1.0 ? shrink : 1.0));
   const ListSearch search(l);
   const int32_t chunks = l.first[l.tensors];
   int32_t at = blockIdx.x;
@@ -248,7 +261,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(GradList l, ClipArgs
   while (k.n > 0) {
     at += gridDim.x;
     const Chunk next = at < chunks ? Chunk(l, search, chunks - 1 - at) : Chunk();
-    if (!k.own || f != 1.0f || zero) {  // else it holds the result
+    if (!k.own || !f.one() || zero) {  // else it holds the result
       if (k.type == THD_BF16) scale_tensor<Bf16>(k, f, zero);
       else if (k.type == THD_FP16) scale_tensor<Fp16>(k, f, zero);
       else scale_tensor<float>(k, f, zero);
