@@ -133,7 +133,11 @@ def embedding_backward(drows, ids, vocab, mask=None, scale=1.0, out=None, accumu
 
 def _tensors(tensors, name, device):
     """Host arrays (addresses, elements, types) of contiguous tensors on one device."""
-    dtypes = list(map(_dtype_of, tensors))
+    try:
+        dtypes = list(map(_dtype_of, tensors))
+    except AttributeError:
+        i = next(i for i, t in enumerate(tensors) if not isinstance(t, _Tensor))
+        raise ValueError(f"{name}[{i}] must be a tensor, got {type(tensors[i]).__name__}") from None
     # one look at all of them; the one that is wrong is found only where there is one
     if not _DTYPES.keys() >= set(dtypes):
         i = next(i for i, d in enumerate(dtypes) if d not in _DTYPES)
