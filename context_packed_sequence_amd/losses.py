@@ -63,7 +63,7 @@ def _address(x, name, dtype, count, device, required=False):
     if x.numel() != count:
         raise ValueError(f"{name} must have {count} elements, got {x.numel()}")
     if x.get_device() != device:
-        raise ValueError(f"{name} must be on the logits' device, got {x.device}")
+        raise ValueError(f"{name} must be on {f'cuda:{device}' if device >= 0 else 'cpu'}, got {x.device}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return x.data_ptr()
