@@ -83,3 +83,27 @@ def test_gradient_of_weak_values(torch, thd, gap, dtype):
     floor = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -39}[dtype]
     bound = (HALF[dtype] + r_p + n * U) * want + n * floor + HALF[dtype] * want + TINY[dtype]
     _within(dv[1:], np.full((n - 1, 1, 64), want), np.full((n - 1, 1, 64), bound), "dv")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("cap", [0.0, 4.0])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_not_finite_stays_in_its_document(torch, thd, dtype, cap, dim):
+    # fp16 holds all documents' gradients of scores by one power of two, from the largest norms of
+    # dout and v: they stand in a clean document, so that both runs take the same
+    say("attention values that are not finite", dtype, cap, dim)
+    b = Batch(torch, [70, 64, 70], heads=4, kv_heads=2, dim=dim, dtype=dtype, cap=cap)
+    for x in (b.v, b.dout):
+        x[3] = 8.0
+    clean, lse, _ = b.forward(thd)
+    grads = b.backward(thd, clean, lse)[:3]
+    for x in (b.q, b.k, b.v, b.dout):
+        x[70:134] = math.inf
+        x[80] = math.nan
+    out, lse2, _ = b.forward(thd)
+    got = b.backward(thd, out, lse2)[:3]
+    for part in (slice(0, 70), slice(134, 204)):
+        assert torch.equal(out[part], clean[part]) and torch.equal(lse2[:, part], lse[:, part])
+        for x, y in zip(got, grads):
+            assert torch.equal(x[part], y[part])
+    assert not out[70:134].isfinite().any()
