@@ -402,45 +402,71 @@ __device__ __forceinline__ void finish_row(const EmbedArgs& a, uint32_t v, int32
     }
 }
 
-// Partial sums: [unit][0: run from the unit before, 1: run into the next][width].
+// Partial sums: [unit][0: run from the unit before, 1: run into the next][partial_width].
 template <int kPer>
-__device__ __forceinline__ void store_partial(const EmbedArgs& a, const EmbedSort& s, int32_t unit, int32_t slot,
-                                              int32_t word, const float (&acc)[kPer]) {
-  float* to = s.partial + (2 * static_cast<int64_t>(unit) + slot) * a.width + word * kPer;
-  if (word * kPer + kPer <= a.width) {
+__device__ __forceinline__ void store_partial(const EmbedSort& s, int32_t unit, int32_t slot, int32_t word,
+                                              const float (&acc)[kPer]) {
+  float* to = s.partial + (2 * static_cast<int64_t>(unit) + slot) * s.partial_width + word * kPer;
 #pragma unroll
-    for (int part = 0; part < kPer; part += 4)
-      store_loose(to + part, Word4{__builtin_bit_cast(uint32_t, acc[part]), __builtin_bit_cast(uint32_t, acc[part + 1]),
-                                   __builtin_bit_cast(uint32_t, acc[part + 2]),
-                                   __builtin_bit_cast(uint32_t, acc[part + 3])});
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (word * kPer + j < a.width) to[j] = acc[j];
+  for (int part = 0; part < kPer; part += 4)
+    *reinterpret_cast<float4*>(to + part) = float4{acc[part], acc[part + 1], acc[part + 2], acc[part + 3]};
 }
 
 template <int kPer>
-__device__ __forceinline__ void load_partial(const EmbedArgs& a, const EmbedSort& s, int32_t unit, int32_t slot,
-                                             int32_t word, float (&x)[kPer]) {
-  const float* from = s.partial + (2 * static_cast<int64_t>(unit) + slot) * a.width + word * kPer;
-  if (word * kPer + kPer <= a.width) {
+__device__ __forceinline__ void load_partial(const EmbedSort& s, int32_t unit, int32_t slot, int32_t word,
+                                             float (&x)[kPer]) {
+  const float* from = s.partial + (2 * static_cast<int64_t>(unit) + slot) * s.partial_width + word * kPer;
 #pragma unroll
-    for (int part = 0; part < kPer; part += 4) {
-      const Word4 w = load_loose(from + part);
+  for (int part = 0; part < kPer; part += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(from + part);
+    x[part] = f.x, x[part + 1] = f.y, x[part + 2] = f.z, x[part + 3] = f.w;
+  }
+}
+
+// A row's word of a thread.  Where the row ends inside the word, the 16 bytes that end
+// with the row are loaded, and the elements of the word before dropped once all loads are
+// on their way: element by element each row was waited for (20510 rows of 10 fp16 elements:
+// the launch 61 us).  Rows shorter than a word go element by element.
+template <typename T, bool kShort>
+struct RowWord {
+  static constexpr int kPer = Elem<T>::kPer, kBits = 128 / kPer;
+  int32_t at, width;  // elements
+  int32_t up, down;   // bits to shift by, to bring the word's own elements to their places
+  __device__ __forceinline__ RowWord(int32_t row_width, int32_t word) : width(row_width) {
+    at = kShort ? 0 : min(word * kPer, row_width - kPer);
+    up = kShort ? kBits * (kPer - row_width) : 0;
+    down = kShort ? up : kBits * (word * kPer - at);
+  }
+  // whether any word of a row has to be shifted
+  __device__ __forceinline__ bool ragged() const { return width % kPer != 0; }
+  __device__ __forceinline__ Word4 load(const T* row) const {
+    if constexpr (!kShort) {
+      return load_loose(row + at);
+    } else {
+      uint32_t x[kPer];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t bits = w[j];
-        x[part + j] = __builtin_bit_cast(float, bits);
-      }
+      for (int j = 0; j < kPer; ++j) x[j] = load_raw(row + min(j, width - 1));
+      Word4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = kPer == 8 ? x[2 * i % kPer] | (x[(2 * i + 1) % kPer] << 16) : x[i];
+      return w;
     }
-    return;
   }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) x[j] = word * kPer + j < a.width ? from[j] : 0.0f;
-}
+  // the word's own elements of what was loaded, zeros after the row
+  __device__ __forceinline__ Word4 own(Word4 w) const {
+    uint64_t low = w[0] | (static_cast<uint64_t>(w[1]) << 32), high = w[2] | (static_cast<uint64_t>(w[3]) << 32);
+    if constexpr (kShort) {  // the elements after the row's go
+      if (up >= 64) high = low << (up - 64), low = 0;
+      else if (up > 0) high = (high << up) | (low >> (64 - up)), low <<= up;
+    }
+    if (down >= 64) low = high >> (down - 64), high = 0;
+    else if (down > 0) low = (low >> down) | (high << (64 - down)), high >>= down;
+    return Word4{static_cast<uint32_t>(low), static_cast<uint32_t>(low >> 32), static_cast<uint32_t>(high),
+                 static_cast<uint32_t>(high >> 32)};
+  }
+};
 
-template <typename TI, typename TO>
+template <typename TI, typename TO, bool kShort>
 __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort s, int32_t words, FastDiv by_words,
                                                          int32_t unit_blocks, ZeroRows z) {
   constexpr int kPer = Elem<TI>::kPer;
@@ -473,7 +499,7 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort 
   if (unit64 >= s.units) return;
   const auto unit = static_cast<int32_t>(unit64);
   const int32_t first = unit * s.unit, last = min(a.rows - first, s.unit) + first;
-  const bool whole = word * kPer + kPer <= a.width;
+  const RowWord<TI, kShort> mine(a.width, word);
   uint32_t key = s.a[first].key;
   if (key == none) return;  // as are all after it
   bool open = first > 0 && s.a[first - 1].key == key;  // the run began in a unit before
@@ -485,25 +511,17 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort 
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) item[i] = i0 + i < last ? s.a[i0 + i] : TokenRow{none, 0};
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      x[i] = Word4{0, 0, 0, 0};
-      if (item[i].key == none) continue;
-      const TI* from = static_cast<const TI*>(a.drows) + static_cast<int64_t>(item[i].row) * a.in_stride + word * kPer;
-      if (whole) {
-        x[i] = load_loose(from);
-      } else {
-        float v[kPer] = {};
+    for (int i = 0; i < kBatch; ++i)  // rows that do not count: any row, not looked at
+      x[i] = mine.load(static_cast<const TI*>(a.drows) + static_cast<int64_t>(item[i].row) * a.in_stride);
+    if (mine.ragged()) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (word * kPer + j < a.width) v[j] = Elem<TI>::load(from + j);
-        x[i] = Elem<TI>::pack(v);
-      }
+      for (int i = 0; i < kBatch; ++i) x[i] = mine.own(x[i]);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (i0 + i >= last || key == none) continue;
       if (item[i].key != key) {
-        if (open) store_partial<kPer>(a, s, unit, 0, word, acc);
+        if (open) store_partial<kPer>(s, unit, 0, word, acc);
         else finish_row<TI, TO>(a, key, word, acc);
         open = false;
         key = item[i].key;
@@ -518,8 +536,8 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort 
     }
   }
   if (key == none) return;
-  if (open) store_partial<kPer>(a, s, unit, 0, word, acc);
-  else if (last < a.rows && s.a[last].key == key) store_partial<kPer>(a, s, unit, 1, word, acc);
+  if (open) store_partial<kPer>(s, unit, 0, word, acc);
+  else if (last < a.rows && s.a[last].key == key) store_partial<kPer>(s, unit, 1, word, acc);
   else finish_row<TI, TO>(a, key, word, acc);
 }
 
@@ -548,12 +566,12 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, EmbedSort 
   }
   const int32_t end = (low - 1) / s.unit;  // the run's last unit
   float acc[kPer];
-  load_partial<kPer>(a, s, unit, 1, word, acc);
+  load_partial<kPer>(s, unit, 1, word, acc);
   constexpr int kBatch = 8;  // parts in flight
   for (int32_t u0 = unit + 1; u0 <= end; u0 += kBatch) {
     float part[kBatch][kPer];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) load_partial<kPer>(a, s, min(u0 + i, end), 0, word, part[i]);
+    for (int i = 0; i < kBatch; ++i) load_partial<kPer>(s, min(u0 + i, end), 0, word, part[i]);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
 #pragma unroll
@@ -593,8 +611,12 @@ hipError_t sums(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
   const auto unit_blocks = static_cast<int32_t>((static_cast<int64_t>(s.units) * words + 255) / 256);
   const ZeroRows z = zero_rows(a, cleared_early(a), a.vocab, 65536, 256);  // rows are searched for side by side
   const int64_t blocks = unit_blocks + zero_blocks(a, z);
-  if (blocks > 0)
-    embed_sums_kernel<TI, TO><<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, s, words, by_words, unit_blocks, z);
+  if (blocks > 0 && a.width < Elem<TI>::kPer)
+    embed_sums_kernel<TI, TO, true>
+        <<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, s, words, by_words, unit_blocks, z);
+  else if (blocks > 0)
+    embed_sums_kernel<TI, TO, false>
+        <<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, s, words, by_words, unit_blocks, z);
   if (unit_blocks > 0 && s.units > 1)
     embed_join_kernel<TI, TO><<<unit_blocks, 256, 0, stream>>>(a, s, words, by_words);
   return hipGetLastError();

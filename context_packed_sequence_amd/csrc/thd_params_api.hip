@@ -79,7 +79,8 @@ EmbedLayout embed_layout(void* workspace, int64_t rows, int64_t vocab, int64_t w
     l.sort.b = reinterpret_cast<thdcp::TokenRow*>(take(rows * static_cast<int64_t>(sizeof(thdcp::TokenRow))));
     l.sort.counts = reinterpret_cast<int32_t*>(take((thdcp::kSortBlocks * (thdcp::kSortBins + 1)) * 4LL));
   }
-  l.sort.partial = reinterpret_cast<float*>(take(static_cast<int64_t>(l.sort.units) * 2 * width * 4));
+  l.sort.partial_width = static_cast<int32_t>(align_up(width, 8));
+  l.sort.partial = reinterpret_cast<float*>(take(static_cast<int64_t>(l.sort.units) * 2 * l.sort.partial_width * 4));
   return l;
 }
 

@@ -44,7 +44,8 @@ struct EmbedSort {
   int32_t* counts;           // [blocks][kSortBins]
   int32_t blocks, turns;     // turns of kSortTile rows in a workgroup
   int32_t passes, bits;      // digits of `bits` bits
-  float* partial;            // [units][2][width]
+  float* partial;            // [units][2][partial_width]
+  int32_t partial_width;     // width in whole words of any type
   int32_t unit;              // sorted rows of a unit
   int32_t units;
 };

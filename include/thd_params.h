@@ -46,8 +46,8 @@ int thd_embedding(const int64_t* ids, const uint8_t* mask, int64_t rows, const v
 /*
  * thd_embedding_workspace_bytes -- workspace of thd_embedding_backward, 16-byte
  * aligned: 16 bytes a row, partial sums of runs of one token that pass the borders of
- * units of 16 to 128 sorted rows (8 bytes for each element of a row and unit), and up
- * to 0.5 MiB.  -1 for sizes the call refuses.  Host-only arithmetic.
+ * units of 16 to 128 sorted rows (8 bytes for each element of a row and unit, rows in
+ * whole eights of elements), and up to 0.5 MiB.  -1 for sizes the call refuses.  Host-only arithmetic.
  */
 int64_t thd_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t width);
 
