@@ -555,27 +555,31 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, EmbedSort 
   const auto unit = static_cast<int32_t>(unit64);
   const int32_t first = unit * s.unit, last = min(a.rows - first, s.unit) + first;
   if (last >= a.rows) return;
-  const uint32_t key = s.a[last - 1].key;
-  if (key == none || s.a[last].key != key) return;
-  if (first > 0 && s.a[first].key == key && s.a[first - 1].key == key) return;  // it began before
-  int32_t low = last, high = a.rows;  // first place after the run
-  while (low < high) {
-    const int32_t mid = low + ((high - low) >> 1);
-    if (s.a[mid].key == key) low = mid + 1;
-    else high = mid;
-  }
-  const int32_t end = (low - 1) / s.unit;  // the run's last unit
+  const uint32_t begin = s.a[first].key, before = s.a[max(first - 1, 0)].key;
+  const uint32_t key = s.a[last - 1].key, next = s.a[last].key;
+  if (key == none || next != key) return;
+  if (first > 0 && begin == key && before == key) return;  // it began before
   float acc[kPer];
   load_partial<kPer>(s, unit, 1, word, acc);
-  constexpr int kBatch = 8;  // parts in flight
-  for (int32_t u0 = unit + 1; u0 <= end; u0 += kBatch) {
+  // Units whose first row holds the token have a part of the run; their keys come with
+  // the parts, those past the run's end for nothing.
+  constexpr int kBatch = 16;  // parts in flight
+  bool more = true;
+  for (int32_t u0 = unit + 1; more; u0 += kBatch) {
     float part[kBatch][kPer];
+    uint32_t k[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) load_partial<kPer>(s, min(u0 + i, end), 0, word, part[i]);
+    for (int i = 0; i < kBatch; ++i) {
+      const int32_t u = min(u0 + i, s.units - 1);
+      k[i] = s.a[static_cast<int64_t>(u) * s.unit].key;
+      load_partial<kPer>(s, u, 0, word, part[i]);
+    }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < kBatch; ++i) {
+      more = more && u0 + i < s.units && k[i] == key;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) acc[j] += u0 + i <= end ? part[i][j] : 0.0f;
+      for (int j = 0; j < kPer; ++j) acc[j] += more ? part[i][j] : 0.0f;
+    }
   }
   finish_row<TI, TO>(a, key, word, acc);
 }
