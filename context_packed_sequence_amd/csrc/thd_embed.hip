@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kEarlyRows = 4096;  // of the table, at most, that a workgroup beside the sort clears
 
 // 16 bytes at any element's alignment: the hardware takes them as they lie.
 struct __attribute__((packed, aligned(2))) LooseWord {
@@ -201,7 +202,8 @@ template <int kEach>
 __device__ __forceinline__ void rank_digits(const uint32_t (&digit)[kEach], const bool (&in)[kEach], int32_t bits,
                                             int32_t (*s_count)[kSortBins], int32_t* s_total, int32_t (&rank)[kEach]) {
   const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int32_t i = threadIdx.x; i < kSortWaves * kSortBins; i += kSortThreads) (&s_count[0][0])[i] = 0;
+  const int32_t bins = 1 << bits;
+  for (int32_t i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) s_count[i >> bits][i & (bins - 1)] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -224,28 +226,33 @@ __device__ __forceinline__ void rank_digits(const uint32_t (&digit)[kEach], cons
   __syncthreads();
   for (int32_t d = threadIdx.x; d < kSortBins; d += kSortThreads) {
     int32_t sum = 0;
+    if (d < bins) {
+      int32_t n[kSortWaves];
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int32_t n = s_count[w][d];
-      s_count[w][d] = sum;
-      sum += n;
+      for (int w = 0; w < kSortWaves; ++w) n[w] = s_count[w][d];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        s_count[w][d] = sum;
+        sum += n[w];
+      }
     }
     s_total[d] = sum;
   }
   __syncthreads();
 }
 
-// Up to kSortBlock rows: one workgroup, all passes in LDS (4099 rows, 100003 tokens: 20
-// us).  The others clear rows of tokens that do not occur meanwhile, having looked
+// Up to kSortBlock rows: one workgroup, all passes in LDS, kEach rows a thread: what each
+// costs in instructions is most of the time.  The others clear rows of tokens that do not occur meanwhile, having looked
 // through the ids themselves.
+template <int kEach>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_block_kernel(EmbedArgs a, EmbedSort s, ZeroRows z) {
-  constexpr int kEach = kSortBlock / kSortThreads;
   __shared__ int32_t s_count[kSortWaves][kSortBins];
   __shared__ int32_t s_total[kSortBins];
   __shared__ int32_t s_wave[kSortWaves + 1];
   __shared__ int s_bad;
-  __shared__ TokenRow s_item[kSortBlock];
+  __shared__ TokenRow s_item[kEach * kSortThreads];
   if (blockIdx.x > 0) {
+    static_assert(sizeof(s_item) >= kEarlyRows, "a byte a row");
     auto* s_taken = reinterpret_cast<uint8_t*>(s_item);
     const int32_t r0 = z.row(static_cast<int32_t>(blockIdx.x) - 1), n = min(z.each, z.end - r0);
     find_taken<kSortThreads>(a, r0, n, s_taken);
@@ -663,8 +670,12 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t stream) {
 
 hipError_t launch_embedding_sort(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
   if (a.rows <= kSortBlock) {
-    const ZeroRows z = zero_rows(a, 0, cleared_early(a), 262144, 4096);
-    embed_sort_block_kernel<<<static_cast<uint32_t>(1 + zero_blocks(a, z)), kSortThreads, 0, stream>>>(a, s, z);
+    const ZeroRows z = zero_rows(a, 0, cleared_early(a), 262144, kEarlyRows);
+    const auto blocks = static_cast<uint32_t>(1 + zero_blocks(a, z));
+    if (a.rows <= kSortThreads) embed_sort_block_kernel<1><<<blocks, kSortThreads, 0, stream>>>(a, s, z);
+    else if (a.rows <= 2 * kSortThreads) embed_sort_block_kernel<2><<<blocks, kSortThreads, 0, stream>>>(a, s, z);
+    else if (a.rows <= 4 * kSortThreads) embed_sort_block_kernel<4><<<blocks, kSortThreads, 0, stream>>>(a, s, z);
+    else embed_sort_block_kernel<kSortBlock / kSortThreads><<<blocks, kSortThreads, 0, stream>>>(a, s, z);
     return hipGetLastError();
   }
   const TokenRow* from = nullptr;
