@@ -507,18 +507,23 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort 
   const auto unit = static_cast<int32_t>(unit64);
   const int32_t first = unit * s.unit, last = min(a.rows - first, s.unit) + first;
   const RowWord<TI, kShort> mine(a.width, word);
-  uint32_t key = s.a[first].key;
-  if (key == none) return;  // as are all after it
-  bool open = first > 0 && s.a[first - 1].key == key;  // the run began in a unit before
-  float acc[kPer] = {};
   constexpr int kBatch = 8;
+  TokenRow item[kBatch], next[kBatch];
+  const auto items = [&](int32_t from, TokenRow (&to)[kBatch]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) to[i] = s.a[from < a.rows - i ? from + i : a.rows - 1];
+  };
+  const uint32_t before = s.a[max(first - 1, 0)].key;
+  items(first, item);
+  uint32_t key = item[0].key;
+  if (key == none) return;  // as are all after it
+  bool open = first > 0 && before == key;  // the run began in a unit before
+  float acc[kPer] = {};
   for (int32_t i0 = first; i0 < last && key != none; i0 += kBatch) {
-    TokenRow item[kBatch];
     Word4 x[kBatch];
+    items(i0 + kBatch < last ? i0 + kBatch : i0, next);  // ahead of the rows they are needed after
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) item[i] = i0 + i < last ? s.a[i0 + i] : TokenRow{none, 0};
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)  // rows that do not count: any row, not looked at
+    for (int i = 0; i < kBatch; ++i)  // also rows that do not count, not looked at
       x[i] = mine.load(static_cast<const TI*>(a.drows) + static_cast<int64_t>(item[i].row) * a.in_stride);
     if (mine.ragged()) {
 #pragma unroll
@@ -541,6 +546,8 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedArgs a, EmbedSort 
 #pragma unroll
       for (int j = 0; j < kPer; ++j) acc[j] += v[j];
     }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) item[i] = next[i];
   }
   if (key == none) return;
   if (open) store_partial<kPer>(s, unit, 0, word, acc);
