@@ -67,7 +67,7 @@ struct EmbedLayout {
 };
 
 EmbedLayout embed_layout(void* workspace, int64_t rows, int64_t vocab, int64_t width) {
-  EmbedLayout l{thdcp::embed_sort(rows, vocab), 0};
+  EmbedLayout l{thdcp::embed_sort(rows, vocab, width), 0};
   char* base = static_cast<char*>(workspace);
   const auto take = [&](int64_t n) {
     char* p = base + l.bytes;

@@ -50,7 +50,7 @@ struct EmbedSort {
   int32_t units;
 };
 
-EmbedSort embed_sort(int64_t rows, int64_t vocab);
+EmbedSort embed_sort(int64_t rows, int64_t vocab, int64_t width);
 
 hipError_t launch_embedding(const EmbedArgs& a, hipStream_t stream);
 hipError_t launch_embedding_sort(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream);

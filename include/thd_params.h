@@ -54,7 +54,8 @@ int64_t thd_embedding_workspace_bytes(int64_t rows, int64_t vocab, int64_t width
 /*
  * thd_embedding_backward -- dtable[v] = scale sum of drows[t] over the rows t with
  * ids[t] = v and mask not 0, in 32 bits in the rows' order within units of 16 to 128
- * sorted rows (the more rows, the longer), those sums in order, rounded once.
+ * sorted rows (the more and the wider the rows, the longer), those sums in order, rounded
+ * once.
  *
  * drows: [rows][width] of dtype, rows `row_stride` elements apart; dtable:
  * [vocab][width] of out_dtype, which is dtype or THD_FP32, rows `table_stride` apart.
