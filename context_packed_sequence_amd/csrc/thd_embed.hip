@@ -185,14 +185,31 @@ __device__ __forceinline__ void find_taken(const EmbedArgs& a, int32_t r0, int32
 
 // ---- sort -------------------------------------------------------------------
 
-// Row t as it enters the sort: rows that do not count come last.
-__device__ __forceinline__ TokenRow token_row(const EmbedArgs& a, int32_t t, bool* bad) {
-  TokenRow r{static_cast<uint32_t>(a.vocab), static_cast<uint32_t>(t)};
-  if (a.mask && a.mask[t] == 0) return r;
-  const int64_t id = a.ids[t];
-  if (id < 0 || id >= a.vocab) *bad = true;
-  else r.key = static_cast<uint32_t>(id);
-  return r;
+// Row t as it enters the sort, from its id and mask: rows that do not count come last.
+__device__ __forceinline__ TokenRow token_row(const EmbedArgs& a, int32_t t, int64_t id, bool on, bool* bad) {
+  const bool good = id >= 0 && id < a.vocab;
+  *bad |= on && !good;
+  return TokenRow{static_cast<uint32_t>(on && good ? id : a.vocab), static_cast<uint32_t>(t)};
+}
+
+// Rows t[i] as they enter the sort, where in[i]; ids and masks of all of them are on their
+// way before the first is waited for.
+template <int kEach>
+__device__ __forceinline__ void token_rows(const EmbedArgs& a, const uint32_t (&t)[kEach], const bool (&in)[kEach],
+                                           TokenRow (&item)[kEach], bool* bad) {
+  // without a mask its places are read from the ids, and not looked at
+  const uint8_t* mask = a.mask ? a.mask : reinterpret_cast<const uint8_t*>(a.ids);
+  int64_t id[kEach];
+  uint8_t on[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t at = in[i] ? t[i] : 0u;
+    id[i] = a.ids[at];
+    on[i] = mask[at];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    item[i] = in[i] ? token_row(a, static_cast<int32_t>(t[i]), id[i], !a.mask || on[i] != 0, bad) : TokenRow{0, 0};
 }
 
 // Ranks of a workgroup's items among those with the same digit: on return
@@ -263,13 +280,14 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_block_kernel(EmbedArg
   const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (threadIdx.x == 0) s_bad = 0;
   TokenRow item[kEach];
+  uint32_t place[kEach];
   bool in[kEach], bad = false;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int32_t t = (wave * kEach + i) * 64 + lane;
-    in[i] = t < a.rows;
-    item[i] = in[i] ? token_row(a, t, &bad) : TokenRow{0, 0};
+    place[i] = (wave * kEach + i) * 64 + lane;
+    in[i] = place[i] < static_cast<uint32_t>(a.rows);
   }
+  token_rows<kEach>(a, place, in, item, &bad);
   for (int32_t p = 0; p < s.passes; ++p) {
     uint32_t digit[kEach];
     int32_t rank[kEach];
@@ -313,9 +331,25 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedArgs a, 
   const uint32_t first = blockIdx.x * static_cast<uint32_t>(s.turns) * kSortTile;
   const uint32_t end = min(static_cast<uint32_t>(a.rows), first + static_cast<uint32_t>(s.turns) * kSortTile);
   bool bad = false;
-  for (uint32_t t = first + threadIdx.x; t < end; t += kSortThreads) {
-    const TokenRow r = from ? from[t] : token_row(a, static_cast<int32_t>(t), &bad);
-    atomicAdd(&s_count[(r.key >> shift) & ((1u << s.bits) - 1)], 1);
+  constexpr int kEach = kSortTile / kSortThreads;
+  for (uint32_t t0 = first + threadIdx.x; t0 < end; t0 += kSortTile) {
+    TokenRow item[kEach];
+    uint32_t t[kEach];
+    bool in[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      t[i] = t0 + i * kSortThreads;
+      in[i] = t[i] < end;
+    }
+    if (from) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) item[i] = from[in[i] ? t[i] : 0u];
+    } else {
+      token_rows<kEach>(a, t, in, item, &bad);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (in[i]) atomicAdd(&s_count[(item[i].key >> shift) & ((1u << s.bits) - 1)], 1);
   }
   if (bad) s_bad = 1;
   __syncthreads();
@@ -324,7 +358,9 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedArgs a, 
 }
 
 // ... and its rows placed: a digit's first place is that of all smaller digits
-// and of the workgroups before, which every workgroup adds up for itself.
+// and of the workgroups before, which every workgroup adds up for itself (counting all
+// rows' digits in each of them instead of a launch before: 9000 rows 40 -> 38 us, 32768
+// 50 -> 65).
 __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedArgs a, EmbedSort s, const TokenRow* from,
                                                                    TokenRow* to, int32_t shift) {
   constexpr int kEach = kSortTile / kSortThreads;
@@ -333,6 +369,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedArgs a, 
   __shared__ int32_t s_wave[kSortWaves + 1];
   __shared__ int s_bad;
   const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(s.turns) * kSortTile;
+  bool bad = false;
   if (!from && a.status && blockIdx.x == 0) {
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
@@ -353,20 +391,24 @@ __global__ __launch_bounds__(kSortThreads) void embed_place_kernel(EmbedArgs a, 
   const int32_t smaller = block_exclusive_scan<kSortThreads>(all, s_wave, &sum);
   if (threadIdx.x < kSortBins) s_first[threadIdx.x] = smaller + before;
   __syncthreads();
-  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(s.turns) * kSortTile;
-  bool bad = false;
   for (int32_t turn = 0; turn < s.turns; ++turn) {
     TokenRow item[kEach];
-    uint32_t digit[kEach];
+    uint32_t digit[kEach], t[kEach];
     bool in[kEach];
     int32_t rank[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const uint32_t t = begin + static_cast<uint32_t>(turn) * kSortTile + (wave * kEach + i) * 64 + lane;
-      in[i] = t < static_cast<uint32_t>(a.rows);
-      item[i] = !in[i] ? TokenRow{0, 0} : from ? from[t] : token_row(a, static_cast<int32_t>(t), &bad);
-      digit[i] = (item[i].key >> shift) & ((1u << s.bits) - 1);
+      t[i] = begin + static_cast<uint32_t>(turn) * kSortTile + (wave * kEach + i) * 64 + lane;
+      in[i] = t[i] < static_cast<uint32_t>(a.rows);
     }
+    if (from) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) item[i] = in[i] ? from[t[i]] : TokenRow{0, 0};
+    } else {
+      token_rows<kEach>(a, t, in, item, &bad);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) digit[i] = (item[i].key >> shift) & ((1u << s.bits) - 1);
     rank_digits<kEach>(digit, in, s.bits, s_count, s_total, rank);
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
@@ -617,10 +659,17 @@ int64_t zero_blocks(const EmbedArgs& a, const ZeroRows& z) {
   return a.accumulate ? 0 : (static_cast<int64_t>(z.end) - z.first + z.each - 1) / z.each;
 }
 // Rows of the table that are cleared beside the sort of a small batch, which leaves most
-// of the chip free; the others are, beside the sums (4099 rows of 1001 floats in a table
-// of 100003: none 119 us, a quarter 102, five eighths 104, all 107).
+// of the chip free; the others are, beside the sums.  What fits beside a sort is bytes: so
+// many and so many more for each row that it has to sort.  A quarter of the table
+// instead (in microseconds, fp32): 153 rows, table of 69994 x 267 29.8 against 24.2; 8000
+// rows, 262000 x 64 41.0 and 33.7, 100000 x 500 56.6 and 48.3; 4099 rows, 100003 x 1001 95.6
+// and 97.0; half as many bytes 24.4, 33.4, 50.7 and 99.6.
+constexpr int64_t kEarlyBytes = 28000000, kEarlyBytesPerRow = 9000;
 int32_t cleared_early(const EmbedArgs& a) {
-  return a.rows > 0 && a.rows <= kSortBlock ? a.vocab / 4 : 0;
+  if (a.rows == 0 || a.rows > kSortBlock) return 0;
+  const int64_t row = static_cast<int64_t>(a.width) * (a.out_dtype == THD_FP32 ? 4 : 2);
+  const int64_t most = (kEarlyBytes + kEarlyBytesPerRow * a.rows) / row;
+  return static_cast<int32_t>(most < a.vocab ? most : a.vocab);
 }
 
 template <typename TI, typename TO>
@@ -684,7 +733,7 @@ hipError_t launch_embedding(const EmbedArgs& a, hipStream_t stream) {
 
 hipError_t launch_embedding_sort(const EmbedArgs& a, const EmbedSort& s, hipStream_t stream) {
   if (a.rows <= kSortBlock) {
-    const ZeroRows z = zero_rows(a, 0, cleared_early(a), 262144, kEarlyRows);
+    const ZeroRows z = zero_rows(a, 0, cleared_early(a), 131072, kEarlyRows);
     const auto blocks = static_cast<uint32_t>(1 + zero_blocks(a, z));
     if (a.rows <= kSortThreads) embed_sort_block_kernel<1><<<blocks, kSortThreads, 0, stream>>>(a, s, z);
     else if (a.rows <= 2 * kSortThreads) embed_sort_block_kernel<2><<<blocks, kSortThreads, 0, stream>>>(a, s, z);
