@@ -140,17 +140,49 @@ struct ZeroRows {
   char* to;
   int64_t stride;
   int32_t bytes, words;
-  FastDiv by_words;
+  FastDiv by_words, by_bytes;
   int32_t first, end;  // rows of the table
   int32_t each;        // of them to a workgroup
+  bool run;            // rows follow one another without gaps, and are more than caches hold
   __device__ __forceinline__ int32_t row(int32_t block) const { return first + block * each; }
 };
 
-// Clears those of rows r0 .. r0 + n - 1 whose flag is not set.  Plain stores: parts of
-// a line at rows' ends meet in the caches (400 MB of rows of 1001 floats 74 us; stores
-// that pass the caches 97, and no faster for aligned rows).
+// Two bytes of a run of rows without gaps, unless their row's flag is set.
+__device__ __forceinline__ void clear_pair(const ZeroRows& z, char* base, int32_t at, const uint8_t* s_taken) {
+  if (!s_taken[z.by_bytes(at)]) *reinterpret_cast<uint16_t*>(base + at) = 0;
+}
+
+// Clears those of rows r0 .. r0 + n - 1 whose flag is not set.  A large table without gaps
+// is cleared as one run, in 16-byte words from a line's start on whose stores pass the
+// caches; a word that holds parts of rows with and without a token goes by twos of bytes.
+// Other tables go row by row with plain stores, which meet in the caches at rows' ends and
+// stay there.  fp32, few rows: 133106 x 1185 as a run 105 us, row by row 127; 100000 x 1024 73
+// and 82; but 250000 x 250, which the 256 MB cache in front of memory holds, 50 and 44.
 template <int kThreads>
 __device__ __forceinline__ void clear_rows(const ZeroRows& z, int32_t r0, int32_t n, const uint8_t* s_taken) {
+  if (z.run) {
+    char* base = z.to + static_cast<int64_t>(r0) * z.stride;
+    const int32_t size = n * z.bytes, lead = min(size, static_cast<int32_t>(-reinterpret_cast<uintptr_t>(base) & 127));
+    const int32_t words = (size - lead) / 128 * 8, tail = lead + 16 * words;
+    const StreamStore store(base + lead, 16 * words);
+    for (int32_t w = threadIdx.x; w < words; w += kThreads) {
+      const int32_t at = lead + 16 * w, first = z.by_bytes(at), last = z.by_bytes(at + 15);
+      bool any = s_taken[first] != 0, all = any;
+      for (int32_t r = first + 1; r <= last; ++r) {
+        const bool taken = s_taken[r] != 0;
+        any |= taken;
+        all &= taken;
+      }
+      if (!any) {
+        store(w, StoreW4{0, 0, 0, 0});
+      } else if (!all) {
+        for (int32_t b = 0; b < 16; b += 2) clear_pair(z, base, at + b, s_taken);
+      }
+    }
+    for (int32_t at = 2 * threadIdx.x; at < lead; at += 2 * kThreads) clear_pair(z, base, at, s_taken);
+    for (int32_t at = tail + 2 * threadIdx.x; at < size; at += 2 * kThreads) clear_pair(z, base, at, s_taken);
+    return;
+  }
   for (int32_t i = threadIdx.x; i < n * z.words; i += kThreads) {
     const int32_t r = z.by_words(i), at = 16 * (i - r * z.words);
     if (s_taken[r]) continue;
@@ -641,7 +673,10 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedArgs a, EmbedSort 
   finish_row<TI, TO>(a, key, word, acc);
 }
 
-// Rows [first, end) of the table, `bytes` of it and at most so many rows to a workgroup.
+constexpr int64_t kCachedTable = 256 << 20;
+
+// Rows [first, end) of the table, at most so many to a workgroup, and `bytes` of it: a
+// quarter of that for a run and a few ids, which are looked through in no time.
 ZeroRows zero_rows(const EmbedArgs& a, int32_t first, int32_t end, int64_t bytes, int32_t most_rows) {
   const int64_t size = a.out_dtype == THD_FP32 ? 4 : 2, row = a.width * size;
   ZeroRows z{};
@@ -650,8 +685,11 @@ ZeroRows zero_rows(const EmbedArgs& a, int32_t first, int32_t end, int64_t bytes
   z.bytes = static_cast<int32_t>(row);
   z.words = static_cast<int32_t>((row + 15) / 16);
   z.by_words = FastDiv::make(z.words);
+  z.by_bytes = FastDiv::make(z.bytes);
   z.first = first;
   z.end = end;
+  z.run = a.out_stride == a.width && row * a.vocab > kCachedTable;
+  if (z.run && a.rows <= kSortThreads) bytes /= 4;
   z.each = static_cast<int32_t>(row >= bytes ? 1 : bytes / row < most_rows ? bytes / row : most_rows);
   return z;
 }
