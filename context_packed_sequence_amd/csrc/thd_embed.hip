@@ -690,7 +690,8 @@ ZeroRows zero_rows(const EmbedArgs& a, int32_t first, int32_t end, int64_t bytes
   z.end = end;
   z.run = a.out_stride == a.width && row * a.vocab > kCachedTable;
   if (z.run && a.rows <= kSortThreads) bytes /= 4;
-  z.each = static_cast<int32_t>(row >= bytes ? 1 : bytes / row < most_rows ? bytes / row : most_rows);
+  const int64_t each = (bytes + row / 2) / row;
+  z.each = static_cast<int32_t>(each < 1 ? 1 : each < most_rows ? each : most_rows);
   return z;
 }
 int64_t zero_blocks(const EmbedArgs& a, const ZeroRows& z) {
