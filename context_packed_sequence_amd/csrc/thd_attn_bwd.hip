@@ -21,8 +21,9 @@
 // documents, 32 heads of 128: 54 us of 446).
 //
 // Bound as the forward pass is; one document of 8192 tokens, causal, 32 heads of 128
-// over 8: dq 713 us (1157 TFLOP/s, matrix units busy 61 %), dk and dv 996 (1104, 53 %)
-// and 70 to add up their parts; with a cap 888 and 1202.
+// over 8: dq 713 us (1157 TFLOP/s, matrix units busy 61 %, LDS 30 %), dk and dv 996 (1104,
+// 53 %, 40 %) and 70 to add up their parts; with a cap 888 and 1202; in fp16 781 and 1108,
+// and 46 for delta and the largest norms.
 //
 // fp16: p times 2^14 and dz times a power of two for which no dz passes the
 // type's range (from the largest norms of a dout row and of a v row) keep small

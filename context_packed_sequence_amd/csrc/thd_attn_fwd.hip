@@ -21,11 +21,13 @@
 // 8192 tokens, 32 heads of 128 over 8, causal, fp16: 566 us against 563 without, 575 with
 // 2^13 and 2^2.
 //
-// Bound by the matrix units and the vector units together, which hardly overlap: one
-// document of 8192 tokens, causal, 32 heads over 8, takes 524 us with heads of 128 (1050
-// TFLOP/s; the matrix units busy for 57 % of the cycles, vector instructions for 47 %),
-// 429 with 96, 311 with 64, and 639 with 128 and a cap.  A large matrix product of the
-// library reaches 1415 TFLOP/s.
+// Long documents are bound by the matrix units and the vector units together, which hardly
+// overlap: one of 8192 tokens, causal, 32 heads over 8, takes 524 us with heads of 128 (1050
+// TFLOP/s; the matrix units busy for 57 % of the cycles, vector instructions for 47 %, LDS
+// for 28 %), 429 with 96, 311 with 64, and 639 with 128 and a cap.  A large matrix product
+// of the library reaches 1415 TFLOP/s.  Short ones are bound by starting and ending tiles
+// (32768 tokens of documents of 64 to 1024: ten steps a tile, matrix units busy for 34 %),
+// few long ones by the chain of a tile's steps (93 steps of 12 heads of 72: 0.95 us each).
 #include "thd_attn_device.h"
 
 namespace thdcp {

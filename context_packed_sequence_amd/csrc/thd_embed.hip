@@ -8,12 +8,17 @@
 // a wave finds a digit's rank among its 64 lanes from ballots, one per bit, and
 // the counts of waves, workgroups and digits before it make it a place.  Then units
 // of 16 to 128 sorted rows are summed, one thread per 16-byte column of a unit, in
-// order: balanced however often a token occurs (the commonest of a text makes
-// thousands of rows).  A token whose rows lie within one unit is stored at once;
+// order: even however often a token occurs (the commonest of a text makes thousands of
+// rows).  A token whose rows lie within one unit is stored at once;
 // where its run passes a unit's border the sums go to a workspace, and the thread
 // of the unit in which the run begins adds them up, in order, in the last launch.
 // The rows of tokens that do not occur are cleared beside the sort of a small batch, or
 // beside the sums of a large one.
+//
+// Long rows are bound by memory (32768 rows of 4096 bf16, table of 32000: 155 us, the sums
+// 4.7 TB/s at random rows; 4099 of 1001 fp32, table of 100003: 85 us, 400 MB of it zeros),
+// short ones by the launches that wait for each other: three up to 8192 rows (3090 of 178
+// fp32 26 us), four to eight beyond (20510 of 10 fp16 49 us).
 #include "thd_loss_device.h"
 #include "thd_params_internal.h"
 
