@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int64_t kFewSums = 8192;
+constexpr int64_t kFewSums = 8192, kMostShort = 2048;
 constexpr int kEarlyRows = 4096;  // of the table, at most, that a workgroup beside the sort clears
 
 // 16 bytes at any element's alignment: the hardware takes them as they lie.
@@ -761,11 +761,12 @@ EmbedSort embed_sort(int64_t rows, int64_t vocab, int64_t width) {
   // 162, 131072 385, 361 and 345)
   s.unit = rows <= kSortBlock ? 16 : rows < 16384 ? 32 : rows < 65536 ? 64 : 128;
   // Short rows leave few threads, and lanes of a wave then hold different units, whose
-  // tokens end one by one: shorter units while there are fewer than kFewSums threads
-  // (sums and joining of 20510 rows of 10 fp16 44 -> 27 us, of 84222 of 94 72 -> 49, of
-  // 131072 of 20 bf16 88 -> 57; with twice as many threads the last takes 79).
+  // tokens end one by one: shorter units while there are fewer than kFewSums threads, but
+  // no more than kMostShort units, as a run's parts are added one after the other (sums and
+  // joining of 20510 rows of 10 fp16 44 -> 27 us, of 84222 of 94 72 -> 49, of 131072 of 20
+  // bf16 88 -> 59; 131072 rows of one token in units of 16 688).
   const int64_t words = (width + 7) / 8;
-  while (s.unit > 16 && rows / s.unit * words < kFewSums) s.unit /= 2;
+  while (s.unit > 16 && rows / s.unit * words < kFewSums && rows / s.unit * 2 <= kMostShort) s.unit /= 2;
   s.units = static_cast<int32_t>((rows + s.unit - 1) / s.unit);
   return s;
 }
