@@ -22,7 +22,7 @@
 //
 // Bound as the forward pass is; one document of 8192 tokens, causal, 32 heads of 128
 // over 8: dq 713 us (1157 TFLOP/s, matrix units busy 61 %, LDS 30 %), dk and dv 996 (1104,
-// 53 %, 40 %) and 70 to add up their parts; with a cap 888 and 1202; in fp16 781 and 1108,
+// 53 %, 40 %) and 70 to add up their parts; with a cap 888 and 1202; in fp16 798 and 1124,
 // and 46 for delta and the largest norms.
 //
 // fp16: p times 2^14 and dz times a power of two for which no dz passes the
@@ -34,8 +34,7 @@ namespace thdcp {
 
 namespace {
 
-// Of fp16 probabilities, which are 1 at most but for the roundings of their scores: the
-// type ends below 2^16.  Those from 2^-28 on keep all their bits.
+// Of fp16 probabilities, which are 1 at most.  Those from 2^-28 on keep all their bits.
 constexpr float kProbabilityScale = 16384.0f;
 
 // Power of two by which fp16 score gradients are held: |dz| <= 2 |dout| |v|.
@@ -146,7 +145,10 @@ __device__ __forceinline__ void score_gradients(const AttnArgs& a, F32x16 s, F32
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float z = s[r + e] * root, slope = kCap ? fmaf(-z, z, held) : held;
-      p[e] = visible(r + e) ? attn_exp2(fmaf(s[r + e], factor, -lse(r + e))) : 0.0f;
+      float x = fmaf(s[r + e], factor, -lse(r + e));
+      // 1 is p's most, which roundings of large scores pass, and fp16's range with it; NaN stays
+      if (T::kNarrow) x = __builtin_elementwise_minimum(x, 0.0f);
+      p[e] = visible(r + e) ? attn_exp2(x) : 0.0f;
       dz[e] = p[e] * (dp[r + e] - delta(r + e)) * slope;
       if (T::kNarrow) p[e] *= kProbabilityScale;
     }

@@ -40,6 +40,8 @@ template <typename T>
 constexpr float kLift = T::kNarrow ? 9.0f : 0.0f;
 template <typename T>
 constexpr float kGrowth = T::kNarrow ? 6.0f : 8.0f;
+// Larger maxima have no bits to stand kLift above anything.
+constexpr float kLiftUpTo = 0x1p22f;
 
 template <typename T, int kDim, bool kCap>
 struct ForwardWave {
@@ -91,8 +93,8 @@ struct ForwardWave {
 #pragma unroll
     for (int r = 2; r < 16; r += 2) m = fmaxf(fmaxf(m, s[r]), s[r + 1]);
     m = max_halves(m) * factor;
-    if (__any(m > top + (kLift<T> + kGrowth<T>))) {
-      const float to = fmaxf(top, m - kLift<T>);
+    if (__any(m - top > kLift<T> + kGrowth<T>)) {  // a difference: exact, however large they are
+      const float to = fmaxf(top, m - (fabsf(m) < kLiftUpTo ? kLift<T> : 0.0f));
       const float shrink = to == -kAttnInf ? 1.0f : attn_exp2(top - to);
       top = to;
       sum *= shrink;

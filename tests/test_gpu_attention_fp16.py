@@ -107,3 +107,23 @@ def test_not_finite_stays_in_its_document(torch, thd, dtype, cap, dim):
         for x, y in zip(got, grads):
             assert torch.equal(x[part], y[part])
     assert not out[70:134].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("spread", [300.0, 2000.0, 4000.0, 8000.0])
+@pytest.mark.parametrize("cap", [0.0, 1e7])
+def test_scores_past_their_precision(torch, thd, spread, dtype, cap):
+    # scores up to 3e8 are known to some whole numbers only; out still is a mean of values,
+    # and fp16's factors stay within the type, as no p passes 1
+    say("attention scores past their precision", spread, dtype, cap)
+    b = Batch(torch, [600], heads=4, kv_heads=4, dim=64, dtype=dtype, cap=cap)
+    for x in (b.q, b.k):
+        x.copy_((x.float() * spread).clamp(-6e4, 6e4))
+    out, lse, _ = b.forward(thd)
+    assert bool(lse.isfinite().all())
+    most = b.v.double().abs().amax(0)
+    assert bool((out.double().abs() <= most * (1 + 2 * HALF[dtype])).all())
+    *_, dv, _ = b.backward(thd, out, lse)
+    assert bool(dv.isfinite().all())
+    if dtype == "fp16":
+        assert bool((dv.double().abs() <= b.dout.double().abs().sum(0) * (1 + 4 * HALF[dtype])).all())
